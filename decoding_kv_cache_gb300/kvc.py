@@ -17,12 +17,15 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkvc.so")
 
 KVC_BF16, KVC_F32 = 0, 1
 KVC_STATUS_BUDGET_RANGE, KVC_STATUS_COUNT_RANGE, KVC_STATUS_BAD_INDEX, KVC_STATUS_TIMEOUT = 0x1, 0x2, 0x4, 0x8
+KVC_STATUS_NO_PAGES, KVC_STATUS_BAD_PAGE, KVC_STATUS_TABLE_FULL = 0x10, 0x20, 0x40
 KVC_MAX_LAYERS = 128
 
 EXPORTED = ("kvc_fps_update", "kvc_score_workspace_size", "kvc_score", "kvc_select", "kvc_compact",
             "kvc_evict_workspace_size", "kvc_evict", "kvc_evict_launch_count", "kvc_strerror", "kvc_abi_version",
             "kvc_score_static", "kvc_debug_fault", "kvc_head_budget", "kvc_append", "kvc_epikv_workspace_size",
-            "kvc_epikv_score", "kvc_epikv_evict")
+            "kvc_epikv_score", "kvc_epikv_evict", "kvc_page_bytes", "kvc_page_workspace_size", "kvc_page_init",
+            "kvc_page_extend", "kvc_page_store", "kvc_page_read", "kvc_page_fork", "kvc_page_free",
+            "kvc_page_compact", "kvc_page_attend_workspace_size", "kvc_page_attend")
 KVC_ABI_VERSION = 5
 KVC_AGG_MAX, KVC_AGG_MEAN, KVC_AGG_SUM = 0, 1, 2
 KVC_BUDGET_GIVEN, KVC_BUDGET_ENTROPY = 0, 1
@@ -51,6 +54,17 @@ class kvc_opts(C.Structure):
                 ("kernel", C.c_int32), ("entropy", C.c_void_p)]
 
 
+class kvc_pool(C.Structure):
+    _fields_ = [("D", C.c_int32), ("page", C.c_int32), ("npages", C.c_int32), ("pad_", C.c_int32),
+                ("k_scale", C.c_float), ("v_scale", C.c_float), ("data", C.c_void_p), ("refs", C.c_void_p),
+                ("free_list", C.c_void_p), ("nfree", C.c_void_p)]
+
+
+class kvc_pages(C.Structure):
+    _fields_ = [("L", C.c_int32), ("B", C.c_int32), ("Hkv", C.c_int32), ("maxp", C.c_int32), ("table", C.c_void_p),
+                ("len", C.c_void_p)]
+
+
 _lib = None
 
 
@@ -66,6 +80,7 @@ def lib():
     vp, i32, i64, dbl, sz = C.c_void_p, C.c_int32, C.c_int64, C.c_double, C.c_size_t
     pc = C.POINTER(kvc_cache)
     po = C.POINTER(kvc_opts)
+    pl, pg, ps = C.POINTER(kvc_pool), C.POINTER(kvc_pages), C.POINTER(i64)
     sig = {
         "kvc_fps_update": (C.c_int, [i32, i32, i32, i32, i32, vp, i32, vp, vp, vp, vp]),
         "kvc_append": (C.c_int, [i32, i32, i32, i32, i32, vp, vp, i64, dbl, vp, i32, vp, vp, i32, vp, vp, vp]),
@@ -82,6 +97,17 @@ def lib():
         "kvc_epikv_workspace_size": (sz, [i32, i32]),
         "kvc_epikv_score": (C.c_int, [i32, i32, i32, i32, vp, vp, i32, C.c_float, vp, vp, vp, sz, vp]),
         "kvc_epikv_evict": (C.c_int, [pc, vp, vp, i32, i32, C.c_float, i32, i32, vp, i32, vp, vp, vp, vp, vp, sz, vp]),
+        "kvc_page_bytes": (sz, [i32, i32]),
+        "kvc_page_workspace_size": (sz, [pl, pg]),
+        "kvc_page_init": (C.c_int, [pl, pg, vp]),
+        "kvc_page_extend": (C.c_int, [pl, pg, vp, i32, vp, vp, vp, sz, vp]),
+        "kvc_page_store": (C.c_int, [pl, pg, i32, i32, vp, ps, vp, ps, vp, vp, vp, vp]),
+        "kvc_page_read": (C.c_int, [pl, pg, i32, vp, i32, i32, vp, vp, i64, vp, vp]),
+        "kvc_page_fork": (C.c_int, [pl, pg, vp, pg, vp, vp, sz, vp]),
+        "kvc_page_free": (C.c_int, [pl, pg, vp, i32, vp, vp, sz, vp]),
+        "kvc_page_compact": (C.c_int, [pl, pg, vp, vp, i32, i32, vp, vp, sz, vp]),
+        "kvc_page_attend_workspace_size": (sz, [pl, pg, i32, i32]),
+        "kvc_page_attend": (C.c_int, [pl, pg, i32, i32, i32, vp, ps, vp, C.c_float, vp, vp, vp, vp, sz, vp]),
         "kvc_strerror": (C.c_char_p, [C.c_int]),
         "kvc_abi_version": (C.c_int, []),
         "kvc_debug_fault": (C.c_int, [i32]),
@@ -306,3 +332,220 @@ def kvc_epikv_evict(cache: Cache, hA: torch.Tensor, hB: torch.Tensor, window: in
     _check(lib().kvc_epikv_evict(cache.ref, _p(hA), _p(hB), dm, int(window), float(eps), int(prefix), int(recent),
                                  _p(budget), int(budget_all), _p(kept_idx), _p(kept_len), _p(scores), _p(status),
                                  _p(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------------------------
+# the paged 4-bit cache
+# ---------------------------------------------------------------------------------------------
+def kvc_page_bytes(D: int, page: int) -> int:
+    return int(lib().kvc_page_bytes(D, page))
+
+
+def _ints(t: Optional[torch.Tensor], shape, dev, what: str, dtype=torch.int32):
+    """The pointer of a contiguous tensor of the given shape and type on the pool's device, or None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.device != dev or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}")
+    return t.data_ptr()
+
+
+class Pool:
+    """A ``kvc_pool`` over torch tensors: ``data`` uint8 [npages, kvc_page_bytes(D, page)], ``refs`` and
+    ``free_list`` int32 [npages], ``nfree`` int32 [1]. ``Pool.empty`` allocates and initialises them."""
+
+    def __init__(self, data: torch.Tensor, refs: torch.Tensor, free_list: torch.Tensor, nfree: torch.Tensor, D: int,
+                 page: int, k_scale: float = 1.0, v_scale: float = 1.0):
+        nb = kvc_page_bytes(D, page)
+        if not nb:
+            raise KvcError(-3 if D not in (64, 128) else -1, "unsupported head dimension or page size")
+        if not data.is_cuda:
+            raise ValueError("libkvc takes CUDA tensors")
+        n = data.shape[0]
+        dev = data.device
+        self.data, self.refs, self.free_list, self.nfree = data, refs, free_list, nfree
+        self.device, self.D, self.page, self.npages = dev, D, page, n
+        self.k_scale, self.v_scale = float(k_scale), float(v_scale)
+        self.c = kvc_pool(D=D, page=page, npages=n, pad_=0, k_scale=k_scale, v_scale=v_scale,
+                          data=_ints(data, (n, nb), dev, "data", torch.uint8),
+                          refs=_ints(refs, (n,), dev, "refs"), free_list=_ints(free_list, (n,), dev, "free_list"),
+                          nfree=_ints(nfree, (1,), dev, "nfree"))
+        self.ref = C.byref(self.c)
+
+    @classmethod
+    def empty(cls, npages: int, D: int, page: int = 64, k_scale: float = 1.0, v_scale: float = 1.0, device="cuda"):
+        """A pool of ``npages`` free pages."""
+        z = lambda shape, dt=torch.int32: torch.zeros(shape, dtype=dt, device=device)
+        p = cls(z((npages, kvc_page_bytes(D, page)), torch.uint8), z(npages), z(npages), z(1), D, page, k_scale, v_scale)
+        kvc_page_init(p)
+        return p
+
+
+class Pages:
+    """A ``kvc_pages`` over torch tensors: ``table`` int32 [L, B, Hkv, maxp], ``len`` int32 [L, B, Hkv]."""
+
+    def __init__(self, table: torch.Tensor, len: torch.Tensor):
+        L, B, Hkv, maxp = table.shape
+        dev = table.device
+        self.table, self.len, self.device = table, len, dev
+        self.c = kvc_pages(L=L, B=B, Hkv=Hkv, maxp=maxp, table=_ints(table, (L, B, Hkv, maxp), dev, "table"),
+                           len=_ints(len, (L, B, Hkv), dev, "len"))
+        self.ref = C.byref(self.c)
+
+    @classmethod
+    def empty(cls, L: int, B: int, Hkv: int, maxp: int, device="cuda"):
+        return cls(torch.full((L, B, Hkv, maxp), -1, dtype=torch.int32, device=device),
+                   torch.zeros((L, B, Hkv), dtype=torch.int32, device=device))
+
+    def layer(self, l: int) -> "Pages":
+        return Pages(self.table[l:l + 1], self.len[l:l + 1])
+
+    @property
+    def shape(self):
+        return self.c.L, self.c.B, self.c.Hkv
+
+
+def _page_call(name: str, pool: Pool, pages: Optional[Pages], stream, args):
+    """One entry point on the pool's device: ``args`` follow the pool and the pages, the stream comes last."""
+    if pages is not None and pages.device != pool.device:
+        raise ValueError("the pool and its pages are on different devices")
+    f = getattr(_lib or lib(), name)
+    cur = torch.cuda.current_device()
+    if pool.device.index == cur:
+        if stream is None:
+            stream = torch.cuda.current_stream(pool.device)
+        rc = f(pool.ref, None if pages is None else pages.ref, *args, _stream(stream))
+    else:
+        with torch.cuda.device(pool.device):
+            rc = f(pool.ref, None if pages is None else pages.ref, *args, _stream(stream))
+    _check(rc)
+
+
+def _page_ws(nbytes: int, pool: Pool, workspace):
+    """(pointer, bytes, tensor) of the caller's workspace, or of one made for this call."""
+    if workspace is None:
+        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=pool.device)
+    elif workspace.device != pool.device or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on the pool's device")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _word(status, pool: Pool):
+    return None if status is None else _ints(status, (1,), pool.device, "status")
+
+
+def kvc_page_workspace_size(pool: Pool, pages: Pages) -> int:
+    return int(lib().kvc_page_workspace_size(pool.ref, pages.ref))
+
+
+def kvc_page_attend_workspace_size(pool: Pool, pages: Pages, Hq: int, T: int) -> int:
+    return int(lib().kvc_page_attend_workspace_size(pool.ref, pages.ref, Hq, T))
+
+
+def kvc_page_init(pool: Pool, pages: Optional[Pages] = None, stream=None):
+    """Every page free and, with ``pages``, every stream empty."""
+    _page_call("kvc_page_init", pool, pages, stream, ())
+
+
+def kvc_page_extend(pool: Pool, pages: Pages, add: Optional[torch.Tensor] = None, add_all: int = 0,
+                    start: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, stream=None):
+    """Room for ``add`` [B] (or ``add_all``) more tokens in every stream; ``start`` [L, B, Hkv] receives the
+    old lengths (see kvc.h)."""
+    dev = pool.device
+    wp, wb, ws = _page_ws(0 if workspace is not None else kvc_page_workspace_size(pool, pages), pool, workspace)
+    _page_call("kvc_page_extend", pool, pages, stream,
+               (_ints(add, (pages.c.B,), dev, "add"), int(add_all), _ints(start, pages.shape, dev, "start"),
+                _word(status, pool), wp, wb))
+
+
+def kvc_page_free(pool: Pool, pages: Pages, drop: Optional[torch.Tensor] = None, drop_all: int = 0,
+                  status: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """The last ``drop`` [B] (or ``drop_all``) tokens of every stream go, with the pages they leave empty."""
+    wp, wb, ws = _page_ws(0 if workspace is not None else kvc_page_workspace_size(pool, pages), pool, workspace)
+    _page_call("kvc_page_free", pool, pages, stream,
+               (_ints(drop, (pages.c.B,), pool.device, "drop"), int(drop_all), _word(status, pool), wp, wb))
+
+
+def kvc_page_fork(pool: Pool, pages: Pages, parent: torch.Tensor, out: Pages, status: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None, stream=None):
+    """``out``'s sequence c becomes a copy of ``pages``' sequence ``parent[c]``; ``pages`` is given up."""
+    if out.device != pool.device:
+        raise ValueError("the pool and its pages are on different devices")
+    wp, wb, ws = _page_ws(0 if workspace is not None else kvc_page_workspace_size(pool, pages), pool, workspace)
+    _page_call("kvc_page_fork", pool, pages, stream,
+               (_ints(parent, (out.c.B,), pool.device, "parent"), out.ref, _word(status, pool), wp, wb))
+
+
+def kvc_page_compact(pool: Pool, pages: Pages, kept_idx: torch.Tensor, kept_len: torch.Tensor,
+                     status: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """The kept tokens to every stream's front: lists per stream ([L, B, Hkv, n] and [L, B, Hkv], as
+    kvc_select's) or per sequence ([B, n] and [B], as kvc_epikv_evict's)."""
+    per_seq = kept_idx.dim() == 2
+    lead = (pages.c.B,) if per_seq else pages.shape
+    wp, wb, ws = _page_ws(0 if workspace is not None else kvc_page_workspace_size(pool, pages), pool, workspace)
+    _page_call("kvc_page_compact", pool, pages, stream,
+               (_ints(kept_idx, lead + (kept_idx.shape[-1],), pool.device, "kept_idx"),
+                _ints(kept_len, lead, pool.device, "kept_len"), kept_idx.shape[-1], int(per_seq), _word(status, pool),
+                wp, wb))
+
+
+def _rows(x: torch.Tensor, shape, pool: Pool, what: str):
+    """The pointer and strides of [B, T, heads, D] rows with contiguous channels."""
+    if x.device != pool.device or tuple(x.shape) != tuple(shape) or x.stride(3) != 1:
+        raise ValueError(f"{what} must be a {tuple(shape)} tensor on {pool.device} with contiguous channels")
+    s = x.stride()
+    return x.data_ptr(), (C.c_int64 * 3)(s[0], s[1], s[2])
+
+
+def kvc_page_store(pool: Pool, pages: Pages, k: torch.Tensor, v: torch.Tensor, start: torch.Tensor,
+                   n: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None):
+    """One layer's new rows ``k``, ``v`` [B, T, Hkv, D] (any batch, token and head strides that are multiples of
+    16 bytes) into tokens ``start`` [1, B, Hkv] and on; ``n`` [B] rows of them (default all T)."""
+    _, B, Hkv = pages.shape
+    if k.dim() != 4 or v.dtype != k.dtype:
+        raise ValueError("k and v must be [B, T, Hkv, D] tensors of one dtype")
+    shape = (B, k.shape[1], Hkv, pool.D)
+    kp, ks = _rows(k, shape, pool, "k")
+    vp, vs = _rows(v, shape, pool, "v")
+    _page_call("kvc_page_store", pool, pages, stream,
+               (_dtype_code(k), shape[1], kp, ks, vp, vs, _ints(n, (B,), pool.device, "n"),
+                _ints(start, pages.shape, pool.device, "start"), _word(status, pool)))
+
+
+def kvc_page_read(pool: Pool, pages: Pages, k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None,
+                  first: Optional[torch.Tensor] = None, first_all: int = 0, count: Optional[int] = None,
+                  status: Optional[torch.Tensor] = None, stream=None):
+    """Tokens ``first`` [L, B, Hkv] (or ``first_all``) and on of every stream into rows 0..count-1 (default
+    all) of dense ``k``, ``v`` [L, B, Hkv, ncap, D]; rows past a stream's length are left as they were."""
+    x = k if k is not None else v
+    if x is None:
+        raise ValueError("kvc_page_read needs k or v")
+    if x.dim() != 5 or tuple(x.shape[:3]) != pages.shape or x.shape[4] != pool.D:
+        raise ValueError("k and v must be [L, B, Hkv, ncap, D] tensors")
+    for t in (k, v):
+        if t is not None and (t.shape != x.shape or t.dtype != x.dtype or t.device != pool.device or not t.is_contiguous()):
+            raise ValueError("k and v must be contiguous [L, B, Hkv, ncap, D] tensors of one dtype on the pool's device")
+    ncap = x.shape[3]
+    _page_call("kvc_page_read", pool, pages, stream,
+               (_dtype_code(x), _ints(first, pages.shape, pool.device, "first"), int(first_all),
+                ncap if count is None else int(count), None if k is None else k.data_ptr(),
+                None if v is None else v.data_ptr(), ncap, _word(status, pool)))
+
+
+def kvc_page_attend(pool: Pool, pages: Pages, q: torch.Tensor, out: torch.Tensor, lse: Optional[torch.Tensor] = None,
+                    n_q: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                    status: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Attention of ``q`` [B, T, Hq, D] (strided like kvc_page_store's rows), the newest T tokens' queries, over
+    one layer of the cache; ``out`` [B, T, Hq, D], ``lse`` [B, T, Hq] fp32; ``scale`` defaults to 1/sqrt(D)."""
+    B = pages.c.B
+    if q.dim() != 4:
+        raise ValueError("q must be a [B, T, Hq, D] tensor")
+    _, T, Hq, D = q.shape
+    qp, qs = _rows(q, (B, T, Hq, pool.D), pool, "q")
+    wp, wb, ws = _page_ws(0 if workspace is not None else kvc_page_attend_workspace_size(pool, pages, Hq, T), pool,
+                          workspace)
+    _page_call("kvc_page_attend", pool, pages, stream,
+               (_dtype_code(q), Hq, T, qp, qs, _ints(n_q, (B,), pool.device, "n_q"),
+                float(D ** -0.5 if scale is None else scale), _ints(out, q.shape, pool.device, "out", q.dtype),
+                _ints(lse, (B, T, Hq), pool.device, "lse", torch.float32), _word(status, pool), wp, wb))

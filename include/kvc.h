@@ -73,6 +73,9 @@ enum {
 #define KVC_STATUS_COUNT_RANGE 0x2u  /* a query-buffer count < 0 or > qmax: head left alone */
 #define KVC_STATUS_BAD_INDEX 0x4u    /* kvc_compact: kept list not strictly increasing in [k, N) */
 #define KVC_STATUS_TIMEOUT 0x8u      /* a bounded device-side wait gave up; that work was skipped */
+#define KVC_STATUS_NO_PAGES 0x10u    /* the pool has too few free pages: the call changed nothing */
+#define KVC_STATUS_BAD_PAGE 0x20u    /* a page number, count or length out of range, or a shared page written */
+#define KVC_STATUS_TABLE_FULL 0x40u  /* a stream would need more than maxp pages: left alone */
 
 /*
  * Scoring and budget options (kvc_score, kvc_score_static, kvc_evict). A NULL
@@ -398,6 +401,163 @@ KVC_API int kvc_epikv_evict(const kvc_cache* c, const void* hA, const void* hB, 
                             int32_t prefix, int32_t recent, const int32_t* budget, int32_t budget_all,
                             int32_t* kept_idx, int32_t* kept_len, float* scores, int32_t* status, void* workspace,
                             size_t ws_bytes, void* stream);
+
+/*
+ * The paged 4-bit cache (kvc_page_*)
+ * ----------------------------------
+ * Eviction frees the tail of every head, and with per-head budgets (ReasonAlloc note, "Core
+ * Mechanism": a budget B_{L_i,H_j} per head) every head its own amount; held in pages, what one
+ * head gives up another can take. None of the pages describes paging or quantised storage: the
+ * format and these operators are this library's own.
+ *
+ * A pool is npages pages of `page` tokens of one KV head of one layer, 4.5 bits a value. A page is
+ * a run of 16-token blocks of 18 D bytes:
+ *   K codes [16][D/2], K scales [16][D/16], V codes [16][D/2], V scales [16][D/16]
+ * Two e2m1 codes a byte, the even channel in the low nibble (bit 3 the sign, values 0, .5, 1, 1.5,
+ * 2, 3, 4, 6); an e4m3 scale per 16 channels; a code stands for ts * scale * e2m1(code), with the
+ * pool's fp32 tensor scale ts (k_scale or v_scale).
+ *
+ * A kvc_pages describes L layers' streams: for each (l, b, h) a row of maxp page numbers and a
+ * length in tokens. Entry i of a row holds tokens [i*page, (i+1)*page); entries past the length are
+ * not read, and are -1 where these operators leave them. Several kvc_pages may use one pool; one
+ * layer of a kvc_pages is the kvc_pages with L = 1 and the pointers moved to that layer.
+ *
+ * Pages are counted (refs: how many streams hold a page) and only sequences of the same layer and
+ * head share one, as kvc_page_fork makes them. free_list holds the free pages, *nfree of them; pages
+ * are taken from its end, streams in (l, b, h) order, and join it in the order of their numbers, so
+ * results never depend on timing. The arrays start from kvc_page_init and only these operators
+ * change them; streams of one pool are changed by one call at a time (order the calls on a stream).
+ * A page number out of range is reported (KVC_STATUS_BAD_PAGE), never followed.
+ */
+typedef struct {
+  int32_t D;          /* head dimension, 64 or 128 */
+  int32_t page;       /* tokens per page: 16, 32, 64, 128 or 256 */
+  int32_t npages;     /* 1 .. 2^28 */
+  int32_t pad_;       /* must be 0 */
+  float k_scale;      /* tensor scales, 1e-20 .. 1e20 (1: codes and scales stand for the values) */
+  float v_scale;
+  void* data;         /* npages * kvc_page_bytes(D, page) bytes (device, 16-byte aligned) */
+  int32_t* refs;      /* [npages] (device) */
+  int32_t* free_list; /* [npages] (device) */
+  int32_t* nfree;     /* [1] (device) */
+} kvc_pool;
+
+typedef struct {
+  int32_t L, B, Hkv; /* L * B * Hkv <= 2^20 streams */
+  int32_t maxp;      /* pages a stream can hold; maxp * page <= 2^30 */
+  int32_t* table;    /* [L,B,Hkv,maxp] page numbers (device) */
+  int32_t* len;      /* [L,B,Hkv] tokens (device) */
+} kvc_pages;
+
+/* Bytes of a page; 0 for an unsupported D or page. */
+KVC_API size_t kvc_page_bytes(int32_t D, int32_t page);
+
+/* Device scratch of kvc_page_extend, _free, _fork and _compact (256-byte aligned; contents on entry do
+ * not matter; two calls that may overlap need two). 0 for bad arguments. */
+KVC_API size_t kvc_page_workspace_size(const kvc_pool* pool, const kvc_pages* pages);
+
+/* kvc_page_init -- every page free (taken in the order 0, 1, ...), and, with pages non-NULL, every
+ * stream empty. */
+KVC_API int kvc_page_init(const kvc_pool* pool, const kvc_pages* pages, void* stream);
+
+/*
+ * kvc_page_extend -- room for new tokens: every stream of sequence b grows by add[b] tokens (add_all
+ * when add is NULL), whose rows kvc_page_store then writes.
+ *
+ * A stream takes the pages it lacks; a partly filled last page that other streams share is copied
+ * first (when all its sharers grow in this call, the lowest sequence keeps it). The copied page comes
+ * before the fresh ones. start[l,b,h] (device, out, may be NULL) receives the old length, -1 for a
+ * stream that was left alone because of an error: add[b] < 0 (KVC_STATUS_BAD_INDEX), more than maxp
+ * pages (KVC_STATUS_TABLE_FULL), a bad length or last page (KVC_STATUS_BAD_PAGE). With too few free
+ * pages for the whole call nothing changes and every start is -1 (KVC_STATUS_NO_PAGES).
+ */
+KVC_API int kvc_page_extend(const kvc_pool* pool, const kvc_pages* pages, const int32_t* add, int32_t add_all,
+                            int32_t* start, int32_t* status, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * kvc_page_store -- new K and V rows into their pages, quantised. One layer (pages->L == 1): row t of
+ * stream (b, h) becomes token start[b,h] + t, for t < n[b] (all T when n is NULL); streams with
+ * start < 0 are skipped. Per group of 16 channels x:
+ *   scale = e4m3(clamp(max|x| / (6 ts), 2^-9, 448)); code = e2m1 nearest to x / (scale ts), ties to
+ *   the even code, larger quotients saturate; both roundings are those of the exact quotient when ts
+ *   is a power of two. A NaN is stored as 0, an infinity as 6 * 448 ts with its sign.
+ * A row past the stream's length (KVC_STATUS_BAD_INDEX) or in a page that is missing or shared
+ * (KVC_STATUS_BAD_PAGE) is skipped.
+ *
+ *   dtype      kvc_dtype of k and v
+ *   k, v       [B][T][Hkv][D] rows (device, 16-byte aligned), channels contiguous; *_strides: host
+ *              array of the batch, token and head strides in elements (multiples of 16 bytes)
+ *   n          [B] (device) or NULL;  start [B,Hkv] (device), as kvc_page_extend wrote it for this layer
+ */
+KVC_API int kvc_page_store(const kvc_pool* pool, const kvc_pages* pages, int32_t dtype, int32_t T, const void* k,
+                           const int64_t* k_strides, const void* v, const int64_t* v_strides, const int32_t* n,
+                           const int32_t* start, int32_t* status, void* stream);
+
+/*
+ * kvc_page_read -- rows read back dense: token first[l,b,h] + i (first_all + i when first is NULL) of
+ * every stream to row i < count of a kvc_cache layout [L,B,Hkv,ncap,D] (k, v: device, either may be
+ * NULL); rows at or past a stream's length are left as they were. So that kvc_score can rank the keys
+ * of a paged cache, whose kept lists kvc_page_compact then takes.
+ */
+KVC_API int kvc_page_read(const kvc_pool* pool, const kvc_pages* pages, int32_t dtype, const int32_t* first,
+                          int32_t first_all, int32_t count, void* k, void* v, int64_t ncap, int32_t* status,
+                          void* stream);
+
+/*
+ * kvc_page_fork -- sequences replaced by copies: out's sequence c becomes a copy of pages' sequence
+ * parent[c], without moving any row (pages are shared, and copied when written: kvc_page_extend).
+ * Sequences of `pages` that no child names give up their pages; `pages` itself is not valid
+ * afterwards (out takes its place). out->B may differ; L, Hkv and maxp are the same, and out's arrays
+ * do not overlap those of pages. parent[c] = -1 makes an empty sequence, another value out of [0, B)
+ * too (KVC_STATUS_BAD_INDEX).
+ */
+KVC_API int kvc_page_fork(const kvc_pool* pool, const kvc_pages* pages, const int32_t* parent, const kvc_pages* out,
+                          int32_t* status, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * kvc_page_free -- the last drop[b] tokens of every stream of sequence b go (drop_all when drop is NULL;
+ * all its tokens where it has fewer): a finished sequence, or drafts that were not accepted. Pages
+ * left without a token are given up. drop[b] < 0 leaves the sequence alone (KVC_STATUS_BAD_INDEX).
+ */
+KVC_API int kvc_page_free(const kvc_pool* pool, const kvc_pages* pages, const int32_t* drop, int32_t drop_all,
+                          int32_t* status, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * kvc_page_compact -- kvc_compact on pages: every stream's kept tokens move to its front in order, its
+ * length becomes kept_len, and the pages behind are given up. Codes and scales move unchanged. Pages
+ * that other streams share are not written: where rows move into one, the stream takes a fresh page
+ * instead (KVC_STATUS_NO_PAGES when there are too few for the whole call: nothing changes). Rows past
+ * kept_len keep their bytes. A malformed list (as kvc_compact; here also longer than the stream) sets
+ * KVC_STATUS_BAD_INDEX, a bad page or length KVC_STATUS_BAD_PAGE: that stream is left alone.
+ *
+ *   kept_idx, kept_len  one list per stream, [L,B,Hkv,kept_stride] and [L,B,Hkv] (kvc_select), or
+ *                       with list_per_seq = 1 one per sequence, [B,kept_stride] and [B] (kvc_epikv_evict)
+ */
+KVC_API int kvc_page_compact(const kvc_pool* pool, const kvc_pages* pages, const int32_t* kept_idx,
+                             const int32_t* kept_len, int32_t kept_stride, int32_t list_per_seq, int32_t* status,
+                             void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * kvc_page_attend -- attention of T new queries per sequence over one layer of the cache (pages->L ==
+ * 1), whose newest n_q[b] tokens (all T when n_q is NULL; clamped to [0, T]) are the queries' own: query
+ * i < n_q sees tokens j <= len - n_q + i of its KV head's stream, in storage order (after an eviction the
+ * kept tokens, each head its own).
+ *   out[b,i,hq] = sum_j softmax_j(scale q.k_j) v_j,  lse[b,i,hq] = log sum_j exp(scale q.k_j)
+ * in fp32 (dot products of fp16 factors: codes times scales are exact in fp16, queries and
+ * probabilities are fp16, in two terms each when dtype is KVC_F32). A query that sees no token gets
+ * out = 0 and lse = -inf; queries i >= n_q[b] are not written. Tokens of a bad page take no part, and a
+ * stream of bad length counts as empty (KVC_STATUS_BAD_PAGE).
+ *
+ *   dtype      kvc_dtype of q and out
+ *   q          [B][T][Hq][D] rows (device, 16-byte aligned), strides as kvc_page_store's
+ *   scale      finite; 1/sqrt(D) is usual
+ *   out, lse   [B,T,Hq,D] and [B,T,Hq] fp32 (device); lse may be NULL
+ *   workspace  at least kvc_page_attend_workspace_size() bytes, 256-byte aligned
+ */
+KVC_API size_t kvc_page_attend_workspace_size(const kvc_pool* pool, const kvc_pages* pages, int32_t Hq, int32_t T);
+KVC_API int kvc_page_attend(const kvc_pool* pool, const kvc_pages* pages, int32_t dtype, int32_t Hq, int32_t T,
+                            const void* q, const int64_t* q_strides, const int32_t* n_q, float scale, void* out,
+                            float* lse, int32_t* status, void* workspace, size_t ws_bytes, void* stream);
 
 /* Number of kernels one kvc_evict call with these arguments and default options
  * launches (host only; for accounting, e.g. counting launches inside a timed region;
