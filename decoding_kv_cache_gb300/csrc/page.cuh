@@ -132,7 +132,7 @@ struct AttendArgs {
   int32_t* status;
   void* ws;
 };
-size_t attend_ws_bytes(int D, int B, int Hkv, int Hq, int T);
+size_t attend_ws_bytes(const PoolGeom& g, const PageTab& t, int Hq, int T);
 int launch_page_attend(const AttendArgs& a, int dtype, cudaStream_t s);
 
 }  // namespace kvc

@@ -217,7 +217,7 @@ size_t kvc_page_attend_workspace_size(const kvc_pool* pool, const kvc_pages* pag
   PoolGeom g;
   PageTab t;
   if (check_pool(pool, &g) || check_pages(pages, g.lp, &t) || Hq < 1 || Hq % t.Hkv || T < 1) return 0;
-  return attend_ws_bytes(g.D, t.B, t.Hkv, Hq, T);
+  return attend_ws_bytes(g, t, Hq, T);
 }
 
 int kvc_page_attend(const kvc_pool* pool, const kvc_pages* pages, int32_t dtype, int32_t Hq, int32_t T, const void* q,
@@ -233,7 +233,7 @@ int kvc_page_attend(const kvc_pool* pool, const kvc_pages* pages, int32_t dtype,
   if ((long long)a.t.B * Hq > (1LL << 30) || (long long)a.t.B * Hq * T > (1LL << 30)) return KVC_ERR_TOO_LARGE;
   if ((rc = check_rows(q, q_strides, es, &a.qs))) return rc;
   if (!at16(out) || !at4(lse)) return KVC_ERR_ALIGNMENT;
-  if (!workspace || ws_bytes < attend_ws_bytes(a.g.D, a.t.B, a.t.Hkv, Hq, T) ||
+  if (!workspace || ws_bytes < attend_ws_bytes(a.g, a.t, Hq, T) ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return KVC_ERR_WORKSPACE;
   a.q = q;

@@ -3,90 +3,725 @@
 // T new queries of each sequence (already stored in the cache) over its streams' tokens: query i of n_q
 // sees the first len - n_q + i + 1 tokens of its KV head;
 //   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q.k_j),  lse = log sum_j p_j,
-// and a query that sees no token gets out = 0 and lse = -inf. Running maximum and sum in fp32.
+// and a query that sees no token gets out = 0 and lse = -inf. One pass over the cache with a running
+// maximum and sum in fp32.
+//
+// A KV head's R = T * Hq/Hkv query rows are taken 8 * NT at a time (a row block). The tokens lie on the
+// m axis of mma.sync m16n8k16 and the rows on its n axis (S^T = K Q^T, then O^T = V^T P^T), so eight rows
+// fill a tile and the 4-bit operand is decoded straight into A fragments in registers: a lane reads its
+// tokens' codes with one vector load, two codes become an fp16 pair by one conversion and one multiply by
+// their scale (exact: at most six significant bits), and P^T's fragment is S^T's transposed by movmatrix.
+// Why mma.sync: with at most 8 * NT rows the contraction needs a few percent of the tensor peak; what has
+// to keep up with memory is the decoding, and tcgen05 would need the decoded tile written to shared or
+// tensor memory first. (Probed on this chip: conversion and multiply of 32 code pairs take 14 ns of an SM's
+// issue; masks and shifts to 4-bit integers with an fma 27 ns.)
+//
+// Work is split by tokens over all CTAs of one wave, whatever the streams' lengths: the 64-token units of
+// all streams form one list, CTA i takes units [W i/grid, W (i+1)/grid). A stream cut by a CTA border leaves
+// partial (max, sum, O) rows in the workspace; the combine kernel merges them (and writes the rows of empty
+// streams). In a CTA each of the four warps takes every fourth 32-token chunk with its own two-stage
+// ring of bulk copies; nothing but the end of a stream's part synchronises them.
 #include "page.cuh"
+#include "tc_ptx.cuh"
 
 namespace kvc {
 namespace {
 
-// One warp per query row; each lane owns D/32 channels.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) attend_simple_kernel(AttendArgs a) {
+constexpr int kWarps = 4;
+constexpr int kUnit = 64;    // tokens of a work unit
+constexpr int kChunk32 = 32;  // tokens of a ring stage
+constexpr int kStages = 2;
+constexpr int kMaxGridSMs = 160;
+constexpr float kOff = 10.f;  // probabilities are held times 2^10 (fp16's range is used below the maximum too)
+constexpr float kRaise = 5.f; // a reference may lag the maximum by 2^5: 2^15 at most, inside fp16
+
+struct Plan {
+  int nrb;     // row blocks per stream
+  int rb;      // rows per block
+  int G;
+  int nvs;     // streams * nrb
+  int grid;    // CTAs of the main kernel
+  float* part;  // [grid][2][rb][D]
+  float2* ml;   // [grid][2][rb] (reference, sum)
+};
+
+struct Stream {  // what a (stream, row block) has to see
+  int s, b, h, len, nq, r0, rows, vis;
+};
+
+__device__ __forceinline__ Stream stream_of(const AttendArgs& a, const Plan& p, int vs, bool report) {
+  Stream x;
+  x.s = vs / p.nrb;
+  x.r0 = (vs % p.nrb) * p.rb;
+  x.b = x.s / a.t.Hkv;
+  x.h = x.s % a.t.Hkv;
+  x.len = a.t.len[x.s];
+  x.nq = a.n_q ? min(max(a.n_q[x.b], 0), a.T) : a.T;
+  if (x.len < 0 || x.len > ((long long)a.t.maxp << a.g.lp)) {
+    if (report) status_or(a.status, KVC_STATUS_BAD_PAGE);
+    x.len = 0;
+  }
+  x.rows = max(0, min(p.rb, x.nq * p.G - x.r0));
+  const int tmax = min((x.r0 + p.rb - 1) / p.G, x.nq - 1);
+  x.vis = x.rows ? max(0, x.len - x.nq + tmax + 1) : 0;
+  return x;
+}
+__device__ __forceinline__ int units_of(const Stream& x) { return (x.vis + kUnit - 1) / kUnit; }
+
+// Units before each thread's run of streams and in all (block of kThr threads; every thread calls).
+template <int kThr>
+__device__ __forceinline__ int scan_units(const AttendArgs& a, const Plan& p, int* sm, int per, int* total) {
+  int mine = 0;
+  for (int i = 0; i < per; ++i) {
+    const int vs = threadIdx.x * per + i;
+    if (vs < p.nvs) mine += units_of(stream_of(a, p, vs, false));
+  }
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kFull, incl, o);
+    if ((threadIdx.x & 31) >= o) incl += v;
+  }
+  if ((threadIdx.x & 31) == 31) sm[threadIdx.x >> 5] = incl;
+  __syncthreads();
+  int base = 0, all = 0;
+#pragma unroll
+  for (int i = 0; i < kThr / 32; ++i) {
+    const int v = sm[i];
+    if (i < (int)(threadIdx.x >> 5)) base += v;
+    all += v;
+  }
+  *total = all;
+  return base + incl - mine;
+}
+
+__device__ __forceinline__ int cta_first(int W, int i, int grid) { return (int)((long long)W * i / grid); }
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+                   tc::smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
+               : "memory");
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t x, uint32_t y) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __half2 r = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <int D, int NT>
+struct Smem {
+  static constexpr int kStage = 2 * blk_bytes(D);  // 32 tokens
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kMerge = kRows * D * 4 + kRows * 8;  // one warp's O^T, references and sums
+  static constexpr int bytes = kWarps * kStages * kStage + 2 * kMerge;
+};
+
+// Rows per thread in the accumulators: of tile nt, rows 2t and 2t+1 (t = lane % 4); channels
+// CPV*g + 2 mt (+1), g = lane / 4.
+template <typename T, int D, int NT, int PARTS, int MINB>
+__global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a, Plan p) {
+  using SM = Smem<D, NT>;
+  constexpr int KS = D / 16;   // k steps of Q K^T and m tiles of V^T
+  constexpr int CPL = D / 4;   // channels of a lane in K
+  constexpr int CPV = D / 8;   // channels of a lane in V
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t bars[kWarps][kStages];
+  __shared__ uint32_t oks[kWarps][kStages];
+  __shared__ int sm_scan[kWarps], sm_first[2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  uint8_t* ring = smem + warp * kStages * SM::kStage;
+  float* merge = reinterpret_cast<float*>(smem + kWarps * kStages * SM::kStage);
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) tc::mbar_init(&bars[warp][i], 1);
+    tc::mbar_fence_init();
+  }
   griddep_wait();
-  constexpr int E = D / 32;
-  const int row = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int G = a.Hq / a.t.Hkv;
-  if (row >= a.t.B * a.T * a.Hq) return;
-  const int hq = row % a.Hq, t = row / a.Hq % a.T, b = row / (a.Hq * a.T);
-  const int nq = a.n_q ? min(max(a.n_q[b], 0), a.T) : a.T;
-  if (t >= nq) return;
-  const int s = b * a.t.Hkv + hq / G;
-  const int len = a.t.len[s];
-  int seen = len - nq + t + 1;
-  if (len < 0 || len > ((long long)a.t.maxp << a.g.lp)) {
-    if (lane == 0) status_or(a.status, KVC_STATUS_BAD_PAGE);
-    seen = 0;
-  }
-  const T* qp = static_cast<const T*>(a.q) + b * a.qs.b + t * a.qs.t + hq * a.qs.h + lane * E;
-  float q[E], o[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = to_f32(qp[e]) * a.scale;
-    o[e] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  for (int j = 0; j < seen; ++j) {
-    const int p = a.t.table[(size_t)s * a.t.maxp + (j >> a.g.lp)];
-    if (!page_ok(a.g, p)) {
-      if (lane == 0) status_or(a.status, KVC_STATUS_BAD_PAGE);
-      continue;
+
+  // this CTA's units, and the stream its first one lies in
+  const int per = (p.nvs + 32 * kWarps - 1) / (32 * kWarps);
+  int W;
+  int before = scan_units<32 * kWarps>(a, p, sm_scan, per, &W);
+  const int w0 = cta_first(W, blockIdx.x, p.grid), w1 = cta_first(W, blockIdx.x + 1, p.grid);
+  if (w0 >= w1) return;
+  for (int i = 0; i < per; ++i) {
+    const int vs = threadIdx.x * per + i;
+    if (vs >= p.nvs) break;
+    const int u = units_of(stream_of(a, p, vs, false));
+    if (before <= w0 && w0 < before + u) {
+      sm_first[0] = vs;
+      sm_first[1] = before;
     }
-    const int in = j & ((1 << a.g.lp) - 1);
-    const uint8_t* blk = block_of(a.g, p, in >> 4);
-    float kv[2][E];
+    before += u;
+  }
+  __syncthreads();
+  int vs = sm_first[0];
+  int ua = w0 - sm_first[1];  // first unit of this CTA in the stream
+  int left = w1 - w0;
+  uint32_t n = 0;  // chunks this warp has waited for
+  bool alive = true;
+
+  for (; left > 0; ++vs, ua = 0) {
+    const Stream x = stream_of(a, p, vs, true);
+    const int U = units_of(x);
+    if (U == 0) continue;
+    const int ub = min(U, ua + left);
+    left -= ub - ua;
+    const int c1 = min(2 * ub, (x.vis + kChunk32 - 1) / kChunk32);  // chunks [2 ua, c1) of the stream
+    const int c0 = 2 * ua + warp;
+    const int mine = c1 > c0 ? (c1 - c0 + kWarps - 1) / kWarps : 0;
+    const int32_t* row = a.t.table + (size_t)x.s * a.t.maxp;
+    const int last = pages_of(x.len, a.g.lp) - 1;
+
+    // page numbers of this warp's next 32 chunks, one a lane (two where a page is half a chunk)
+    int ids[2];
+    auto load_ids = [&](int i) {
+      const int tok = (c0 + kWarps * (i + lane)) * kChunk32;
+      const int q0 = tok >> a.g.lp, q1 = (tok + 16) >> a.g.lp;
+      ids[0] = q0 <= last ? row[q0] : -1;
+      ids[1] = a.g.lp > 4 ? ids[0] : q1 <= last ? row[q1] : -1;
+    };
+    auto issue = [&](int i) {  // chunk i of this warp into its stage
+      if ((i & 31) == 0) load_ids(i);
+      const int id0 = __shfl_sync(kFull, ids[0], i & 31), id1 = __shfl_sync(kFull, ids[1], i & 31);
+      if (lane == 0) {
+        const int st = (n + i) % kStages;  // n: chunks waited for before this stream's part
+        uint8_t* dst = ring + st * SM::kStage;
+        uint64_t* bar = &bars[warp][st];
+        const int tok = (c0 + kWarps * i) * kChunk32;
+        const bool ok0 = page_ok(a.g, id0), ok1 = page_ok(a.g, id1);
+        const bool in1 = tok + 16 < x.vis;  // the second block is needed
+        const uint32_t nb = (ok0 ? 1 : 0) + (ok1 && in1 ? 1 : 0);
+        oks[warp][st] = (ok0 ? 1u : 0u) | (ok1 ? 2u : 0u);
+        if (!ok0 || (in1 && !ok1)) status_or(a.status, KVC_STATUS_BAD_PAGE);
+        tc::mbar_expect_tx(bar, nb * blk_bytes(D));
+        const int blk = (tok & ((1 << a.g.lp) - 1)) >> 4;
+        if (a.g.lp > 4) {
+          if (nb) bulk_load(dst, block_of(a.g, id0, blk), nb * blk_bytes(D), bar);
+        } else {
+          if (ok0) bulk_load(dst, block_of(a.g, id0, 0), blk_bytes(D), bar);
+          if (ok1 && in1) bulk_load(dst + blk_bytes(D), block_of(a.g, id1, 0), blk_bytes(D), bar);
+        }
+      }
+    };
+    const uint32_t nbase = n;
+    for (int i = 0; i < kStages && i < mine && alive; ++i) issue(i);
+
+    // the query rows as B fragments: k step i, k = 2t,2t+1 -> channels CPL t + 4 i + 0,1 and
+    // k = 2t+8,2t+9 -> + 2,3. Each row is brought to [256, 512) by a power of two, which makes bf16
+    // values exact in fp16 (fp32 ones split in two terms).
+    uint32_t qf[NT][PARTS][KS][2];
+    float f[NT][2];  // rows 2t, 2t+1: scale * log2 e over that power
+    int lim[NT][2];
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const uint8_t* c = blk + piece_off(D, 2 * w) + (in & 15) * (D / 2) + lane * (E / 2);
-      const float sc = e4m3_f32(blk[piece_off(D, 2 * w + 1) + (in & 15) * (D / 16) + lane * E / 16]);
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = x.r0 + nt * 8 + g;
+      const bool in = nt * 8 + g < x.rows;
+      float v[CPL];
+      float mx = 0.f;
+      if (in) {
+        const T* qp = static_cast<const T*>(a.q) + x.b * a.qs.b + (r / p.G) * a.qs.t + (x.h * p.G + r % p.G) * a.qs.h +
+                      CPL * t;
+        constexpr int per16 = 16 / (int)sizeof(T);
 #pragma unroll
-      for (int e = 0; e < E / 2; ++e) {
-        const float2 x = f16x2_f32(e2m1x2_f16x2(c[e]));
-        kv[w][2 * e] = x.x * sc;
-        kv[w][2 * e + 1] = x.y * sc;
+        for (int i = 0; i < CPL / per16; ++i) {
+          const uint4 w = __ldg(reinterpret_cast<const uint4*>(qp) + i);
+          const T* e = reinterpret_cast<const T*>(&w);
+#pragma unroll
+          for (int u = 0; u < per16; ++u) v[i * per16 + u] = to_f32(e[u]);
+        }
+#pragma unroll
+        for (int i = 0; i < CPL; ++i) mx = fmaxf(mx, fabsf(v[i]));
+      } else {
+#pragma unroll
+        for (int i = 0; i < CPL; ++i) v[i] = 0.f;
+      }
+      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
+      const int ex = max((int)(__float_as_uint(mx) >> 23), 24);
+      const float mul = __uint_as_float((uint32_t)(262 - ex) << 23);
+      const float inv = __uint_as_float((uint32_t)(ex - 8) << 23) * (a.scale * kLog2e);
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float lo = v[4 * i + 2 * u] * mul, hi = v[4 * i + 2 * u + 1] * mul;
+          const uint32_t w = pack2(lo, hi);
+          qf[nt][0][i][u] = w;
+          if constexpr (PARTS == 2) {
+            const float2 b = f16x2_f32(w);
+            qf[nt][1][i][u] = pack2(lo - b.x, hi - b.y);
+          }
+        }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        f[nt][e] = __shfl_sync(kFull, inv, 8 * t + 4 * e);
+        const int rr = nt * 8 + 2 * t + e;
+        lim[nt][e] = rr < x.rows ? min(max(x.len - x.nq + (x.r0 + rr) / p.G + 1, 0), x.vis) : x.vis;
       }
     }
-    float d = 0.f;
+    const int minlim = min(max(x.len - x.nq + x.r0 / p.G + 1, 0), x.vis);
+
+    float o[NT][KS][4];
+    float ref[NT][2], l[NT][2];  // reference minus kOff (0 until a token is seen), this lane's part of the sum
+    bool none[NT][2];
 #pragma unroll
-    for (int e = 0; e < E; ++e) d += q[e] * kv[0][e];
-    d = warp_sum(d);
-    const float mn = fmaxf(m, d), c = expf(m - mn), x = expf(d - mn);
-    l = l * c + x;
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * c + x * kv[1][e];
-    m = mn;
+      for (int i = 0; i < KS; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        ref[nt][e] = 0.f;
+        l[nt][e] = 0.f;
+        none[nt][e] = true;
+      }
+    }
+
+    for (int i = 0; i < mine && alive; ++i, ++n) {
+      const int st = n % kStages;
+      if (!tc::mbar_wait(&bars[warp][st], (n / kStages) & 1)) {
+        if (lane == 0) status_or(a.status, KVC_STATUS_TIMEOUT);
+        alive = false;
+      }
+      alive = __all_sync(kFull, alive);
+      if (!alive) {  // nothing more is issued; the copies in flight get a second, bounded wait
+        for (int k = 1; k < kStages && i + k < mine; ++k)
+          (void)tc::mbar_wait(&bars[warp][(n + k) % kStages], ((n + k) / kStages) & 1);
+        break;
+      }
+      const uint8_t* buf = ring + st * SM::kStage;
+      const int tok0 = (c0 + kWarps * i) * kChunk32;
+      const uint32_t ok = *reinterpret_cast<volatile uint32_t*>(&oks[warp][st]);
+
+      // S^T of the two 16-token blocks
+      float sc[2][NT][4];
+#pragma unroll
+      for (int blk = 0; blk < 2; ++blk) {
+        const uint8_t* kb = buf + blk * blk_bytes(D);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[blk][nt][e] = 0.f;
+        uint32_t w[2][CPL / 8], s2[2][2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const uint8_t* kr = kb + (g + 8 * half) * (D / 2) + t * (CPL / 2);
+          const uint8_t* sr = kb + piece_off(D, 1) + (g + 8 * half) * (D / 16);
+          if constexpr (D == 128) {
+            const uint4 v = *reinterpret_cast<const uint4*>(kr);
+            w[half][0] = v.x, w[half][1] = v.y, w[half][2] = v.z, w[half][3] = v.w;
+            const uint32_t two = e4m3x2_f16x2(*reinterpret_cast<const uint16_t*>(sr + 2 * t));
+            s2[half][0] = __byte_perm(two, two, 0x1010);
+            s2[half][1] = __byte_perm(two, two, 0x3232);
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(kr);
+            w[half][0] = v.x, w[half][1] = v.y;
+            const uint32_t two = e4m3x2_f16x2(sr[t]);
+            s2[half][0] = s2[half][1] = __byte_perm(two, two, 0x1010);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < CPL / 8; ++j) {  // a word: two k steps
+          uint32_t k0[4], k1[4];
+          e2m1x8_f16(w[0][j], k0);
+          e2m1x8_f16(w[1][j], k1);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int ks = 2 * j + e, sg = D == 128 ? ks / 4 : 0;
+            const uint32_t af[4] = {hmul2(k0[2 * e], s2[0][sg]), hmul2(k1[2 * e], s2[1][sg]),
+                                    hmul2(k0[2 * e + 1], s2[0][sg]), hmul2(k1[2 * e + 1], s2[1][sg])};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int q = 0; q < PARTS; ++q) mma16816(sc[blk][nt], af, qf[nt][q][ks][0], qf[nt][q][ks][1]);
+          }
+        }
+      }
+
+      // logits in base 2; what a row does not see is -inf
+      const bool masked = tok0 + kChunk32 > minlim || ok != 3;
+#pragma unroll
+      for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[blk][nt][e] *= f[nt][e & 1];
+      if (masked) {
+#pragma unroll
+        for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int tok = tok0 + 16 * blk + g + (e >= 2 ? 8 : 0);
+              if (tok >= lim[nt][e & 1] || !(ok >> blk & 1)) sc[blk][nt][e] = -INFINITY;
+            }
+      }
+      // raise the references where a logit passes them by more than 2^kRaise
+      float mx[NT][2];
+      bool raise = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          mx[nt][e] = fmaxf(fmaxf(sc[0][nt][e], sc[0][nt][e + 2]), fmaxf(sc[1][nt][e], sc[1][nt][e + 2]));
+          raise |= none[nt][e] ? mx[nt][e] > -INFINITY : mx[nt][e] > ref[nt][e] + (kOff + kRaise);
+        }
+      if (__any_sync(kFull, raise)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float m = mx[nt][e];
+            m = fmaxf(m, __shfl_xor_sync(kFull, m, 4));
+            m = fmaxf(m, __shfl_xor_sync(kFull, m, 8));
+            m = fmaxf(m, __shfl_xor_sync(kFull, m, 16));
+            if (m > -INFINITY && (none[nt][e] || m > ref[nt][e] + kOff)) {
+              const float to = m - kOff, c = none[nt][e] ? 1.f : ex2(ref[nt][e] - to);
+              none[nt][e] = false;
+              ref[nt][e] = to;
+              l[nt][e] *= c;
+#pragma unroll
+              for (int k = 0; k < KS; ++k) {
+                o[nt][k][e] *= c;
+                o[nt][k][e + 2] *= c;
+              }
+            }
+          }
+      }
+      // P^T fragments
+      uint32_t pf[2][NT][PARTS][2];
+#pragma unroll
+      for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const float p0 = ex2(sc[blk][nt][2 * half] - ref[nt][0]), p1 = ex2(sc[blk][nt][2 * half + 1] - ref[nt][1]);
+            l[nt][0] += p0;
+            l[nt][1] += p1;
+            const uint32_t w = pack2(p0, p1);
+            pf[blk][nt][0][half] = transpose8x8(w);
+            if constexpr (PARTS == 2) {
+              const float2 b = f16x2_f32(w);
+              pf[blk][nt][1][half] = transpose8x8(pack2(p0 - b.x, p1 - b.y));
+            }
+          }
+
+      // O^T += V^T P^T
+#pragma unroll
+      for (int blk = 0; blk < 2; ++blk) {
+        const uint8_t* vb = buf + blk * blk_bytes(D) + piece_off(D, 2);
+        const uint8_t* sb = buf + blk * blk_bytes(D) + piece_off(D, 3);
+        uint32_t w[4][CPV / 8], s[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int tk = 2 * t + (e & 1) + (e >= 2 ? 8 : 0);
+          const uint8_t* vr = vb + tk * (D / 2) + g * (CPV / 2);
+          if constexpr (D == 128) {
+            const uint2 v = *reinterpret_cast<const uint2*>(vr);
+            w[e][0] = v.x, w[e][1] = v.y;
+            s[e] = sb[tk * 8 + g];
+          } else {
+            w[e][0] = *reinterpret_cast<const uint32_t*>(vr);
+            s[e] = sb[tk * 4 + (g >> 1)];
+          }
+          // behind the last visible token lies anything: a zero scale keeps it out of 0 * NaN
+          if (masked && (tok0 + 16 * blk + tk >= x.vis || !(ok >> blk & 1))) s[e] = 0;
+        }
+        const uint32_t s01 = e4m3x2_f16x2(s[0] | s[1] << 8), s23 = e4m3x2_f16x2(s[2] | s[3] << 8);
+#pragma unroll
+        for (int j = 0; j < CPV / 8; ++j) {
+          uint32_t e01[4], o01[4], e23[4], o23[4];
+          constexpr uint32_t m = 0x0f0f0f0fu;
+          e2m1x8_f16((w[0][j] & m) | (w[1][j] << 4 & ~m), e01);
+          e2m1x8_f16((w[0][j] >> 4 & m) | (w[1][j] & ~m), o01);
+          e2m1x8_f16((w[2][j] & m) | (w[3][j] << 4 & ~m), e23);
+          e2m1x8_f16((w[2][j] >> 4 & m) | (w[3][j] & ~m), o23);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t af[4] = {hmul2(e01[e], s01), hmul2(o01[e], s01), hmul2(e23[e], s23), hmul2(o23[e], s23)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int q = 0; q < PARTS; ++q) mma16816(o[nt][4 * j + e], af, pf[blk][nt][q][0], pf[blk][nt][q][1]);
+          }
+        }
+      }
+      __syncwarp();  // every lane is done with the stage
+      if (i + kStages < mine) {
+        // the stage index in issue() counts from this part's first chunk
+        const uint32_t keep = n;
+        n = nbase;
+        issue(i + kStages);
+        n = keep;
+      }
+    }
+
+    // a row's sum over the eight lanes that hold its tokens
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[nt][e] += __shfl_xor_sync(kFull, l[nt][e], 4);
+        l[nt][e] += __shfl_xor_sync(kFull, l[nt][e], 8);
+        l[nt][e] += __shfl_xor_sync(kFull, l[nt][e], 16);
+      }
+    // the four warps' parts into warp 0: 2, 3 to 0, 1, then 1 to 0
+    for (int gap = 2; gap; gap >>= 1) {
+      float* mb = merge + (warp & (gap - 1)) * (SM::kMerge / 4);
+      float2* ml = reinterpret_cast<float2*>(mb + SM::kRows * D);
+      if (warp >= gap && warp < 2 * gap) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if (g == 0) {
+            ml[nt * 8 + 2 * t] = make_float2(ref[nt][0], l[nt][0]);
+            ml[nt * 8 + 2 * t + 1] = make_float2(ref[nt][1], l[nt][1]);
+          }
+#pragma unroll
+          for (int k = 0; k < KS; ++k)
+            *reinterpret_cast<float4*>(mb + ((nt * KS + k) * 32 + lane) * 4) =
+                make_float4(o[nt][k][0], o[nt][k][1], o[nt][k][2], o[nt][k][3]);
+        }
+      }
+      __syncthreads();
+      if (warp < gap) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float ca[2], cb[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float2 y = ml[nt * 8 + 2 * t + e];
+            const float m = y.y > 0.f ? (l[nt][e] > 0.f ? fmaxf(ref[nt][e], y.x) : y.x) : ref[nt][e];
+            ca[e] = l[nt][e] > 0.f ? ex2(ref[nt][e] - m) : 0.f;
+            cb[e] = y.y > 0.f ? ex2(y.x - m) : 0.f;
+            if (isnan(l[nt][e]) || isnan(y.y)) ca[e] = NAN;
+            l[nt][e] = l[nt][e] * ca[e] + y.y * cb[e];
+            ref[nt][e] = m;
+          }
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            const float4 y = *reinterpret_cast<const float4*>(mb + ((nt * KS + k) * 32 + lane) * 4);
+            o[nt][k][0] = o[nt][k][0] * ca[0] + y.x * cb[0];
+            o[nt][k][1] = o[nt][k][1] * ca[1] + y.y * cb[1];
+            o[nt][k][2] = o[nt][k][2] * ca[0] + y.z * cb[0];
+            o[nt][k][3] = o[nt][k][3] * ca[1] + y.w * cb[1];
+          }
+        }
+      }
+      __syncthreads();
+    }
+    if (warp == 0) {
+      const bool whole = ua == 0 && ub == U;
+      const size_t slot = (size_t)blockIdx.x * 2 + (ua == 0 ? 1 : 0);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int rr = nt * 8 + 2 * t + e;
+          if (rr >= x.rows) continue;
+          if (whole) {
+            const int r = x.r0 + rr;
+            const size_t at = ((size_t)x.b * a.T + r / p.G) * a.Hq + x.h * p.G + r % p.G;
+            const float inv = l[nt][e] == 0.f ? 0.f : a.g.ts[1] / l[nt][e];
+            T* op = static_cast<T*>(a.out) + at * D + CPV * g;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+              op[2 * k] = from_f32<T>(o[nt][k][e] * inv);
+              op[2 * k + 1] = from_f32<T>(o[nt][k][e + 2] * inv);
+            }
+            if (a.lse && g == 0)
+              a.lse[at] = l[nt][e] == 0.f ? -INFINITY : (ref[nt][e] + log2f(l[nt][e])) * 0.6931471805599453f;
+          } else {
+            float* op = p.part + (slot * SM::kRows + rr) * D + CPV * g;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) *reinterpret_cast<float2*>(op + 2 * k) = make_float2(o[nt][k][e], o[nt][k][e + 2]);
+            if (g == 0) p.ml[slot * SM::kRows + rr] = make_float2(ref[nt][e], l[nt][e]);
+          }
+        }
+    }
   }
-  const float inv = l > 0.f ? a.g.ts[1] / l : 0.f;
-  T* op = static_cast<T*>(a.out) + (size_t)row * D + lane * E;
+}
+
+// Rows whose stream several CTAs shared, and rows of streams without tokens: a CTA per (stream, row
+// block, row), its warps taking every fourth part.
+constexpr int kCombThreads = 128;
+template <typename T, int D>
+__global__ void __launch_bounds__(kCombThreads) combine_kernel(AttendArgs a, Plan p) {
+  __shared__ int sm_scan[kCombThreads / 32], sm_before;
+  __shared__ float sm_o[kCombThreads / 32][D];
+  __shared__ float2 sm_ml[kCombThreads / 32];
+  griddep_wait();
+  const int vs = blockIdx.x / p.rb, rr = blockIdx.x % p.rb;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per = (p.nvs + kCombThreads - 1) / kCombThreads;
+  int W;
+  int before = scan_units<kCombThreads>(a, p, sm_scan, per, &W);
+  if (vs / per == (int)threadIdx.x) {
+    for (int i = threadIdx.x * per; i < vs; ++i) before += units_of(stream_of(a, p, i, false));
+    sm_before = before;
+  }
+  __syncthreads();
+  before = sm_before;
+  const Stream x = stream_of(a, p, vs, threadIdx.x == 0 && rr == 0);
+  if (rr >= x.rows) return;
+  const int U = units_of(x);
+  const int r = x.r0 + rr;
+  const size_t at = ((size_t)x.b * a.T + r / p.G) * a.Hq + x.h * p.G + r % p.G;
+  T* op = static_cast<T*>(a.out) + at * D;
+  if (U == 0) {
+    for (int i = threadIdx.x; i < D; i += kCombThreads) op[i] = from_f32<T>(0.f);
+    if (a.lse && threadIdx.x == 0) a.lse[at] = -INFINITY;
+    return;
+  }
+  // the CTAs that hold units [before, before + U)
+  auto owner = [&](int u) {
+    int c = (int)(((long long)u * p.grid) / W);
+    while (c > 0 && cta_first(W, c, p.grid) > u) --c;
+    while (cta_first(W, c + 1, p.grid) <= u) ++c;
+    return c;
+  };
+  const int ca = owner(before), cb = owner(before + U - 1);
+  if (ca == cb) return;  // written by that CTA
+  constexpr int E = D / 32;
+  float o[E], l = 0.f, m = -INFINITY;
 #pragma unroll
-  for (int e = 0; e < E; ++e) op[e] = from_f32<T>(o[e] * inv);
-  if (a.lse && lane == 0) a.lse[row] = l > 0.f ? m + logf(l) : -INFINITY;
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  auto add = [&](float y_m, float y_l, const float (&y)[E]) {
+    if (y_l == 0.f) return;
+    const float to = l == 0.f ? y_m : fmaxf(m, y_m);
+    const float c0 = l == 0.f ? 0.f : ex2(m - to), c1 = ex2(y_m - to);
+    l = l * c0 + y_l * c1;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = o[e] * c0 + y[e] * c1;
+    m = to;
+  };
+  for (int c = ca + warp; c <= cb; c += kCombThreads / 32) {
+    if (cta_first(W, c, p.grid) >= cta_first(W, c + 1, p.grid)) continue;  // a CTA without units
+    const size_t slot = (size_t)c * 2 + (c == ca ? 1 : 0);
+    // the first CTA's part begins at the stream's first unit, the others' behind it
+    const float2 ml = p.ml[slot * p.rb + rr];
+    float y[E];
+    const float* src = p.part + (slot * p.rb + rr) * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) y[e] = src[e];
+    add(ml.x, ml.y, y);
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) sm_o[warp][lane * E + e] = o[e];
+  if (lane == 0) sm_ml[warp] = make_float2(m, l);
+  __syncthreads();
+  if (warp == 0) {
+    for (int w = 1; w < kCombThreads / 32; ++w) {
+      float y[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[e] = sm_o[w][lane * E + e];
+      add(sm_ml[w].x, sm_ml[w].y, y);
+    }
+    const float inv = l == 0.f ? 0.f : a.g.ts[1] / l;
+#pragma unroll
+    for (int e = 0; e < E; ++e) op[lane * E + e] = from_f32<T>(o[e] * inv);
+    if (a.lse && lane == 0) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  }
+}
+
+// Row tiles of 8 a block takes: one covers the decode step of up to 8 query heads per KV head; more rows
+// share the decoding of a chunk.
+int tiles_for(int R, int parts) { return R <= 8 ? 1 : (R <= 16 || parts == 2) ? 2 : 4; }
+int min_blocks(int nt, int parts) { return nt * parts == 1 ? 4 : nt * parts == 2 ? 3 : 2; }
+
+Plan make_plan(const AttendArgs& a, int parts, int sms, size_t* bytes) {
+  Plan p = {};
+  p.G = a.Hq / a.t.Hkv;
+  const int R = p.G * a.T, nt = tiles_for(R, parts);
+  p.rb = 8 * nt;
+  p.nrb = (R + p.rb - 1) / p.rb;
+  p.nvs = a.t.S * p.nrb;
+  p.grid = (sms < kMaxGridSMs ? sms : kMaxGridSMs) * min_blocks(nt, parts);
+  const long long units = (long long)p.nvs * ((((long long)a.t.maxp << a.g.lp) + kUnit - 1) / kUnit);
+  if (units < p.grid) p.grid = (int)units;
+  const size_t slots = (size_t)p.grid * 2 * p.rb;
+  const size_t ml = (slots * sizeof(float2) + 255) & ~(size_t)255;
+  p.ml = static_cast<float2*>(a.ws);
+  p.part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + ml);
+  if (bytes) *bytes = ml + slots * a.g.D * sizeof(float);
+  return p;
+}
+
+template <typename T, int D, int NT, int PARTS>
+int go(const AttendArgs& a, const Plan& p, cudaStream_t s) {
+  constexpr int MINB = NT * PARTS == 1 ? 4 : NT * PARTS == 2 ? 3 : 2;
+  auto k = attend_kernel<T, D, NT, PARTS, MINB>;
+  constexpr int smem = Smem<D, NT>::bytes;
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return KVC_ERR_LAUNCH;
+  if (launch_pdl(k, dim3(p.grid), dim3(32 * kWarps), smem, s, false, a, p) != cudaSuccess) return KVC_ERR_LAUNCH;
+  if (launch_pdl(combine_kernel<T, D>, dim3((unsigned)((long long)p.nvs * p.rb)), dim3(kCombThreads), 0, s, false, a,
+                 p) != cudaSuccess)
+    return KVC_ERR_LAUNCH;
+  return KVC_OK;
+}
+
+template <typename T, int D, int PARTS>
+int go_tiles(const AttendArgs& a, const Plan& p, cudaStream_t s) {
+  switch (p.rb / 8) {
+    case 1: return go<T, D, 1, PARTS>(a, p, s);
+    case 2: return go<T, D, 2, PARTS>(a, p, s);
+    default:
+      if constexpr (PARTS == 1) return go<T, D, 4, PARTS>(a, p, s);
+      return KVC_ERR_INVALID_ARG;
+  }
 }
 
 }  // namespace
 
-size_t attend_ws_bytes(int, int, int, int, int) { return 256; }
+size_t attend_ws_bytes(const PoolGeom& g, const PageTab& t, int Hq, int T) {
+  AttendArgs a = {};
+  a.g = g;
+  a.t = t;
+  a.Hq = Hq;
+  a.T = T;
+  size_t most = 0;
+  for (int parts = 1; parts <= 2; ++parts) {
+    size_t n;
+    make_plan(a, parts, kMaxGridSMs, &n);
+    most = n > most ? n : most;
+  }
+  return most;
+}
 
 int launch_page_attend(const AttendArgs& a, int dtype, cudaStream_t s) {
-  const long long rows = (long long)a.t.B * a.T * a.Hq;
-  const dim3 grid((unsigned)((rows + 3) / 4));
-  cudaError_t e;
-  if (dtype == KVC_BF16)
-    e = launch_pdl(a.g.D == 128 ? attend_simple_kernel<__nv_bfloat16, 128> : attend_simple_kernel<__nv_bfloat16, 64>,
-                   grid, dim3(128), 0, s, false, a);
-  else
-    e = launch_pdl(a.g.D == 128 ? attend_simple_kernel<float, 128> : attend_simple_kernel<float, 64>, grid, dim3(128),
-                   0, s, false, a);
-  return e == cudaSuccess ? KVC_OK : KVC_ERR_LAUNCH;
+  int dev, sms;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return KVC_ERR_LAUNCH;
+  if (dtype == KVC_BF16) {
+    const Plan p = make_plan(a, 1, sms, nullptr);
+    return a.g.D == 128 ? go_tiles<__nv_bfloat16, 128, 1>(a, p, s) : go_tiles<__nv_bfloat16, 64, 1>(a, p, s);
+  }
+  const Plan p = make_plan(a, 2, sms, nullptr);
+  return a.g.D == 128 ? go_tiles<float, 128, 2>(a, p, s) : go_tiles<float, 64, 2>(a, p, s);
 }
 
 }  // namespace kvc
