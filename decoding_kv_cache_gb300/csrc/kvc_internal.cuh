@@ -44,6 +44,10 @@ __device__ __forceinline__ void status_or(int32_t* status, unsigned bits) {
 // the overlap is the launch's own latency and the waiting roles' prologue.
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 
+// For kernels of a few CTAs (the page operators), whose successors' waiting CTAs cost nothing: lets
+// the next kernel of the stream come up and wait in griddep_wait().
+__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+
 // Launch with programmatic stream serialisation (and cooperatively if asked); when the
 // runtime refuses the attribute, launch again without it.
 template <typename... Params, typename... Args>

@@ -36,15 +36,14 @@ struct PageTab {
   int32_t* len;            // [S]
 };
 
-// Workspace of the page operators (kvc_page_workspace_size): the first two are zeroed by each call
-// that uses them.
+// Workspace of the page operators (kvc_page_workspace_size).
 struct PageWs {
-  int32_t* head;     // [0] nfree on entry; compaction: [1] pages it takes, [2] set when it cannot
+  int32_t* head;     // [0] nfree on entry, [1] pages the call took (compaction; -1: too few)
   uint32_t* gone;    // one bit per page: its last reference went in this call
   int32_t* need;     // [S] pages a stream takes (bit 30: its last page is copied)
   int32_t* sums;     // [ceil(S/256)] their sums
   int4* plan;        // [S] compaction: first row written, kept, length, flags
-  int32_t* newtab;   // [S][maxp] compaction: the destination pages (-1: one to be taken)
+  int32_t* newtab;   // [2][S][maxp] compaction: the destination pages (-1: one to be taken), for K and V
   size_t zero_bytes;
 };
 

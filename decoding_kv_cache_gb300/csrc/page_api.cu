@@ -61,7 +61,7 @@ size_t page_ws(const PoolGeom& g, const PageTab& t, PageWs* w, void* base) {
   const size_t o_need = off;  off += up256((size_t)t.S * 4);
   const size_t o_sums = off;  off += up256(((size_t)t.S + 255) / 256 * 4);
   const size_t o_plan = off;  off += up256((size_t)t.S * sizeof(int4));
-  const size_t o_tab = off;   off += up256((size_t)t.S * t.maxp * 4);
+  const size_t o_tab = off;   off += up256((size_t)t.S * t.maxp * 8);
   if (w) {
     w->head = reinterpret_cast<int32_t*>(b);
     w->gone = reinterpret_cast<uint32_t*>(b + o_gone);

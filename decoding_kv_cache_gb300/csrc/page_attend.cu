@@ -156,6 +156,7 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
     for (int i = 0; i < kStages; ++i) tc::mbar_init(&bars[warp][i], 1);
     tc::mbar_fence_init();
   }
+  griddep_launch();  // the combine kernel's CTAs wait beside this wave
   griddep_wait();
 
   // this CTA's units, and the stream its first one lies in
@@ -573,6 +574,7 @@ __global__ void __launch_bounds__(kCombThreads) combine_kernel(AttendArgs a, Pla
   __shared__ int sm_scan[kCombThreads / 32], sm_before;
   __shared__ float sm_o[kCombThreads / 32][D];
   __shared__ float2 sm_ml[kCombThreads / 32];
+  griddep_launch();
   griddep_wait();
   const int vs = blockIdx.x / p.rb, rr = blockIdx.x % p.rb;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

@@ -8,9 +8,10 @@
 // that another stream shares is not written: the stream takes a fresh page in its place, and the old
 // page stays as the source. And the pages behind the kept rows are given back.
 //
-//   plan   a CTA per stream checks the list, finds the first row that moves and lists the destination
+//   plan   a CTA per stream clears its share of the bitmap, checks the list, finds the first row that moves and lists the destination
 //          pages (marking those to be replaced); refs are read here only, before any stream's change
-//   move   a CTA per stream numbers its fresh pages (in stream order), sweeps, then updates its row
+//   move   a CTA per stream and per K or V numbers the fresh pages (in stream order) and sweeps
+//   finish rows and lengths take their new values, pages are counted down
 //   push   the pages nobody holds any more join the free list (page_ops.cu)
 #include "page.cuh"
 
@@ -21,7 +22,7 @@ int page_push(const PoolGeom& g, const PageWs& w, cudaStream_t s);
 namespace {
 
 constexpr int kPlanThreads = 128;
-constexpr int kMoveThreads = 256;
+constexpr int kMoveThreads = 128;
 constexpr int kTile = 64;  // tokens moved at a time
 
 enum { kBad = 1, kMoves = 2 };  // plan.w
@@ -30,6 +31,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PoolGeom g, PageTab 
                                                            const int32_t* kept_len, int stride, int per_seq,
                                                            int32_t* status, PageWs w) {
   __shared__ int sm_bad, sm_k0, sm_need;
+  griddep_launch();
   griddep_wait();
   const int s = blockIdx.x, lst = per_seq ? s / t.Hkv % t.B : s;
   const int32_t* idx = kept_idx + (size_t)lst * stride;
@@ -40,8 +42,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PoolGeom g, PageTab 
     sm_bad = badlen || m < 0 || m > n || m > stride;
     sm_k0 = m;
     sm_need = 0;
-    if (s == 0) w.head[0] = *g.nfree;
+    if (s == 0) {
+      w.head[0] = *g.nfree;
+      w.head[1] = 0;
+    }
   }
+  for (int i = s * kPlanThreads + (int)threadIdx.x; i < (g.npages + 31) / 32; i += t.S * kPlanThreads) w.gone[i] = 0u;
   __syncthreads();
   bool bad = sm_bad;
   int k0 = m;
@@ -59,6 +65,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PoolGeom g, PageTab 
   k0 = sm_k0;
   int32_t* row = t.table + (size_t)s * t.maxp;
   int32_t* to = w.newtab + (size_t)s * t.maxp;
+  int32_t* to_v = to + (size_t)t.S * t.maxp;  // the V rows' CTA numbers the same pages for itself
   if (!bad) {
     // every page the sweep reads must exist, and every page dropped
     const int e = pages_of(n, g.lp);
@@ -70,7 +77,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PoolGeom g, PageTab 
       for (int i = (k0 >> g.lp) + (int)threadIdx.x; i < pe; i += kPlanThreads) {
         const int p = row[i];
         const bool shared = page_ok(g, p) && g.refs[p] > 1;
-        to[i] = shared ? -1 : p;
+        to[i] = to_v[i] = shared ? -1 : p;
         need += shared;
       }
       if (need) atomicAdd(&sm_need, need);
@@ -82,7 +89,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PoolGeom g, PageTab 
     if (sm_bad) status_or(status, sm_bad > 1 ? KVC_STATUS_BAD_PAGE : KVC_STATUS_BAD_INDEX);
     const int need = bad ? 0 : sm_need;
     w.need[s] = need;
-    if (need) atomicAdd(&w.head[1], need);
     // the first row written: with its page replaced, the page's unmoved rows go along
     int first = k0;
     if (!bad && k0 < m && to[k0 >> g.lp] < 0) first = k0 >> g.lp << g.lp;
@@ -98,156 +104,209 @@ __device__ __forceinline__ void drop_one(const PoolGeom& g, const PageWs& w, int
     atomicAdd(&g.refs[p], 1);
 }
 
-// One tile of kTile destinations: each thread carries U code vectors (16 bytes) and, the first ones,
-// a token's scale vector of K or V (D/16 bytes).
+// A CTA moves the K or the V rows of a stream, kTile destinations at a time: a thread carries U code
+// vectors (16 bytes) and, the first ones, a token's scales (D/16 bytes). Three reads hang on one another
+// (list -> page number -> row), so each runs a tile further ahead: while tile i is written, rows of tiles
+// i+1 to i+3, page numbers of i+4 and list entries of i+5 are in flight. (With rows one tile ahead a tile
+// takes a memory latency, whatever the rest: 24.5 us for 36 layers x 8 heads x 1792 kept of 2048.)
 template <int D>
-struct Tile {
-  static constexpr int kVec = D / 32;                          // code vectors of a token's row
-  static constexpr int U = 2 * kTile * kVec / kMoveThreads;    // per thread
-  static constexpr int kSc = 2 * kTile;                        // scale vectors of the tile
-  uint4 c[U];
-  uint64_t sc;
+struct Move {
+  static constexpr int kVec = D / 32;                    // code vectors of a token's row
+  static constexpr int U = kTile * kVec / kMoveThreads;  // per thread
+  static_assert(U >= 1 && kTile <= kMoveThreads, "a tile gives every thread a vector");
 };
-
-template <int D>
-__device__ __forceinline__ uint8_t* row_of(const PoolGeom& g, int page_id, int tok, int piece) {
-  const int in = tok & ((1 << g.lp) - 1);
-  return block_of(g, page_id, in >> 4) + piece_off(D, piece) + (in & 15) * ((piece & 1) ? D / 16 : D / 2);
-}
-
-template <int D>
-__device__ __forceinline__ void tile_load(const PoolGeom& g, const int32_t* row, const int32_t* idx, int t0, int m,
-                                         Tile<D>& x) {
-  using TT = Tile<D>;
-#pragma unroll
-  for (int u = 0; u < TT::U; ++u) {
-    const int e = threadIdx.x + u * kMoveThreads;
-    const int v = e % TT::kVec, k = t0 + e / TT::kVec % kTile, piece = e / (TT::kVec * kTile) * 2;
-    if (k < m) {
-      const int src = idx[k];
-      x.c[u] = reinterpret_cast<const uint4*>(row_of<D>(g, row[src >> g.lp], src, piece))[v];
-    }
-  }
-  if (threadIdx.x < TT::kSc) {
-    const int k = t0 + threadIdx.x % kTile, piece = threadIdx.x / kTile * 2 + 1;
-    if (k < m) {
-      const int src = idx[k];
-      const uint8_t* p = row_of<D>(g, row[src >> g.lp], src, piece);
-      if constexpr (D == 128)
-        x.sc = *reinterpret_cast<const uint64_t*>(p);
-      else
-        x.sc = *reinterpret_cast<const uint32_t*>(p);
-    }
-  }
-}
-
-template <int D>
-__device__ __forceinline__ void tile_store(const PoolGeom& g, const int32_t* to, int t0, int m, const Tile<D>& x) {
-  using TT = Tile<D>;
-#pragma unroll
-  for (int u = 0; u < TT::U; ++u) {
-    const int e = threadIdx.x + u * kMoveThreads;
-    const int v = e % TT::kVec, k = t0 + e / TT::kVec % kTile, piece = e / (TT::kVec * kTile) * 2;
-    if (k < m) reinterpret_cast<uint4*>(row_of<D>(g, to[k >> g.lp], k, piece))[v] = x.c[u];
-  }
-  if (threadIdx.x < TT::kSc) {
-    const int k = t0 + threadIdx.x % kTile, piece = threadIdx.x / kTile * 2 + 1;
-    if (k < m) {
-      uint8_t* p = row_of<D>(g, to[k >> g.lp], k, piece);
-      if constexpr (D == 128)
-        *reinterpret_cast<uint64_t*>(p) = x.sc;
-      else
-        *reinterpret_cast<uint32_t*>(p) = (uint32_t)x.sc;
-    }
-  }
-}
 
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(PoolGeom g, PageTab t, const int32_t* kept_idx, int stride,
                                                            int per_seq, int32_t* status, PageWs w) {
-  __shared__ int sm[8], sm_base;
+  __shared__ int sm[2 * kMoveThreads / 32];
+  griddep_launch();
   griddep_wait();
-  const int s = blockIdx.x;
+  using M = Move<D>;
+  constexpr int kWarpsM = kMoveThreads / 32;
+  const int s = blockIdx.x >> 1, kv = blockIdx.x & 1;
   const int4 plan = w.plan[s];
-  const int nfree = w.head[0], total = w.head[1];
+  const int nfree = w.head[0];
+  // pages the streams before this one take, and all: nearly always none, in one batch of reads
+  int before = 0, total = 0;
+  for (int i = threadIdx.x; i < t.S; i += kMoveThreads) {
+    const int v = w.need[i];
+    total += v;
+    if (i < s) before += v;
+  }
+  if (__syncthreads_or(total)) {
+    before = __reduce_add_sync(kFull, before);
+    total = __reduce_add_sync(kFull, total);
+    if ((threadIdx.x & 31) == 0) {
+      sm[threadIdx.x >> 5] = before;
+      sm[kWarpsM + (threadIdx.x >> 5)] = total;
+    }
+    __syncthreads();
+    before = total = 0;
+#pragma unroll
+    for (int i = 0; i < kWarpsM; ++i) {
+      before += sm[i];
+      total += sm[kWarpsM + i];
+    }
+  }
   const bool none = total > 0 && (total > nfree || nfree > g.npages);
-  if (s == 0 && threadIdx.x == 0) {
-    if (none)
-      status_or(status, KVC_STATUS_NO_PAGES);
-    else
-      *g.nfree = nfree - total;
-    if (none) w.head[2] = 1;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    if (none) status_or(status, KVC_STATUS_NO_PAGES);
+    w.head[1] = none ? -1 : total;  // for the kernels behind
   }
   if (none || (plan.w & kBad)) return;
-  const int first = plan.x, m = plan.y, n = plan.z;
-  int32_t* row = t.table + (size_t)s * t.maxp;
-  int32_t* to = w.newtab + (size_t)s * t.maxp;
-  const int need = w.need[s], p0 = first >> g.lp, pe = pages_of(m, g.lp);
-  if (need) {  // number the fresh pages: the streams before this one, then this row in order
-    int b = 0;
-    for (int i = threadIdx.x; i < s; i += kMoveThreads) b += w.need[i];
-    b = __reduce_add_sync(kFull, b);
-    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = b;
-    __syncthreads();
+  const int first = plan.x, m = plan.y;
+  const int32_t* row = t.table + (size_t)s * t.maxp;
+  int32_t* to = w.newtab + ((size_t)kv * t.S + s) * t.maxp;
+  const int need = w.need[s], pe = pages_of(m, g.lp);
+  if (need) {  // the marked pages' numbers: what the streams before left, this row in order
     if (threadIdx.x < 32) {
-      int at = nfree - 1;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) at -= sm[i];
-      for (int i0 = p0; i0 < pe; i0 += 32) {
+      int at = nfree - 1 - before;
+      for (int i0 = first >> g.lp; i0 < pe; i0 += 32) {
         const int i = i0 + (int)threadIdx.x;
         const bool want = i < pe && to[i] < 0;
         const unsigned mask = __ballot_sync(kFull, want);
         if (want) {
           const int p = g.free_list[at - __popc(mask & ((1u << threadIdx.x) - 1))];
           to[i] = page_ok(g, p) ? p : row[i];
-          if (page_ok(g, p)) g.refs[p] = 1;
         }
         at -= __popc(mask);
       }
     }
     __syncthreads();
   }
-  if (plan.w & kMoves) {
-    const int32_t* idx = kept_idx + (size_t)(per_seq ? s / t.Hkv % t.B : s) * stride;
-    Tile<D> cur, nxt;
-    tile_load<D>(g, row, idx, first, m, cur);
-    for (int t0 = first; t0 < m; t0 += kTile) {
-      if (t0 + kTile < m) tile_load<D>(g, row, idx, t0 + kTile, m, nxt);
-      __syncthreads();  // every thread's loads of this tile are done
-      tile_store<D>(g, to, t0, m, cur);
-      cur = nxt;
+  if (!(plan.w & kMoves)) return;
+
+  const int32_t* idx = kept_idx + (size_t)(per_seq ? s / t.Hkv % t.B : s) * stride;
+  const int lmask = (1 << g.lp) - 1;
+  const int codes = kv ? piece_off(D, 2) : 0, scales = kv ? piece_off(D, 3) : piece_off(D, 1);
+  const bool has_sc = threadIdx.x < kTile;
+  // the tokens of a tile this thread serves: U for the codes, one for the scales
+  const int v = threadIdx.x % M::kVec, k_of = threadIdx.x / M::kVec;
+  constexpr int kStep = kMoveThreads / M::kVec;  // tokens between two of a thread's vectors
+  struct Ahead {
+    int tok[M::U + 1], page[M::U + 1];
+  };
+  auto read_list = [&](int t0, Ahead& x) {
+#pragma unroll
+    for (int u = 0; u < M::U; ++u) {
+      const int k = t0 + k_of + u * kStep;
+      x.tok[u] = k < m ? idx[k] : -1;
     }
+    const int k = t0 + (int)threadIdx.x;
+    x.tok[M::U] = has_sc && k < m ? idx[k] : -1;
+  };
+  auto read_pages = [&](Ahead& x) {
+#pragma unroll
+    for (int u = 0; u <= M::U; ++u) x.page[u] = x.tok[u] >= 0 ? row[x.tok[u] >> g.lp] : 0;
+  };
+  struct Rows {
+    uint4 c[M::U];
+    uint64_t sc;
+  };
+  auto read_rows = [&](const Ahead& x, Rows& r) {
+#pragma unroll
+    for (int u = 0; u < M::U; ++u)
+      if (x.tok[u] >= 0) {
+        const int in = x.tok[u] & lmask;
+        r.c[u] = __ldcs(reinterpret_cast<const uint4*>(block_of(g, x.page[u], in >> 4) + codes + (in & 15) * (D / 2)) + v);
+      }
+    if (x.tok[M::U] >= 0) {
+      const int in = x.tok[M::U] & lmask;
+      const uint8_t* p = block_of(g, x.page[M::U], in >> 4) + scales + (in & 15) * (D / 16);
+      if constexpr (D == 128)
+        r.sc = *reinterpret_cast<const uint64_t*>(p);
+      else
+        r.sc = *reinterpret_cast<const uint32_t*>(p);
+    }
+  };
+  auto write_rows = [&](int t0, const Rows& r) {
+#pragma unroll
+    for (int u = 0; u < M::U; ++u) {
+      const int k = t0 + k_of + u * kStep;
+      if (k < m) {
+        const int in = k & lmask;
+        reinterpret_cast<uint4*>(block_of(g, to[k >> g.lp], in >> 4) + codes + (in & 15) * (D / 2))[v] = r.c[u];
+      }
+    }
+    const int k = t0 + (int)threadIdx.x;
+    if (has_sc && k < m) {
+      const int in = k & lmask;
+      uint8_t* p = block_of(g, to[k >> g.lp], in >> 4) + scales + (in & 15) * (D / 16);
+      if constexpr (D == 128)
+        *reinterpret_cast<uint64_t*>(p) = r.sc;
+      else
+        *reinterpret_cast<uint32_t*>(p) = (uint32_t)r.sc;
+    }
+  };
+
+  Ahead x[2];
+  Rows r[4];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    read_list(first + i * kTile, x[0]);
+    read_pages(x[0]);
+    read_rows(x[0], r[i]);
   }
-  __syncthreads();
-  if (need) {
-    for (int i = p0 + (int)threadIdx.x; i < pe; i += kMoveThreads) {
+  read_list(first + 3 * kTile, x[1]);
+  read_pages(x[1]);
+  read_list(first + 4 * kTile, x[0]);
+  for (int t0 = first; t0 < m; t0 += 4 * kTile)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {  // tile i = t0 / kTile + j
+      const int ti = t0 + j * kTile;
+      read_rows(x[(j + 1) & 1], r[(j + 3) & 3]);      // tile i + 3
+      read_pages(x[j & 1]);                           // i + 4
+      read_list(ti + 5 * kTile, x[(j + 1) & 1]);      // i + 5
+      __syncthreads();                                // every thread's rows of tile i are read
+      write_rows(ti, r[j]);
+    }
+}
+
+// After the moves: rows and lengths of a stream (a warp each), its replaced pages and those behind the
+// kept rows counted down.
+__global__ void __launch_bounds__(256) finish_kernel(PoolGeom g, PageTab t, PageWs w) {
+  griddep_launch();
+  griddep_wait();
+  const int s = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
+  const int total = w.head[1];
+  if (s >= t.S) return;
+  if (total < 0) {  // too few pages: nothing happened, and nothing is taken
+    return;
+  }
+  const int4 plan = w.plan[s];
+  if (plan.w & kBad) return;
+  int32_t* row = t.table + (size_t)s * t.maxp;
+  const int32_t* to = w.newtab + (size_t)s * t.maxp;
+  const int pe = pages_of(plan.y, g.lp);
+  if (w.need[s])
+    for (int i = (plan.x >> g.lp) + lane; i < pe; i += 32) {
       const int old = row[i], p = to[i];
       if (p != old) {
         row[i] = p;
+        g.refs[p] = 1;
         drop_one(g, w, old);
       }
     }
-  }
-  for (int i = pe + (int)threadIdx.x; i < pages_of(n, g.lp); i += kMoveThreads) {
+  for (int i = pe + lane; i < pages_of(plan.z, g.lp); i += 32) {
     drop_one(g, w, row[i]);
     row[i] = -1;
   }
-  if (threadIdx.x == 0) t.len[s] = m;
+  if (lane == 0) t.len[s] = plan.y;
 }
 
 }  // namespace
 
 int launch_page_compact(const PoolGeom& g, const PageTab& t, const int32_t* kept_idx, const int32_t* kept_len,
                         int stride, int per_seq, int32_t* status, const PageWs& w, cudaStream_t s) {
-  if (cudaMemsetAsync(w.head, 0, w.zero_bytes, s) != cudaSuccess) return KVC_ERR_LAUNCH;
   if (launch_pdl(plan_kernel, dim3(t.S), dim3(kPlanThreads), 0, s, false, g, t, kept_idx, kept_len, stride, per_seq,
                  status, w) != cudaSuccess)
     return KVC_ERR_LAUNCH;
-  const cudaError_t e = g.D == 128 ? launch_pdl(move_kernel<128>, dim3(t.S), dim3(kMoveThreads), 0, s, false, g, t,
-                                                kept_idx, stride, per_seq, status, w)
-                                   : launch_pdl(move_kernel<64>, dim3(t.S), dim3(kMoveThreads), 0, s, false, g, t,
-                                                kept_idx, stride, per_seq, status, w);
-  if (e != cudaSuccess) return KVC_ERR_LAUNCH;
+  if (launch_pdl(g.D == 128 ? move_kernel<128> : move_kernel<64>, dim3(2 * t.S), dim3(kMoveThreads), 0, s, false, g, t,
+                 kept_idx, stride, per_seq, status, w) != cudaSuccess)
+    return KVC_ERR_LAUNCH;
+  if (launch_pdl(finish_kernel, dim3((t.S + 7) / 8), dim3(256), 0, s, false, g, t, w) != cudaSuccess)
+    return KVC_ERR_LAUNCH;
   return page_push(g, w, s);
 }
 

@@ -3,17 +3,21 @@
 // Every result is a function of the arguments alone: pages are taken from the free list's end in
 // stream order, counted with integer atomics (whose order cannot show), and given back in the order
 // of their numbers through a bitmap. A call that cannot get all its pages changes nothing.
+#include <cooperative_groups.h>
+
 #include "page.cuh"
 
 namespace kvc {
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr int kCopyFlag = 1 << 30;
 constexpr int kPlanThreads = 256;   // streams per planning CTA
-constexpr int kAssignStreams = 32;  // streams per assigning CTA
+constexpr int kAssignStreams = 8;   // streams per assigning CTA, a warp each
 constexpr int kAssignThreads = 256;
 constexpr int kPushThreads = 256;
-constexpr int kPushWords = 1024;  // bitmap words per giving-back CTA
+constexpr int kPushWords = kPushThreads;  // bitmap words per giving-back CTA
 
 __device__ __forceinline__ int warp_sum_i(int v) { return __reduce_add_sync(kFull, v); }
 
@@ -30,6 +34,7 @@ __device__ __forceinline__ int block_sum(int v, int* sm) {
 }
 
 __global__ void init_kernel(PoolGeom g, PageTab t) {
+  griddep_launch();
   griddep_wait();
   const long long n = (long long)g.npages, e = (long long)t.S * t.maxp;
   const long long step = (long long)gridDim.x * blockDim.x;
@@ -71,6 +76,7 @@ __device__ __forceinline__ bool extend_wants(const PoolGeom& g, const PageTab& t
 __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(PoolGeom g, PageTab t, const int32_t* add,
                                                                   int add_all, int32_t* status, PageWs w) {
   __shared__ int sm[8];
+  griddep_launch();
   griddep_wait();
   const int s = blockIdx.x * kPlanThreads + threadIdx.x;
   int need = 0;
@@ -133,27 +139,29 @@ __device__ __forceinline__ void need_before(const PageWs& w, int S, int s0, int*
   *before = block_sum(b, sm);
 }
 
-__device__ __forceinline__ void copy_page(const PoolGeom& g, int dst, int src, int lane, int lanes) {
+__device__ __forceinline__ void copy_page(const PoolGeom& g, int dst, int src, int lane) {
   const size_t bytes = (size_t)blk_bytes(g.D) << (g.lp - 4);
   uint4* d = reinterpret_cast<uint4*>(g.data + (size_t)dst * bytes);
   const uint4* x = reinterpret_cast<const uint4*>(g.data + (size_t)src * bytes);
   const int n = (int)(bytes / 16);
-  for (int i = lane; i < n; i += 4 * lanes) {
-    uint4 v[4];
+  constexpr int kDeep = 9;  // vectors a lane has in flight: two rounds for 64 tokens of D = 128
+  for (int i = lane; i < n; i += kDeep * 32) {
+    uint4 v[kDeep];
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (i + u * lanes < n) v[u] = x[i + u * lanes];
+    for (int u = 0; u < kDeep; ++u)
+      if (i + u * 32 < n) v[u] = x[i + u * 32];
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (i + u * lanes < n) d[i + u * lanes] = v[u];
+    for (int u = 0; u < kDeep; ++u)
+      if (i + u * 32 < n) d[i + u * 32] = v[u];
   }
 }
 
-// The pages handed out: 32 streams a CTA, a warp per stream in turn; the copies go with them.
+// The pages handed out: a warp per stream, which also copies its page.
 __global__ void __launch_bounds__(kAssignThreads) extend_assign_kernel(PoolGeom g, PageTab t, const int32_t* add,
                                                                       int add_all, int32_t* start, int32_t* status,
                                                                       PageWs w) {
   __shared__ int sm[8];
+  griddep_launch();
   griddep_wait();
   const int s0 = blockIdx.x * kAssignStreams, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int before, total;
@@ -166,48 +174,38 @@ __global__ void __launch_bounds__(kAssignThreads) extend_assign_kernel(PoolGeom 
     else
       *g.nfree = nfree - total;
   }
-  int incl = s0 + lane < t.S ? need_of(w, s0 + lane) : 0;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(kFull, incl, o);
-    if (lane >= o) incl += v;
+  const int s = s0 + warp;
+  if (s >= t.S) return;
+  for (int i = s0; i < s; ++i) before += need_of(w, i);
+  const int need = w.need[s];
+  if (none || need < 0) {
+    if (lane == 0 && start) start[s] = -1;
+    return;
   }
-  for (int i = warp; i < kAssignStreams; i += kAssignThreads / 32) {
-    const int s = s0 + i;
-    if (s >= t.S) break;
-    const int need = w.need[s];
-    if (none || need < 0) {
-      if (lane == 0 && start) start[s] = -1;
-      continue;
-    }
-    const int b = s / t.Hkv % t.B;
-    const int a = add ? add[b] : add_all, n = t.len[s];
-    const int end = __shfl_sync(kFull, incl, i);
-    const int k = need & ~kCopyFlag;
-    const int copy = need & kCopyFlag ? 1 : 0;
-    int at = nfree - 1 - (before + end - k);  // free-list slot of the stream's first page
-    int32_t* row = t.table + (size_t)s * t.maxp;
-    if (copy) {
-      const int old = row[n >> g.lp], p = g.free_list[at];
-      if (page_ok(g, p)) copy_page(g, p, old, lane, 32);
-      __syncwarp();
-      if (lane == 0) {
-        row[n >> g.lp] = p;
-        if (page_ok(g, p)) g.refs[p] = 1;
-        atomicSub(&g.refs[old], 1);
-      }
-    }
-    const int first = pages_of(n, g.lp);
-    for (int j = lane; j < k - copy; j += 32) {
-      const int p = g.free_list[at - copy - j];
-      row[first + j] = p;
-      if (page_ok(g, p)) g.refs[p] = 1;
-    }
+  const int b = s / t.Hkv % t.B;
+  const int a = add ? add[b] : add_all, n = t.len[s];
+  const int k = need & ~kCopyFlag, copy = need & kCopyFlag ? 1 : 0;
+  const int at = nfree - 1 - before;  // free-list slot of the stream's first page
+  int32_t* row = t.table + (size_t)s * t.maxp;
+  const int first = pages_of(n, g.lp);
+  for (int j = lane; j < k - copy; j += 32) {
+    const int p = g.free_list[at - copy - j];
+    row[first + j] = p;
+    if (page_ok(g, p)) g.refs[p] = 1;
+  }
+  if (copy) {
+    const int old = row[n >> g.lp], p = g.free_list[at];
+    if (page_ok(g, p)) copy_page(g, p, old, lane);
     __syncwarp();
     if (lane == 0) {
-      t.len[s] = n + a;
-      if (start) start[s] = n;
+      row[n >> g.lp] = p;
+      if (page_ok(g, p)) g.refs[p] = 1;
+      atomicSub(&g.refs[old], 1);
     }
+  }
+  if (lane == 0) {
+    t.len[s] = n + a;
+    if (start) start[s] = n;
   }
 }
 
@@ -229,6 +227,7 @@ __device__ __forceinline__ void drop_page(const PoolGeom& g, const PageWs& w, in
 // a warp per stream
 __global__ void __launch_bounds__(256) free_kernel(PoolGeom g, PageTab t, const int32_t* drop, int drop_all,
                                                   int32_t* status, PageWs w) {
+  griddep_launch();
   griddep_wait();
   const int s = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
   if (s == 0 && lane == 0) w.head[0] = *g.nfree;
@@ -254,6 +253,7 @@ __global__ void __launch_bounds__(256) free_kernel(PoolGeom g, PageTab t, const 
 // zero is the last whatever the order); the others write the children's rows.
 __global__ void __launch_bounds__(256) fork_kernel(PoolGeom g, PageTab t, const int32_t* parent, PageTab out,
                                                   int32_t* status, PageWs w) {
+  griddep_launch();
   griddep_wait();
   const int i = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
   if (i == 0 && lane == 0) w.head[0] = *g.nfree;
@@ -301,52 +301,200 @@ __global__ void __launch_bounds__(256) fork_kernel(PoolGeom g, PageTab t, const 
   }
 }
 
-// The marked pages join the free list in the order of their numbers. Each CTA counts the marks before
-// its words itself (the bitmap is small and in L2), so no CTA waits for another.
-__global__ void __launch_bounds__(kPushThreads) push_kernel(PoolGeom g, PageWs w) {
-  __shared__ int sm[8];
-  griddep_wait();
-  const int words = (g.npages + 31) / 32, w0 = blockIdx.x * kPushWords;
-  int c = 0;
-  const uint4* g4 = reinterpret_cast<const uint4*>(w.gone);
-  for (int i = threadIdx.x; i < w0 / 4; i += kPushThreads) {
-    const uint4 v = g4[i];
-    c += __popc(v.x) + __popc(v.y) + __popc(v.z) + __popc(v.w);
-  }
-  const int base = block_sum(c, sm);
-  // this CTA's words, four neighbours a thread
-  uint32_t m[4];
-  int mine = 0;
-#pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int i = w0 + 4 * threadIdx.x + u;
-    m[u] = i < words ? w.gone[i] : 0u;
-    mine += __popc(m[u]);
-  }
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int incl = mine;
+// The marks of 32 words (one a lane), whose numbers start at word w0, to the free list from `at` on: a
+// word at a time, its pages by the lanes whose bits are set, so that a run of pages is one store.
+__device__ __forceinline__ void push_words(const PoolGeom& g, uint32_t m, int w0, int at) {
+  const int lane = threadIdx.x & 31;
+  int incl = __popc(m);
+  const int mine = incl;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_up_sync(kFull, incl, o);
     if (lane >= o) incl += v;
   }
-  __syncthreads();
-  if (lane == 31) sm[warp] = incl;
-  __syncthreads();
-  int at = base + incl - mine, all = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (i < warp) at += sm[i];
-    all += sm[i];
+  at += incl - mine;
+  for (unsigned any = __ballot_sync(kFull, m != 0); any; any &= any - 1) {
+    const int j = __ffs(any) - 1;
+    const uint32_t x = __shfl_sync(kFull, m, j);
+    const int to = __shfl_sync(kFull, at, j) + __popc(x & ((1u << lane) - 1));
+    if ((x >> lane & 1) && to >= 0 && to < g.npages) g.free_list[to] = (w0 + j) * 32 + lane;
   }
-  const int nfree = w.head[0] - (w.head[2] ? 0 : w.head[1]);  // what the call took is off the list's end
+}
+
+// The marked pages join the free list in the order of their numbers. Each CTA counts the marks before
+// its words itself (the bitmap is small and in L2), so no CTA waits for another.
+__global__ void __launch_bounds__(kPushThreads) push_kernel(PoolGeom g, PageWs w) {
+  __shared__ int sm[8];
+  griddep_launch();
+  griddep_wait();
+  const int words = (g.npages + 31) / 32, w0 = blockIdx.x * kPushWords;
+  const int i = w0 + threadIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t m = i < words ? w.gone[i] : 0u;
+  const int nfree = w.head[0] - max(w.head[1], 0);  // what the call took is off the list's end
+  int c = 0;
+  const uint4* g4 = reinterpret_cast<const uint4*>(w.gone);
+#pragma unroll 4
+  for (int k = threadIdx.x; k < w0 / 4; k += kPushThreads) {
+    const uint4 v = g4[k];
+    c += __popc(v.x) + __popc(v.y) + __popc(v.z) + __popc(v.w);
+  }
+  const int base = block_sum(c, sm);
+  const int in_warp = warp_sum_i(__popc(m));
+  __syncthreads();
+  if (lane == 0) sm[warp] = in_warp;
+  __syncthreads();
+  int at = nfree + base, all = 0;
 #pragma unroll
-  for (int u = 0; u < 4; ++u)
-    for (uint32_t v = m[u]; v; v &= v - 1) {
-      const int to = nfree + at++;
-      if (to >= 0 && to < g.npages) g.free_list[to] = (w0 + 4 * threadIdx.x + u) * 32 + __ffs(v) - 1;
-    }
+  for (int k = 0; k < 8; ++k) {
+    if (k < warp) at += sm[k];
+    all += sm[k];
+  }
+  push_words(g, m, i - lane, at);
   if (w0 + kPushWords >= words && threadIdx.x == 0) *g.nfree = nfree + base + all;
+}
+
+// ---- frees and forks in one launch ----------------------------------------------------------------
+// One cluster of eight CTAs does the counting, and its barrier stands where the wide form starts the
+// next kernel (zeroed bitmap | counts | free list and lengths): three launches' overhead becomes one.
+// Eight SMs suffice for the page entries of ordinary tables; the wide form takes over beyond
+// kOneEntries entries, kOnePages pages or kOneSeqs sequences.
+constexpr int kOneCtas = 8, kOneThreads = 1024;
+constexpr long long kOneEntries = 1 << 14;
+constexpr int kOnePages = 1 << 20, kOneSeqs = 1024;
+
+// The marked pages join the free list: CTA r takes the r-th eighth of the bitmap's words.
+__device__ __forceinline__ void cluster_push(cg::cluster_group& cl, const PoolGeom& g, const PageWs& w, int nfree) {
+  __shared__ int sm[kOneThreads / 32], sm_total;
+  const int rank = cl.block_rank(), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int words = (g.npages + 31) / 32, per = (words + kOneCtas - 1) / kOneCtas;
+  const int w0 = min(words, rank * per), w1 = min(words, w0 + per);
+  int c = 0;
+  for (int i = w0 + threadIdx.x; i < w1; i += kOneThreads) c += __popc(__ldcg(&w.gone[i]));
+  c = warp_sum_i(c);
+  if (lane == 0) sm[warp] = c;
+  __syncthreads();
+  if (warp == 0) {
+    c = warp_sum_i(sm[lane]);
+    if (lane == 0) sm_total = c;
+  }
+  cl.sync();
+  int base = 0, all = 0;
+  for (int r = 0; r < kOneCtas; ++r) {
+    const int v = *cl.map_shared_rank(&sm_total, r);
+    if (r < rank) base += v;
+    all += v;
+  }
+  for (int i0 = w0; i0 < w1; i0 += kOneThreads) {
+    const int i = i0 + threadIdx.x;
+    const uint32_t m = i < w1 ? __ldcg(&w.gone[i]) : 0u;
+    const int in_warp = warp_sum_i(__popc(m));
+    __syncthreads();
+    if (lane == 0) sm[warp] = in_warp;
+    __syncthreads();
+    const int v = sm[lane];
+    push_words(g, m, i - lane, nfree + base + warp_sum_i(lane < warp ? v : 0));
+    base += warp_sum_i(v);
+  }
+  if (rank == 0 && threadIdx.x == 0) *g.nfree = nfree + all;
+  cl.sync();  // no CTA leaves while another reads its shared memory
+}
+
+__device__ __forceinline__ void cluster_zero(const PoolGeom& g, const PageWs& w, int at) {
+  const int words = (g.npages + 31) / 32;
+  for (int i = at; i < words; i += kOneCtas * kOneThreads) w.gone[i] = 0u;
+}
+
+__global__ void __cluster_dims__(kOneCtas, 1, 1) __launch_bounds__(kOneThreads)
+    free_one_kernel(PoolGeom g, PageTab t, const int32_t* drop, int drop_all, int32_t* status, PageWs w) {
+  griddep_launch();
+  griddep_wait();
+  cg::cluster_group cl = cg::this_cluster();
+  const int at = cl.block_rank() * kOneThreads + threadIdx.x, step = kOneCtas * kOneThreads;
+  const int nfree = *g.nfree;
+  const long long cap = (long long)t.maxp << g.lp;
+  cluster_zero(g, w, at);
+  cl.sync();
+  const int entries = t.S * t.maxp;
+#pragma unroll 4
+  for (int e = at; e < entries; e += step) {
+    const int s = e / t.maxp, i = e - s * t.maxp;
+    const int d = drop ? drop[s / t.Hkv % t.B] : drop_all, n = t.len[s], p = t.table[e];
+    if (d < 0 || n < 0 || n > cap) {
+      if (i == 0) status_or(status, d < 0 ? KVC_STATUS_BAD_INDEX : KVC_STATUS_BAD_PAGE);
+      continue;
+    }
+    if (i >= pages_of(n > d ? n - d : 0, g.lp) && i < pages_of(n, g.lp)) {
+      drop_page(g, w, p, status);
+      t.table[e] = -1;
+    }
+  }
+  cl.sync();
+  for (int s = at; s < t.S; s += step) {
+    const int d = drop ? drop[s / t.Hkv % t.B] : drop_all, n = t.len[s];
+    if (d > 0 && n >= 0 && n <= cap) t.len[s] = n > d ? n - d : 0;
+  }
+  cluster_push(cl, g, w, nfree);
+}
+
+__global__ void __cluster_dims__(kOneCtas, 1, 1) __launch_bounds__(kOneThreads)
+    fork_one_kernel(PoolGeom g, PageTab t, const int32_t* parent, PageTab out, int32_t* status, PageWs w) {
+  __shared__ int kids[kOneSeqs];
+  griddep_launch();
+  griddep_wait();
+  cg::cluster_group cl = cg::this_cluster();
+  const int at = cl.block_rank() * kOneThreads + threadIdx.x, step = kOneCtas * kOneThreads;
+  const int nfree = *g.nfree;
+  const long long cap = (long long)t.maxp << g.lp;
+  cluster_zero(g, w, at);
+  for (int b = threadIdx.x; b < t.B; b += kOneThreads) kids[b] = 0;
+  __syncthreads();
+  for (int c = threadIdx.x; c < out.B; c += kOneThreads) {
+    const int b = parent[c];
+    if (b >= 0 && b < t.B)
+      atomicAdd(&kids[b], 1);
+    else if (b != -1)
+      status_or(status, KVC_STATUS_BAD_INDEX);
+  }
+  cl.sync();
+  const int entries = t.S * t.maxp;
+#pragma unroll 4
+  for (int e = at; e < entries; e += step) {
+    const int s = e / t.maxp, i = e - s * t.maxp;
+    const int n = t.len[s], p = t.table[e], delta = kids[s / t.Hkv % t.B] - 1;
+    if (n < 0 || n > cap) {
+      if (i == 0) status_or(status, KVC_STATUS_BAD_PAGE);
+      continue;
+    }
+    if (i >= pages_of(n, g.lp) || delta == 0) continue;
+    if (delta < 0)
+      drop_page(g, w, p, status);
+    else if (page_ok(g, p))
+      atomicAdd(&g.refs[p], delta);
+    else
+      status_or(status, KVC_STATUS_BAD_PAGE);
+  }
+  const int oentries = out.S * t.maxp;
+#pragma unroll 4
+  for (int e = at; e < oentries; e += step) {
+    const int c = e / t.maxp, i = e - c * t.maxp;
+    const int b = parent[c / t.Hkv % out.B];
+    int n = 0, p = -1;
+    if (b >= 0 && b < t.B) {
+      const int s = (c / (t.Hkv * out.B) * t.B + b) * t.Hkv + c % t.Hkv;
+      n = t.len[s];
+      if (n < 0 || n > cap) n = 0;
+      p = t.table[(size_t)s * t.maxp + i];
+    }
+    out.table[e] = i < pages_of(n, g.lp) ? p : -1;
+    if (i == 0) out.len[c] = n;
+  }
+  cl.sync();
+  cluster_push(cl, g, w, nfree);
+}
+
+bool one_fits(const PoolGeom& g, const PageTab& t, const PageTab& o) {
+  return g.npages <= kOnePages && (long long)t.S * t.maxp <= kOneEntries && (long long)o.S * o.maxp <= kOneEntries &&
+         t.B <= kOneSeqs && o.B <= kOneSeqs;
 }
 
 int push_grid(const PoolGeom& g) { return ((g.npages + 31) / 32 + kPushWords - 1) / kPushWords; }
@@ -383,6 +531,11 @@ int launch_page_extend(const PoolGeom& g, const PageTab& t, const int32_t* add, 
 
 int launch_page_free(const PoolGeom& g, const PageTab& t, const int32_t* drop, int drop_all, int32_t* status,
                      const PageWs& w, cudaStream_t s) {
+  if (one_fits(g, t, t))
+    return launch_pdl(free_one_kernel, dim3(kOneCtas), dim3(kOneThreads), 0, s, false, g, t, drop, drop_all, status,
+                      w) == cudaSuccess
+               ? KVC_OK
+               : KVC_ERR_LAUNCH;
   if (cudaMemsetAsync(w.head, 0, w.zero_bytes, s) != cudaSuccess) return KVC_ERR_LAUNCH;
   if (launch_pdl(free_kernel, dim3((t.S + 7) / 8), dim3(256), 0, s, false, g, t, drop, drop_all, status, w) !=
       cudaSuccess)
@@ -392,6 +545,11 @@ int launch_page_free(const PoolGeom& g, const PageTab& t, const int32_t* drop, i
 
 int launch_page_fork(const PoolGeom& g, const PageTab& t, const int32_t* parent, const PageTab& out, int32_t* status,
                      const PageWs& w, cudaStream_t s) {
+  if (one_fits(g, t, out))
+    return launch_pdl(fork_one_kernel, dim3(kOneCtas), dim3(kOneThreads), 0, s, false, g, t, parent, out, status, w) ==
+                   cudaSuccess
+               ? KVC_OK
+               : KVC_ERR_LAUNCH;
   if (cudaMemsetAsync(w.head, 0, w.zero_bytes, s) != cudaSuccess) return KVC_ERR_LAUNCH;
   if (launch_pdl(fork_kernel, dim3((t.S + out.S + 7) / 8), dim3(256), 0, s, false, g, t, parent, out, status, w) !=
       cudaSuccess)

@@ -345,7 +345,7 @@ def _ints(t: Optional[torch.Tensor], shape, dev, what: str, dtype=torch.int32):
     """The pointer of a contiguous tensor of the given shape and type on the pool's device, or None."""
     if t is None:
         return None
-    if t.dtype != dtype or t.device != dev or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}")
     return t.data_ptr()
 
@@ -390,6 +390,7 @@ class Pages:
         self.table, self.len, self.device = table, len, dev
         self.c = kvc_pages(L=L, B=B, Hkv=Hkv, maxp=maxp, table=_ints(table, (L, B, Hkv, maxp), dev, "table"),
                            len=_ints(len, (L, B, Hkv), dev, "len"))
+        self.shape = (L, B, Hkv)
         self.ref = C.byref(self.c)
 
     @classmethod
@@ -400,34 +401,30 @@ class Pages:
     def layer(self, l: int) -> "Pages":
         return Pages(self.table[l:l + 1], self.len[l:l + 1])
 
-    @property
-    def shape(self):
-        return self.c.L, self.c.B, self.c.Hkv
-
 
 def _page_call(name: str, pool: Pool, pages: Optional[Pages], stream, args):
     """One entry point on the pool's device: ``args`` follow the pool and the pages, the stream comes last."""
-    if pages is not None and pages.device != pool.device:
+    dev = pool.device
+    if pages is not None and pages.device != dev:
         raise ValueError("the pool and its pages are on different devices")
+    stream = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream(stream)
     f = getattr(_lib or lib(), name)
-    cur = torch.cuda.current_device()
-    if pool.device.index == cur:
-        if stream is None:
-            stream = torch.cuda.current_stream(pool.device)
-        rc = f(pool.ref, None if pages is None else pages.ref, *args, _stream(stream))
+    if dev.index == torch.cuda.current_device():
+        rc = f(pool.ref, None if pages is None else pages.ref, *args, stream)
     else:
-        with torch.cuda.device(pool.device):
-            rc = f(pool.ref, None if pages is None else pages.ref, *args, _stream(stream))
-    _check(rc)
+        with torch.cuda.device(dev):
+            rc = f(pool.ref, None if pages is None else pages.ref, *args, stream)
+    if rc:
+        _check(rc)
 
 
-def _page_ws(nbytes: int, pool: Pool, workspace):
-    """(pointer, bytes, tensor) of the caller's workspace, or of one made for this call."""
+def _page_ws(nbytes, pool: Pool, workspace):
+    """(pointer, bytes, tensor) of the caller's workspace, or of one of nbytes() made for this call."""
     if workspace is None:
-        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=pool.device)
+        workspace = torch.empty(max(nbytes(), 256), dtype=torch.uint8, device=pool.device)
     elif workspace.device != pool.device or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous and on the pool's device")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    return workspace.data_ptr(), workspace.nbytes, workspace
 
 
 def _word(status, pool: Pool):
@@ -453,18 +450,18 @@ def kvc_page_extend(pool: Pool, pages: Pages, add: Optional[torch.Tensor] = None
     """Room for ``add`` [B] (or ``add_all``) more tokens in every stream; ``start`` [L, B, Hkv] receives the
     old lengths (see kvc.h)."""
     dev = pool.device
-    wp, wb, ws = _page_ws(0 if workspace is not None else kvc_page_workspace_size(pool, pages), pool, workspace)
+    wp, wb, ws = _page_ws(lambda: kvc_page_workspace_size(pool, pages), pool, workspace)
     _page_call("kvc_page_extend", pool, pages, stream,
-               (_ints(add, (pages.c.B,), dev, "add"), int(add_all), _ints(start, pages.shape, dev, "start"),
+               (_ints(add, (pages.shape[1],), dev, "add"), int(add_all), _ints(start, pages.shape, dev, "start"),
                 _word(status, pool), wp, wb))
 
 
 def kvc_page_free(pool: Pool, pages: Pages, drop: Optional[torch.Tensor] = None, drop_all: int = 0,
                   status: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
     """The last ``drop`` [B] (or ``drop_all``) tokens of every stream go, with the pages they leave empty."""
-    wp, wb, ws = _page_ws(0 if workspace is not None else kvc_page_workspace_size(pool, pages), pool, workspace)
+    wp, wb, ws = _page_ws(lambda: kvc_page_workspace_size(pool, pages), pool, workspace)
     _page_call("kvc_page_free", pool, pages, stream,
-               (_ints(drop, (pages.c.B,), pool.device, "drop"), int(drop_all), _word(status, pool), wp, wb))
+               (_ints(drop, (pages.shape[1],), pool.device, "drop"), int(drop_all), _word(status, pool), wp, wb))
 
 
 def kvc_page_fork(pool: Pool, pages: Pages, parent: torch.Tensor, out: Pages, status: Optional[torch.Tensor] = None,
@@ -472,9 +469,9 @@ def kvc_page_fork(pool: Pool, pages: Pages, parent: torch.Tensor, out: Pages, st
     """``out``'s sequence c becomes a copy of ``pages``' sequence ``parent[c]``; ``pages`` is given up."""
     if out.device != pool.device:
         raise ValueError("the pool and its pages are on different devices")
-    wp, wb, ws = _page_ws(0 if workspace is not None else kvc_page_workspace_size(pool, pages), pool, workspace)
+    wp, wb, ws = _page_ws(lambda: kvc_page_workspace_size(pool, pages), pool, workspace)
     _page_call("kvc_page_fork", pool, pages, stream,
-               (_ints(parent, (out.c.B,), pool.device, "parent"), out.ref, _word(status, pool), wp, wb))
+               (_ints(parent, (out.shape[1],), pool.device, "parent"), out.ref, _word(status, pool), wp, wb))
 
 
 def kvc_page_compact(pool: Pool, pages: Pages, kept_idx: torch.Tensor, kept_len: torch.Tensor,
@@ -482,20 +479,23 @@ def kvc_page_compact(pool: Pool, pages: Pages, kept_idx: torch.Tensor, kept_len:
     """The kept tokens to every stream's front: lists per stream ([L, B, Hkv, n] and [L, B, Hkv], as
     kvc_select's) or per sequence ([B, n] and [B], as kvc_epikv_evict's)."""
     per_seq = kept_idx.dim() == 2
-    lead = (pages.c.B,) if per_seq else pages.shape
-    wp, wb, ws = _page_ws(0 if workspace is not None else kvc_page_workspace_size(pool, pages), pool, workspace)
+    lead = (pages.shape[1],) if per_seq else pages.shape
+    wp, wb, ws = _page_ws(lambda: kvc_page_workspace_size(pool, pages), pool, workspace)
     _page_call("kvc_page_compact", pool, pages, stream,
                (_ints(kept_idx, lead + (kept_idx.shape[-1],), pool.device, "kept_idx"),
                 _ints(kept_len, lead, pool.device, "kept_len"), kept_idx.shape[-1], int(per_seq), _word(status, pool),
                 wp, wb))
 
 
+_Strides = C.c_int64 * 3
+
+
 def _rows(x: torch.Tensor, shape, pool: Pool, what: str):
     """The pointer and strides of [B, T, heads, D] rows with contiguous channels."""
-    if x.device != pool.device or tuple(x.shape) != tuple(shape) or x.stride(3) != 1:
-        raise ValueError(f"{what} must be a {tuple(shape)} tensor on {pool.device} with contiguous channels")
     s = x.stride()
-    return x.data_ptr(), (C.c_int64 * 3)(s[0], s[1], s[2])
+    if x.device != pool.device or x.shape != shape or s[3] != 1:
+        raise ValueError(f"{what} must be a {tuple(shape)} tensor on {pool.device} with contiguous channels")
+    return x.data_ptr(), _Strides(s[0], s[1], s[2])
 
 
 def kvc_page_store(pool: Pool, pages: Pages, k: torch.Tensor, v: torch.Tensor, start: torch.Tensor,
@@ -538,13 +538,12 @@ def kvc_page_attend(pool: Pool, pages: Pages, q: torch.Tensor, out: torch.Tensor
                     status: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
     """Attention of ``q`` [B, T, Hq, D] (strided like kvc_page_store's rows), the newest T tokens' queries, over
     one layer of the cache; ``out`` [B, T, Hq, D], ``lse`` [B, T, Hq] fp32; ``scale`` defaults to 1/sqrt(D)."""
-    B = pages.c.B
+    B = pages.shape[1]
     if q.dim() != 4:
         raise ValueError("q must be a [B, T, Hq, D] tensor")
     _, T, Hq, D = q.shape
     qp, qs = _rows(q, (B, T, Hq, pool.D), pool, "q")
-    wp, wb, ws = _page_ws(0 if workspace is not None else kvc_page_attend_workspace_size(pool, pages, Hq, T), pool,
-                          workspace)
+    wp, wb, ws = _page_ws(lambda: kvc_page_attend_workspace_size(pool, pages, Hq, T), pool, workspace)
     _page_call("kvc_page_attend", pool, pages, stream,
                (_dtype_code(q), Hq, T, qp, qs, _ints(n_q, (B,), pool.device, "n_q"),
                 float(D ** -0.5 if scale is None else scale), _ints(out, q.shape, pool.device, "out", q.dtype),

@@ -19,23 +19,25 @@ E4M3 = e4m3_values()
 
 
 def quantise(x, ts):
-    """Rows [..., D] (float64 holding the inputs) -> codes [..., D/2], scale bytes [..., D/16]."""
+    """Rows [..., D] (float64 holding the inputs) -> codes [..., D/2], scale bytes [..., D/16]. The tensor scale, six
+    times it and a group's step are fp32 numbers; the quotients by them are exact."""
+    ts = np.float32(ts)
     x = np.asarray(x, np.float64)
     g = x.reshape(x.shape[:-1] + (-1, 16))
     a = np.abs(g)
     with np.errstate(invalid="ignore"):
         amax = np.where(np.isnan(a), 0.0, a).max(-1)
-        want = np.clip(amax / (6.0 * ts), 2.0 ** -9, 448.0)
+        want = np.clip(amax / np.float64(np.float32(6) * ts), 2.0 ** -9, 448.0)
         pos = E4M3[:127]  # ascending, 0 .. 448
         hi = np.clip(np.searchsorted(pos, want), 1, 126)
         lo = hi - 1
         dl, dh = want - pos[lo], pos[hi] - want
         sb = np.where((dl < dh) | ((dl == dh) & (lo % 2 == 0)), lo, hi).astype(np.uint8)
-        y = a / (E4M3[sb].astype(np.float32) * np.float32(ts)).astype(np.float64)[..., None]
+        y = a / (E4M3[sb].astype(np.float32) * ts).astype(np.float64)[..., None]
         code = np.zeros(g.shape, np.uint8)
         for k, border in enumerate((0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0)):
             code += ((y > border) if k % 2 == 0 else (y >= border)).astype(np.uint8)
-        code += np.where(g < 0, 8, 0).astype(np.uint8)
+        code += np.where(np.signbit(g) & ~np.isnan(g), 8, 0).astype(np.uint8)
     code = code.reshape(x.shape)
     return code[..., 0::2] | (code[..., 1::2] << 4), sb
 

@@ -93,6 +93,8 @@ def rand_rows(shape, dt, seed):
 @pytest.mark.parametrize("dt,D,page,T,scales", [
     ("bf16", 128, 64, 1, (1.0, 1.0)), ("bf16", 128, 16, 37, (0.5, 2.0)), ("bf16", 64, 32, 130, (1.0, 0.25)),
     ("f32", 128, 256, 300, (1.0, 1.0)), ("f32", 64, 16, 16, (0.125, 1.0)), ("bf16", 128, 128, 1000, (1.0, 1.0)),
+    ("bf16", 128, 64, 8000, (1.0, 2.0)), ("f32", 64, 64, 13100, (1.0, 1.0)),  # several rows a thread
+    ("bf16", 64, 64, 13100, (0.7, 1.0)),                                      # a tensor scale that is no power of two
 ])
 def test_store_and_read_match_bit_for_bit(dt, D, page, T, scales):
     B, Hkv = 3, 2
@@ -120,8 +122,9 @@ def test_store_and_read_match_bit_for_bit(dt, D, page, T, scales):
             for j, o in enumerate((ko, vo)):
                 want = torch.full((T + 61, D), -77.0, dtype=torch.float64)
                 rows = R.rows(x.p, x.t, s, j)[f:f + count]
-                want[:len(rows)] = torch.from_numpy(rows)
-                # values of at most 6 bits times a power of two: exact in both types
+                # the code times its fp32 step in fp32, then the type's rounding (no rounding at all where the
+                # tensor scale is a power of two: at most six bits)
+                want[:len(rows)] = torch.from_numpy(rows).float().to(DT[dt]).double()
                 assert torch.equal(o[s].double().cpu(), want), (s, j)
     x.check("read")
 
@@ -179,6 +182,7 @@ def random_lists(rng, t, shrink):
 @pytest.mark.parametrize("seed,D,page,L,B,Hkv,maxp,npages", [
     (0, 64, 16, 1, 2, 1, 8, 40), (1, 128, 64, 2, 3, 2, 5, 90), (2, 64, 32, 3, 5, 7, 6, 700),
     (3, 128, 16, 1, 9, 33, 4, 1500), (4, 64, 16, 2, 40, 4, 9, 2600), (5, 128, 256, 1, 4, 2, 2, 30),
+    (6, 64, 16, 1, 1030, 1, 3, 2500),  # more sequences than the one-launch forms take
 ])
 def test_random_sequences_of_page_operators(seed, D, page, L, B, Hkv, maxp, npages):
     """Extensions, forks, frees, evictions and stores in random order, the pool often nearly exhausted: tables,
