@@ -43,6 +43,7 @@ struct Plan {
   int grid;    // CTAs of the main kernel
   float* part;  // [grid][2][rb][D]
   float2* ml;   // [grid][2][rb] (reference, sum)
+  int2* span;   // [nvs] first and last CTA of a stream's units (streams with units only)
 };
 
 struct Stream {  // what a (stream, row block) has to see
@@ -95,7 +96,16 @@ __device__ __forceinline__ int scan_units(const AttendArgs& a, const Plan& p, in
   return base + incl - mine;
 }
 
-__device__ __forceinline__ int cta_first(int W, int i, int grid) { return (int)((long long)W * i / grid); }
+// CTA i of `grid` takes units [first(i), first(i + 1)) of W: the first W % grid CTAs one more than the others.
+struct Split {
+  int q, rem;
+  __device__ __forceinline__ Split(int W, int grid) : q(W / grid), rem(W % grid) {}
+  __device__ __forceinline__ int first(int i) const { return i * q + min(i, rem); }
+  __device__ __forceinline__ int owner(int u) const {
+    const int big = rem * (q + 1);
+    return u < big ? u / (q + 1) : rem + (u - big) / q;
+  }
+};
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
@@ -156,14 +166,14 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
     for (int i = 0; i < kStages; ++i) tc::mbar_init(&bars[warp][i], 1);
     tc::mbar_fence_init();
   }
-  griddep_launch();  // the combine kernel's CTAs wait beside this wave
   griddep_wait();
 
   // this CTA's units, and the stream its first one lies in
   const int per = (p.nvs + 32 * kWarps - 1) / (32 * kWarps);
   int W;
   int before = scan_units<32 * kWarps>(a, p, sm_scan, per, &W);
-  const int w0 = cta_first(W, blockIdx.x, p.grid), w1 = cta_first(W, blockIdx.x + 1, p.grid);
+  const Split split(W, p.grid);
+  const int w0 = split.first(blockIdx.x), w1 = split.first(blockIdx.x + 1);
   if (w0 >= w1) return;
   for (int i = 0; i < per; ++i) {
     const int vs = threadIdx.x * per + i;
@@ -177,14 +187,15 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
   }
   __syncthreads();
   int vs = sm_first[0];
-  int ua = w0 - sm_first[1];  // first unit of this CTA in the stream
+  int base = sm_first[1];     // units before the stream
+  int ua = w0 - base;         // first unit of this CTA in the stream
   int left = w1 - w0;
   uint32_t n = 0;  // chunks this warp has waited for
   bool alive = true;
 
-  for (; left > 0; ++vs, ua = 0) {
+  for (int U; left > 0; ++vs, ua = 0, base += U) {
     const Stream x = stream_of(a, p, vs, true);
-    const int U = units_of(x);
+    U = units_of(x);
     if (U == 0) continue;
     const int ub = min(U, ua + left);
     left -= ub - ua;
@@ -192,41 +203,38 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
     const int c0 = 2 * ua + warp;
     const int mine = c1 > c0 ? (c1 - c0 + kWarps - 1) / kWarps : 0;
     const int32_t* row = a.t.table + (size_t)x.s * a.t.maxp;
-    const int last = pages_of(x.len, a.g.lp) - 1;
 
-    // page numbers of this warp's next 32 chunks, one a lane (two where a page is half a chunk)
-    int ids[2];
-    auto load_ids = [&](int i) {
+    // Where this warp's next 32 chunks lie, one a lane (two blocks apart where a page is half a chunk): the
+    // lane that knows a chunk's place issues its copy.
+    const uint8_t* src[2];
+    auto locate = [&](int i) {
       const int tok = (c0 + kWarps * (i + lane)) * kChunk32;
       const int q0 = tok >> a.g.lp, q1 = (tok + 16) >> a.g.lp;
-      ids[0] = q0 <= last ? row[q0] : -1;
-      ids[1] = a.g.lp > 4 ? ids[0] : q1 <= last ? row[q1] : -1;
+      const bool want = i + lane < mine, want1 = want && tok + 16 < x.vis;
+      const int id0 = want ? row[q0] : 0;
+      const int id1 = a.g.lp > 4 || !want1 ? id0 : row[q1];
+      const int blk = (tok & ((1 << a.g.lp) - 1)) >> 4;
+      src[0] = page_ok(a.g, id0) ? block_of(a.g, id0, blk) : nullptr;
+      src[1] = want1 && page_ok(a.g, id1) ? (a.g.lp > 4 ? src[0] + blk_bytes(D) : block_of(a.g, id1, 0)) : nullptr;
+      if (want && (!src[0] || (want1 && !src[1]))) status_or(a.status, KVC_STATUS_BAD_PAGE);
     };
-    auto issue = [&](int i) {  // chunk i of this warp into its stage
-      if ((i & 31) == 0) load_ids(i);
-      const int id0 = __shfl_sync(kFull, ids[0], i & 31), id1 = __shfl_sync(kFull, ids[1], i & 31);
-      if (lane == 0) {
-        const int st = (n + i) % kStages;  // n: chunks waited for before this stream's part
+    auto issue = [&](int i, int st) {  // chunk i of this warp into stage st
+      if ((i & 31) == 0) locate(i);
+      if (lane == (i & 31)) {
         uint8_t* dst = ring + st * SM::kStage;
         uint64_t* bar = &bars[warp][st];
-        const int tok = (c0 + kWarps * i) * kChunk32;
-        const bool ok0 = page_ok(a.g, id0), ok1 = page_ok(a.g, id1);
-        const bool in1 = tok + 16 < x.vis;  // the second block is needed
-        const uint32_t nb = (ok0 ? 1 : 0) + (ok1 && in1 ? 1 : 0);
-        oks[warp][st] = (ok0 ? 1u : 0u) | (ok1 ? 2u : 0u);
-        if (!ok0 || (in1 && !ok1)) status_or(a.status, KVC_STATUS_BAD_PAGE);
-        tc::mbar_expect_tx(bar, nb * blk_bytes(D));
-        const int blk = (tok & ((1 << a.g.lp) - 1)) >> 4;
-        if (a.g.lp > 4) {
-          if (nb) bulk_load(dst, block_of(a.g, id0, blk), nb * blk_bytes(D), bar);
+        oks[warp][st] = (src[0] ? 1u : 0u) | (src[1] ? 2u : 0u);
+        if (src[1] == src[0] + blk_bytes(D)) {
+          tc::mbar_expect_tx(bar, 2 * blk_bytes(D));
+          bulk_load(dst, src[0], 2 * blk_bytes(D), bar);
         } else {
-          if (ok0) bulk_load(dst, block_of(a.g, id0, 0), blk_bytes(D), bar);
-          if (ok1 && in1) bulk_load(dst + blk_bytes(D), block_of(a.g, id1, 0), blk_bytes(D), bar);
+          tc::mbar_expect_tx(bar, (src[0] ? blk_bytes(D) : 0) + (src[1] ? blk_bytes(D) : 0));
+          if (src[0]) bulk_load(dst, src[0], blk_bytes(D), bar);
+          if (src[1]) bulk_load(dst + blk_bytes(D), src[1], blk_bytes(D), bar);
         }
       }
     };
-    const uint32_t nbase = n;
-    for (int i = 0; i < kStages && i < mine && alive; ++i) issue(i);
+    for (int i = 0; i < kStages && i < mine && alive; ++i) issue(i, (n + i) % kStages);
 
     // the query rows as B fragments: k step i, k = 2t,2t+1 -> channels CPL t + 4 i + 0,1 and
     // k = 2t+8,2t+9 -> + 2,3. Each row is brought to [256, 512) by a power of two, which makes bf16
@@ -472,13 +480,7 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
         }
       }
       __syncwarp();  // every lane is done with the stage
-      if (i + kStages < mine) {
-        // the stage index in issue() counts from this part's first chunk
-        const uint32_t keep = n;
-        n = nbase;
-        issue(i + kStages);
-        n = keep;
-      }
+      if (i + kStages < mine) issue(i + kStages, st);
     }
 
     // a row's sum over the eight lanes that hold its tokens
@@ -536,6 +538,8 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
     }
     if (warp == 0) {
       const bool whole = ua == 0 && ub == U;
+      // who holds the stream's parts, for the combine kernel
+      if (ua == 0 && lane == 0) p.span[vs] = make_int2(blockIdx.x, whole ? (int)blockIdx.x : split.owner(base + U - 1));
       const size_t slot = (size_t)blockIdx.x * 2 + (ua == 0 ? 1 : 0);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -567,51 +571,33 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
 }
 
 // Rows whose stream several CTAs shared, and rows of streams without tokens: a CTA per (stream, row
-// block, row), its warps taking every fourth part.
-constexpr int kCombThreads = 128;
+// block, row), its warps taking every fourth part, four at a time.
+constexpr int kCombThreads = 128, kCombWarps = kCombThreads / 32;
 template <typename T, int D>
 __global__ void __launch_bounds__(kCombThreads) combine_kernel(AttendArgs a, Plan p) {
-  __shared__ int sm_scan[kCombThreads / 32], sm_before;
-  __shared__ float sm_o[kCombThreads / 32][D];
-  __shared__ float2 sm_ml[kCombThreads / 32];
+  __shared__ float sm_o[kCombWarps][D];
+  __shared__ float2 sm_ml[kCombWarps];
   griddep_launch();
   griddep_wait();
   const int vs = blockIdx.x / p.rb, rr = blockIdx.x % p.rb;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per = (p.nvs + kCombThreads - 1) / kCombThreads;
-  int W;
-  int before = scan_units<kCombThreads>(a, p, sm_scan, per, &W);
-  if (vs / per == (int)threadIdx.x) {
-    for (int i = threadIdx.x * per; i < vs; ++i) before += units_of(stream_of(a, p, i, false));
-    sm_before = before;
-  }
-  __syncthreads();
-  before = sm_before;
+  const int2 span = p.span[vs];  // read beside the length; undefined for a stream without units
   const Stream x = stream_of(a, p, vs, threadIdx.x == 0 && rr == 0);
   if (rr >= x.rows) return;
-  const int U = units_of(x);
   const int r = x.r0 + rr;
   const size_t at = ((size_t)x.b * a.T + r / p.G) * a.Hq + x.h * p.G + r % p.G;
   T* op = static_cast<T*>(a.out) + at * D;
-  if (U == 0) {
+  if (x.vis == 0) {
     for (int i = threadIdx.x; i < D; i += kCombThreads) op[i] = from_f32<T>(0.f);
     if (a.lse && threadIdx.x == 0) a.lse[at] = -INFINITY;
     return;
   }
-  // the CTAs that hold units [before, before + U)
-  auto owner = [&](int u) {
-    int c = (int)(((long long)u * p.grid) / W);
-    while (c > 0 && cta_first(W, c, p.grid) > u) --c;
-    while (cta_first(W, c + 1, p.grid) <= u) ++c;
-    return c;
-  };
-  const int ca = owner(before), cb = owner(before + U - 1);
-  if (ca == cb) return;  // written by that CTA
-  constexpr int E = D / 32;
+  if (span.x == span.y) return;  // written by that CTA
+  constexpr int E = D / 32, N = 4;
   float o[E], l = 0.f, m = -INFINITY;
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-  auto add = [&](float y_m, float y_l, const float (&y)[E]) {
+  auto add = [&](float y_m, float y_l, const float* y) {
     if (y_l == 0.f) return;
     const float to = l == 0.f ? y_m : fmaxf(m, y_m);
     const float c0 = l == 0.f ? 0.f : ex2(m - to), c1 = ex2(y_m - to);
@@ -620,28 +606,36 @@ __global__ void __launch_bounds__(kCombThreads) combine_kernel(AttendArgs a, Pla
     for (int e = 0; e < E; ++e) o[e] = o[e] * c0 + y[e] * c1;
     m = to;
   };
-  for (int c = ca + warp; c <= cb; c += kCombThreads / 32) {
-    if (cta_first(W, c, p.grid) >= cta_first(W, c + 1, p.grid)) continue;  // a CTA without units
-    const size_t slot = (size_t)c * 2 + (c == ca ? 1 : 0);
-    // the first CTA's part begins at the stream's first unit, the others' behind it
-    const float2 ml = p.ml[slot * p.rb + rr];
-    float y[E];
-    const float* src = p.part + (slot * p.rb + rr) * D + lane * E;
+  for (int c0 = span.x + warp; c0 <= span.y; c0 += N * kCombWarps) {
+    float2 ml[N];
+    float y[N][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) y[e] = src[e];
-    add(ml.x, ml.y, y);
+    for (int i = 0; i < N; ++i) {
+      const int c = c0 + i * kCombWarps;
+      ml[i] = make_float2(0.f, 0.f);
+      if (c > span.y) continue;
+      // the first CTA's part begins at the stream's first unit, the others' behind it
+      const size_t row = ((size_t)c * 2 + (c == span.x ? 1 : 0)) * p.rb + rr;
+      ml[i] = p.ml[row];
+      const float* src = p.part + row * D + lane * E;
+      if constexpr (E == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(src);
+        y[i][0] = v.x, y[i][1] = v.y, y[i][2] = v.z, y[i][3] = v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(src);
+        y[i][0] = v.x, y[i][1] = v.y;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) add(ml[i].x, ml[i].y, y[i]);
   }
 #pragma unroll
   for (int e = 0; e < E; ++e) sm_o[warp][lane * E + e] = o[e];
   if (lane == 0) sm_ml[warp] = make_float2(m, l);
   __syncthreads();
   if (warp == 0) {
-    for (int w = 1; w < kCombThreads / 32; ++w) {
-      float y[E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) y[e] = sm_o[w][lane * E + e];
-      add(sm_ml[w].x, sm_ml[w].y, y);
-    }
+    for (int w = 1; w < kCombWarps; ++w) add(sm_ml[w].x, sm_ml[w].y, &sm_o[w][lane * E]);
     const float inv = l == 0.f ? 0.f : a.g.ts[1] / l;
 #pragma unroll
     for (int e = 0; e < E; ++e) op[lane * E + e] = from_f32<T>(o[e] * inv);
@@ -667,8 +661,10 @@ Plan make_plan(const AttendArgs& a, int parts, int sms, size_t* bytes) {
   const size_t slots = (size_t)p.grid * 2 * p.rb;
   const size_t ml = (slots * sizeof(float2) + 255) & ~(size_t)255;
   p.ml = static_cast<float2*>(a.ws);
-  p.part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + ml);
-  if (bytes) *bytes = ml + slots * a.g.D * sizeof(float);
+  const size_t span = ((size_t)p.nvs * sizeof(int2) + 255) & ~(size_t)255;
+  p.span = reinterpret_cast<int2*>(static_cast<char*>(a.ws) + ml);
+  p.part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + ml + span);
+  if (bytes) *bytes = ml + span + slots * a.g.D * sizeof(float);
   return p;
 }
 
