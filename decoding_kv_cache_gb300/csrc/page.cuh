@@ -131,6 +131,7 @@ struct AttendArgs {
   int32_t* status;
   void* ws;
 };
+bool attend_fits(const AttendArgs& a);
 size_t attend_ws_bytes(const PoolGeom& g, const PageTab& t, int Hq, int T);
 int launch_page_attend(const AttendArgs& a, int dtype, cudaStream_t s);
 

@@ -216,7 +216,9 @@ int kvc_page_read(const kvc_pool* pool, const kvc_pages* pages, int32_t dtype, c
 size_t kvc_page_attend_workspace_size(const kvc_pool* pool, const kvc_pages* pages, int32_t Hq, int32_t T) {
   PoolGeom g;
   PageTab t;
-  if (check_pool(pool, &g) || check_pages(pages, g.lp, &t) || Hq < 1 || Hq % t.Hkv || T < 1) return 0;
+  if (check_pool(pool, &g) || check_pages(pages, g.lp, &t) || Hq < 1 || Hq % t.Hkv || T < 1 ||
+      (long long)t.B * Hq * T > (1LL << 30))
+    return 0;
   return attend_ws_bytes(g, t, Hq, T);
 }
 
@@ -231,6 +233,9 @@ int kvc_page_attend(const kvc_pool* pool, const kvc_pages* pages, int32_t dtype,
   if (a.t.L != 1 || Hq < 1 || T < 1 || !out || !isfinite(scale)) return KVC_ERR_INVALID_ARG;
   if (Hq % a.t.Hkv) return KVC_ERR_NOT_DIVISIBLE;
   if ((long long)a.t.B * Hq > (1LL << 30) || (long long)a.t.B * Hq * T > (1LL << 30)) return KVC_ERR_TOO_LARGE;
+  a.Hq = Hq;
+  a.T = T;
+  if (!attend_fits(a)) return KVC_ERR_TOO_LARGE;
   if ((rc = check_rows(q, q_strides, es, &a.qs))) return rc;
   if (!at16(out) || !at4(lse)) return KVC_ERR_ALIGNMENT;
   if (!workspace || ws_bytes < attend_ws_bytes(a.g, a.t, Hq, T) ||
@@ -239,8 +244,6 @@ int kvc_page_attend(const kvc_pool* pool, const kvc_pages* pages, int32_t dtype,
   a.q = q;
   a.out = out;
   a.lse = lse;
-  a.Hq = Hq;
-  a.T = T;
   a.n_q = n_q;
   a.scale = scale * a.g.ts[0];
   a.status = status;

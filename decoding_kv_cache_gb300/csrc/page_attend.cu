@@ -21,8 +21,7 @@
 // partial (max, sum, O) rows in the workspace; the combine kernel merges them (and writes the rows of empty
 // streams). In a CTA each of the four warps takes every fourth 32-token chunk with its own two-stage
 // ring of bulk copies; nothing but the end of a stream's part synchronises them.
-#include "page.cuh"
-#include "tc_ptx.cuh"
+#include "page_attend.cuh"
 
 namespace kvc {
 namespace {
@@ -32,87 +31,6 @@ constexpr int kUnit = 64;    // tokens of a work unit
 constexpr int kChunk32 = 32;  // tokens of a ring stage
 constexpr int kStages = 2;
 constexpr int kMaxGridSMs = 160;
-constexpr float kOff = 10.f;  // probabilities are held times 2^10 (fp16's range is used below the maximum too)
-constexpr float kRaise = 5.f; // a reference may lag the maximum by 2^5: 2^15 at most, inside fp16
-
-struct Plan {
-  int nrb;     // row blocks per stream
-  int rb;      // rows per block
-  int G;
-  int nvs;     // streams * nrb
-  int grid;    // CTAs of the main kernel
-  float* part;  // [grid][2][rb][D]
-  float2* ml;   // [grid][2][rb] (reference, sum)
-  int2* span;   // [nvs] first and last CTA of a stream's units (streams with units only)
-};
-
-struct Stream {  // what a (stream, row block) has to see
-  int s, b, h, len, nq, r0, rows, vis;
-};
-
-__device__ __forceinline__ Stream stream_of(const AttendArgs& a, const Plan& p, int vs, bool report) {
-  Stream x;
-  x.s = vs / p.nrb;
-  x.r0 = (vs % p.nrb) * p.rb;
-  x.b = x.s / a.t.Hkv;
-  x.h = x.s % a.t.Hkv;
-  x.len = a.t.len[x.s];
-  x.nq = a.n_q ? min(max(a.n_q[x.b], 0), a.T) : a.T;
-  if (x.len < 0 || x.len > ((long long)a.t.maxp << a.g.lp)) {
-    if (report) status_or(a.status, KVC_STATUS_BAD_PAGE);
-    x.len = 0;
-  }
-  x.rows = max(0, min(p.rb, x.nq * p.G - x.r0));
-  const int tmax = min((x.r0 + p.rb - 1) / p.G, x.nq - 1);
-  x.vis = x.rows ? max(0, x.len - x.nq + tmax + 1) : 0;
-  return x;
-}
-__device__ __forceinline__ int units_of(const Stream& x) { return (x.vis + kUnit - 1) / kUnit; }
-
-// Units before each thread's run of streams and in all (block of kThr threads; every thread calls).
-template <int kThr>
-__device__ __forceinline__ int scan_units(const AttendArgs& a, const Plan& p, int* sm, int per, int* total) {
-  int mine = 0;
-  for (int i = 0; i < per; ++i) {
-    const int vs = threadIdx.x * per + i;
-    if (vs < p.nvs) mine += units_of(stream_of(a, p, vs, false));
-  }
-  int incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(kFull, incl, o);
-    if ((threadIdx.x & 31) >= o) incl += v;
-  }
-  if ((threadIdx.x & 31) == 31) sm[threadIdx.x >> 5] = incl;
-  __syncthreads();
-  int base = 0, all = 0;
-#pragma unroll
-  for (int i = 0; i < kThr / 32; ++i) {
-    const int v = sm[i];
-    if (i < (int)(threadIdx.x >> 5)) base += v;
-    all += v;
-  }
-  *total = all;
-  return base + incl - mine;
-}
-
-// CTA i of `grid` takes units [first(i), first(i + 1)) of W: the first W % grid CTAs one more than the others.
-struct Split {
-  int q, rem;
-  __device__ __forceinline__ Split(int W, int grid) : q(W / grid), rem(W % grid) {}
-  __device__ __forceinline__ int first(int i) const { return i * q + min(i, rem); }
-  __device__ __forceinline__ int owner(int u) const {
-    const int big = rem * (q + 1);
-    return u < big ? u / (q + 1) : rem + (u - big) / q;
-  }
-};
-
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
-                   tc::smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
-               : "memory");
-}
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -125,20 +43,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(x));
   return r;
 }
-__device__ __forceinline__ uint32_t hmul2(uint32_t x, uint32_t y) {
-  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  const __half2 r = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-  return y;
-}
-
 template <int D, int NT>
 struct Smem {
   static constexpr int kStage = 2 * blk_bytes(D);  // 32 tokens
@@ -150,7 +54,7 @@ struct Smem {
 // Rows per thread in the accumulators: of tile nt, rows 2t and 2t+1 (t = lane % 4); channels
 // CPV*g + 2 mt (+1), g = lane / 4.
 template <typename T, int D, int NT, int PARTS, int MINB>
-__global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a, Plan p) {
+__global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a, AttendPlan p) {
   using SM = Smem<D, NT>;
   constexpr int KS = D / 16;   // k steps of Q K^T and m tiles of V^T
   constexpr int CPL = D / 4;   // channels of a lane in K
@@ -178,7 +82,7 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
   for (int i = 0; i < per; ++i) {
     const int vs = threadIdx.x * per + i;
     if (vs >= p.nvs) break;
-    const int u = units_of(stream_of(a, p, vs, false));
+    const int u = units_of(p, stream_of(a, p, vs, false));
     if (before <= w0 && w0 < before + u) {
       sm_first[0] = vs;
       sm_first[1] = before;
@@ -195,7 +99,7 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
 
   for (int U; left > 0; ++vs, ua = 0, base += U) {
     const Stream x = stream_of(a, p, vs, true);
-    U = units_of(x);
+    U = units_of(p, x);
     if (U == 0) continue;
     const int ub = min(U, ua + left);
     left -= ub - ua;
@@ -570,34 +474,15 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
   }
 }
 
-// Rows whose stream several CTAs shared, and rows of streams without tokens: a CTA per (stream, row
-// block, row), its warps taking every fourth part, four at a time.
-constexpr int kCombThreads = 128, kCombWarps = kCombThreads / 32;
-template <typename T, int D>
-__global__ void __launch_bounds__(kCombThreads) combine_kernel(AttendArgs a, Plan p) {
-  __shared__ float sm_o[kCombWarps][D];
-  __shared__ float2 sm_ml[kCombWarps];
-  griddep_launch();
-  griddep_wait();
-  const int vs = blockIdx.x / p.rb, rr = blockIdx.x % p.rb;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int2 span = p.span[vs];  // read beside the length; undefined for a stream without units
-  const Stream x = stream_of(a, p, vs, threadIdx.x == 0 && rr == 0);
-  if (rr >= x.rows) return;
-  const int r = x.r0 + rr;
-  const size_t at = ((size_t)x.b * a.T + r / p.G) * a.Hq + x.h * p.G + r % p.G;
-  T* op = static_cast<T*>(a.out) + at * D;
-  if (x.vis == 0) {
-    for (int i = threadIdx.x; i < D; i += kCombThreads) op[i] = from_f32<T>(0.f);
-    if (a.lse && threadIdx.x == 0) a.lse[at] = -INFINITY;
-    return;
-  }
-  if (span.x == span.y) return;  // written by that CTA
-  constexpr int E = D / 32, N = 4;
+// One row's parts merged by one warp, from part `first` on every `step`-th, four at a time; E channels a lane.
+template <int E>
+struct Merged {
   float o[E], l = 0.f, m = -INFINITY;
+  __device__ __forceinline__ Merged() {
 #pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
-  auto add = [&](float y_m, float y_l, const float* y) {
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+  }
+  __device__ __forceinline__ void add(float y_m, float y_l, const float* y) {
     if (y_l == 0.f) return;
     const float to = l == 0.f ? y_m : fmaxf(m, y_m);
     const float c0 = l == 0.f ? 0.f : ex2(m - to), c1 = ex2(y_m - to);
@@ -605,63 +490,104 @@ __global__ void __launch_bounds__(kCombThreads) combine_kernel(AttendArgs a, Pla
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = o[e] * c0 + y[e] * c1;
     m = to;
-  };
-  for (int c0 = span.x + warp; c0 <= span.y; c0 += N * kCombWarps) {
-    float2 ml[N];
-    float y[N][E];
+  }
+  __device__ __forceinline__ void parts(const AttendPlan& p, int2 span, int first, int step, int rr, int D) {
+    constexpr int N = 4;
+    const int lane = threadIdx.x & 31;
+    for (int c0 = span.x + first; c0 <= span.y; c0 += N * step) {
+      float2 ml[N];
+      float y[N][E];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int c = c0 + i * kCombWarps;
-      ml[i] = make_float2(0.f, 0.f);
-      if (c > span.y) continue;
-      // the first CTA's part begins at the stream's first unit, the others' behind it
-      const size_t row = ((size_t)c * 2 + (c == span.x ? 1 : 0)) * p.rb + rr;
-      ml[i] = p.ml[row];
-      const float* src = p.part + row * D + lane * E;
-      if constexpr (E == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(src);
-        y[i][0] = v.x, y[i][1] = v.y, y[i][2] = v.z, y[i][3] = v.w;
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(src);
-        y[i][0] = v.x, y[i][1] = v.y;
+      for (int i = 0; i < N; ++i) {
+        const int c = c0 + i * step;
+        ml[i] = make_float2(0.f, 0.f);
+        if (c > span.y) continue;
+        // the first CTA's part begins at the stream's first unit, the others' behind it
+        const size_t row = ((size_t)c * 2 + (c == span.x ? 1 : 0)) * p.rb + rr;
+        ml[i] = p.ml[row];
+        const float* src = p.part + row * D + lane * E;
+        if constexpr (E == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(src);
+          y[i][0] = v.x, y[i][1] = v.y, y[i][2] = v.z, y[i][3] = v.w;
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(src);
+          y[i][0] = v.x, y[i][1] = v.y;
+        }
       }
+#pragma unroll
+      for (int i = 0; i < N; ++i) add(ml[i].x, ml[i].y, y[i]);
     }
-#pragma unroll
-    for (int i = 0; i < N; ++i) add(ml[i].x, ml[i].y, y[i]);
   }
+};
+
+// Rows whose stream several CTAs shared, and rows of streams without tokens. Few rows a block (SPLIT): a CTA
+// per row, its warps taking every fourth part. Many rows, whose streams fewer CTAs share: a warp per row.
+constexpr int kCombThreads = 128, kCombWarps = kCombThreads / 32;
+template <typename T, int D, bool SPLIT>
+__global__ void __launch_bounds__(kCombThreads) combine_kernel(AttendArgs a, AttendPlan p) {
+  __shared__ float sm_o[kCombWarps][D];
+  __shared__ float2 sm_ml[kCombWarps];
+  griddep_launch();
+  griddep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = SPLIT ? blockIdx.x : blockIdx.x * kCombWarps + warp;
+  const int vs = row / p.rb, rr = row % p.rb;
+  if (vs >= p.nvs) return;
+  const int2 span = p.span[vs];  // read beside the length; undefined for a stream without units
+  const Stream x = stream_of(a, p, vs, lane == 0 && rr == 0);
+  if (rr >= x.rows) return;
+  const int r = x.r0 + rr;
+  const size_t at = ((size_t)x.b * a.T + r / p.G) * a.Hq + x.h * p.G + r % p.G;
+  T* op = static_cast<T*>(a.out) + at * D;
+  constexpr int E = D / 32;
+  if (x.vis == 0) {
+    if (!SPLIT || warp == 0) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) sm_o[warp][lane * E + e] = o[e];
-  if (lane == 0) sm_ml[warp] = make_float2(m, l);
-  __syncthreads();
-  if (warp == 0) {
-#pragma unroll
-    for (int w = 1; w < kCombWarps; ++w) add(sm_ml[w].x, sm_ml[w].y, &sm_o[w][lane * E]);
-    const float inv = l == 0.f ? 0.f : a.g.ts[1] / l;
-#pragma unroll
-    for (int e = 0; e < E; ++e) op[lane * E + e] = from_f32<T>(o[e] * inv);
-    if (a.lse && lane == 0) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      for (int e = 0; e < E; ++e) op[lane * E + e] = from_f32<T>(0.f);
+      if (a.lse && lane == 0) a.lse[at] = -INFINITY;
+    }
+    return;
   }
+  if (span.x == span.y) return;  // written by that CTA
+  Merged<E> y;
+  y.parts(p, span, SPLIT ? warp : 0, SPLIT ? kCombWarps : 1, rr, D);
+  if constexpr (SPLIT) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) sm_o[warp][lane * E + e] = y.o[e];
+    if (lane == 0) sm_ml[warp] = make_float2(y.m, y.l);
+    __syncthreads();
+    if (warp) return;
+#pragma unroll
+    for (int w = 1; w < kCombWarps; ++w) y.add(sm_ml[w].x, sm_ml[w].y, &sm_o[w][lane * E]);
+  }
+  const float inv = y.l == 0.f ? 0.f : a.g.ts[1] / y.l;
+#pragma unroll
+  for (int e = 0; e < E; ++e) op[lane * E + e] = from_f32<T>(y.o[e] * inv);
+  if (a.lse && lane == 0) a.lse[at] = y.l == 0.f ? -INFINITY : (y.m + log2f(y.l)) * 0.6931471805599453f;
 }
 
 // Row tiles of 8 a block takes: one covers the decode step of up to 8 query heads per KV head; more rows
-// share the decoding of a chunk.
-int tiles_for(int R, int parts) { return R <= 8 ? 1 : (R <= 16 || parts == 2) ? 2 : 4; }
-int min_blocks(int nt, int parts) { return nt * parts == 1 ? 4 : nt * parts == 2 ? 3 : 2; }
+// share the decoding of a chunk. From kTcMin rows on bf16 queries go to the tcgen05 kernel.
+constexpr int kTcMin = 33;
+constexpr int tiles_for(int R, int parts) { return R <= 8 ? 1 : (R <= 16 || parts == 2) ? 2 : 4; }
+constexpr int min_blocks(int nt, int parts) { return nt * parts == 1 ? 4 : nt * parts == 2 ? 3 : 2; }
 
-Plan make_plan(const AttendArgs& a, int parts, int sms, size_t* bytes) {
-  Plan p = {};
+AttendPlan make_plan(const AttendArgs& a, int parts, int sms, size_t* bytes) {
+  AttendPlan p = {};
   p.G = a.Hq / a.t.Hkv;
   const int R = p.G * a.T, nt = tiles_for(R, parts);
-  p.rb = 8 * nt;
+  const bool tc = parts == 1 && R >= kTcMin;
+  p.unit = tc ? kTcUnit : kUnit;
+  p.rb = tc ? kTcRows : 8 * nt;
   p.nrb = (R + p.rb - 1) / p.rb;
   p.nvs = a.t.S * p.nrb;
-  p.grid = (sms < kMaxGridSMs ? sms : kMaxGridSMs) * min_blocks(nt, parts);
-  const long long units = (long long)p.nvs * ((((long long)a.t.maxp << a.g.lp) + kUnit - 1) / kUnit);
+  p.grid = (sms < kMaxGridSMs ? sms : kMaxGridSMs) * (tc ? 1 : min_blocks(nt, parts));
+  const long long units = (long long)p.nvs * ((((long long)a.t.maxp << a.g.lp) + p.unit - 1) / p.unit);
   if (units < p.grid) p.grid = (int)units;
   const size_t slots = (size_t)p.grid * 2 * p.rb;
   const size_t ml = (slots * sizeof(float2) + 255) & ~(size_t)255;
-  p.ml = static_cast<float2*>(a.ws);
   const size_t span = ((size_t)p.nvs * sizeof(int2) + 255) & ~(size_t)255;
+  p.ml = static_cast<float2*>(a.ws);
   p.span = reinterpret_cast<int2*>(static_cast<char*>(a.ws) + ml);
   p.part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + ml + span);
   if (bytes) *bytes = ml + span + slots * a.g.D * sizeof(float);
@@ -669,30 +595,47 @@ Plan make_plan(const AttendArgs& a, int parts, int sms, size_t* bytes) {
 }
 
 template <typename T, int D, int NT, int PARTS>
-int go(const AttendArgs& a, const Plan& p, cudaStream_t s) {
-  constexpr int MINB = NT * PARTS == 1 ? 4 : NT * PARTS == 2 ? 3 : 2;
-  auto k = attend_kernel<T, D, NT, PARTS, MINB>;
+int go(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
+  auto k = attend_kernel<T, D, NT, PARTS, min_blocks(NT, PARTS)>;
   constexpr int smem = Smem<D, NT>::bytes;
   if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return KVC_ERR_LAUNCH;
-  if (launch_pdl(k, dim3(p.grid), dim3(32 * kWarps), smem, s, false, a, p) != cudaSuccess) return KVC_ERR_LAUNCH;
-  if (launch_pdl(combine_kernel<T, D>, dim3((unsigned)((long long)p.nvs * p.rb)), dim3(kCombThreads), 0, s, false, a,
-                 p) != cudaSuccess)
-    return KVC_ERR_LAUNCH;
-  return KVC_OK;
+  return launch_pdl(k, dim3(p.grid), dim3(32 * kWarps), smem, s, false, a, p) == cudaSuccess ? KVC_OK : KVC_ERR_LAUNCH;
 }
 
 template <typename T, int D, int PARTS>
-int go_tiles(const AttendArgs& a, const Plan& p, cudaStream_t s) {
+int run(const AttendArgs& a, int sms, cudaStream_t s) {
+  const AttendPlan p = make_plan(a, PARTS, sms, nullptr);
+  int rc = KVC_ERR_INVALID_ARG;
   switch (p.rb / 8) {
-    case 1: return go<T, D, 1, PARTS>(a, p, s);
-    case 2: return go<T, D, 2, PARTS>(a, p, s);
-    default:
-      if constexpr (PARTS == 1) return go<T, D, 4, PARTS>(a, p, s);
-      return KVC_ERR_INVALID_ARG;
+    case 1: rc = go<T, D, 1, PARTS>(a, p, s); break;
+    case 2: rc = go<T, D, 2, PARTS>(a, p, s); break;
+    case 4:
+      if constexpr (PARTS == 1) rc = go<T, D, 4, PARTS>(a, p, s);
+      break;
+    case kTcRows / 8:
+      if constexpr (PARTS == 1) rc = launch_attend_tc(a, p, s);
+      break;
   }
+  if (rc) return rc;
+  const long long rows = (long long)p.nvs * p.rb;
+  const cudaError_t e =
+      p.rb <= 16 ? launch_pdl(combine_kernel<T, D, true>, dim3((unsigned)rows), dim3(kCombThreads), 0, s, false, a, p)
+                 : launch_pdl(combine_kernel<T, D, false>, dim3((unsigned)((rows + kCombWarps - 1) / kCombWarps)),
+                              dim3(kCombThreads), 0, s, false, a, p);
+  return e == cudaSuccess ? KVC_OK : KVC_ERR_LAUNCH;
 }
 
 }  // namespace
+
+bool attend_fits(const AttendArgs& a) {  // work units and rows are counted in 32 bits
+  for (int parts = 1; parts <= 2; ++parts) {
+    const int R = a.Hq / a.t.Hkv * a.T, rb = 8 * tiles_for(R, parts);
+    const long long nvs = (long long)a.t.S * ((R + rb - 1) / rb);
+    if (nvs * rb > 0x7fffffffLL || nvs * ((((long long)a.t.maxp << a.g.lp) + kUnit - 1) / kUnit) > 0x7fffffffLL)
+      return false;
+  }
+  return true;
+}
 
 size_t attend_ws_bytes(const PoolGeom& g, const PageTab& t, int Hq, int T) {
   AttendArgs a = {};
@@ -700,6 +643,7 @@ size_t attend_ws_bytes(const PoolGeom& g, const PageTab& t, int Hq, int T) {
   a.t = t;
   a.Hq = Hq;
   a.T = T;
+  if (!attend_fits(a)) return 0;
   size_t most = 0;
   for (int parts = 1; parts <= 2; ++parts) {
     size_t n;
@@ -714,12 +658,8 @@ int launch_page_attend(const AttendArgs& a, int dtype, cudaStream_t s) {
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return KVC_ERR_LAUNCH;
-  if (dtype == KVC_BF16) {
-    const Plan p = make_plan(a, 1, sms, nullptr);
-    return a.g.D == 128 ? go_tiles<__nv_bfloat16, 128, 1>(a, p, s) : go_tiles<__nv_bfloat16, 64, 1>(a, p, s);
-  }
-  const Plan p = make_plan(a, 2, sms, nullptr);
-  return a.g.D == 128 ? go_tiles<float, 128, 2>(a, p, s) : go_tiles<float, 64, 2>(a, p, s);
+  if (dtype == KVC_BF16) return a.g.D == 128 ? run<__nv_bfloat16, 128, 1>(a, sms, s) : run<__nv_bfloat16, 64, 1>(a, sms, s);
+  return a.g.D == 128 ? run<float, 128, 2>(a, sms, s) : run<float, 64, 2>(a, sms, s);
 }
 
 }  // namespace kvc

@@ -1,0 +1,112 @@
+// page_attend.cuh -- what the kernels of kvc_page_attend share: the streams' work units and their split
+// over the CTAs, partial results, and small helpers.
+#pragma once
+
+#include "page.cuh"
+#include "tc_ptx.cuh"
+
+namespace kvc {
+
+constexpr float kOff = 10.f;   // probabilities are held times 2^10 (fp16's range is used below the maximum too)
+constexpr float kRaise = 5.f;  // a reference may lag the maximum by 2^5: 2^15 at most, inside fp16
+
+struct AttendPlan {
+  int unit;    // tokens of a work unit
+  int nrb;     // row blocks per stream
+  int rb;      // rows per block
+  int G;
+  int nvs;     // streams * nrb
+  int grid;    // CTAs of the main kernel
+  float* part;  // [grid][2][rb][D]
+  float2* ml;   // [grid][2][rb] (reference, sum)
+  int2* span;   // [nvs] first and last CTA of a stream's units (streams with units only)
+};
+
+struct Stream {  // what a (stream, row block) has to see
+  int s, b, h, len, nq, r0, rows, vis;
+};
+
+__device__ __forceinline__ Stream stream_of(const AttendArgs& a, const AttendPlan& p, int vs, bool report) {
+  Stream x;
+  x.s = vs / p.nrb;
+  x.r0 = (vs % p.nrb) * p.rb;
+  x.b = x.s / a.t.Hkv;
+  x.h = x.s % a.t.Hkv;
+  x.len = a.t.len[x.s];
+  x.nq = a.n_q ? min(max(a.n_q[x.b], 0), a.T) : a.T;
+  if (x.len < 0 || x.len > ((long long)a.t.maxp << a.g.lp)) {
+    if (report) status_or(a.status, KVC_STATUS_BAD_PAGE);
+    x.len = 0;
+  }
+  x.rows = max(0, min(p.rb, x.nq * p.G - x.r0));
+  const int tmax = min((x.r0 + p.rb - 1) / p.G, x.nq - 1);
+  x.vis = x.rows ? max(0, x.len - x.nq + tmax + 1) : 0;
+  return x;
+}
+__device__ __forceinline__ int units_of(const AttendPlan& p, const Stream& x) { return (x.vis + p.unit - 1) / p.unit; }
+
+// Units before each thread's run of streams and in all (block of kThr threads; every thread calls).
+template <int kThr>
+__device__ __forceinline__ int scan_units(const AttendArgs& a, const AttendPlan& p, int* sm, int per, int* total) {
+  int mine = 0;
+  for (int i = 0; i < per; ++i) {
+    const int vs = threadIdx.x * per + i;
+    if (vs < p.nvs) mine += units_of(p, stream_of(a, p, vs, false));
+  }
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kFull, incl, o);
+    if ((threadIdx.x & 31) >= o) incl += v;
+  }
+  if ((threadIdx.x & 31) == 31) sm[threadIdx.x >> 5] = incl;
+  __syncthreads();
+  int base = 0, all = 0;
+#pragma unroll
+  for (int i = 0; i < kThr / 32; ++i) {
+    const int v = sm[i];
+    if (i < (int)(threadIdx.x >> 5)) base += v;
+    all += v;
+  }
+  *total = all;
+  return base + incl - mine;
+}
+
+// CTA i of `grid` takes units [first(i), first(i + 1)) of W: the first W % grid CTAs one more than the others.
+struct Split {
+  int q, rem;
+  __device__ __forceinline__ Split(int W, int grid) : q(W / grid), rem(W % grid) {}
+  __device__ __forceinline__ int first(int i) const { return i * q + min(i, rem); }
+  __device__ __forceinline__ int owner(int u) const {
+    const int big = rem * (q + 1);
+    return u < big ? u / (q + 1) : rem + (u - big) / q;
+  }
+};
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+                   tc::smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
+               : "memory");
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t x, uint32_t y) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __half2 r = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+
+
+// The kernel for many query rows (tcgen05, 128 rows a block).
+constexpr int kTcRows = 128, kTcUnit = 128;
+int launch_attend_tc(const AttendArgs& a, const AttendPlan& p, cudaStream_t s);
+
+}  // namespace kvc

@@ -356,7 +356,9 @@ def test_attend(dt, D, B, Hkv, G, T, page, lens):
 
 
 @pytest.mark.parametrize("dt,D,B,Hkv,G,T,n", [("bf16", 128, 1, 1, 4, 1, 6000), ("f32", 64, 2, 2, 2, 1, 3001),
-                                              ("bf16", 64, 1, 2, 8, 20, 2500), ("f32", 128, 1, 1, 3, 2, 4097)])
+                                              ("bf16", 64, 1, 2, 8, 20, 2500), ("f32", 128, 1, 1, 3, 2, 4097),
+                                              # several units a CTA, streams cut between CTAs, two row blocks
+                                              ("bf16", 128, 4, 8, 4, 16, 3000), ("bf16", 64, 4, 8, 5, 40, 2200)])
 def test_attend_long(dt, D, B, Hkv, G, T, n):
     rng = np.random.default_rng(n)
     x, q = make_attend(dt, D, B, Hkv, G, T, 64, rng.integers(n // 8, n + 1, B * Hkv), seed=n)
