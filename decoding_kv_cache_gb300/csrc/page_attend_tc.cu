@@ -19,6 +19,8 @@
 //
 // At a part's end the groups' O are merged and written (whole streams) or left for the combine kernel.
 // All waits are bounded; a role that gives up raises KVC_STATUS_TIMEOUT and the others follow.
+#include <type_traits>
+
 #include "page_attend.cuh"
 #include "score_tc.cuh"
 
@@ -47,6 +49,25 @@ struct Bars {
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(tc::smem_u32(bar)) : "memory");
+}
+// The first poll in line, the waiting out of it (the roles' loops stay short: five warps of different roles
+// share an SM quarter's instruction cache).
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
+  return wait_or_abort(bar, parity, abort_flag, status);
+}
+__device__ __forceinline__ bool mbar_ready(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(tc::smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done;
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+  return e;
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
 
@@ -82,6 +103,32 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+
+// 16 columns of this thread's lane, without waiting
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// two fp32 operations in one issue
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 w, x, y;\n"
+      " mov.b64 {%0, %1}, w;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
 
 // A token's codes and scales to a row of fp16 in the swizzled tile; zero: the row stands for nothing.
 template <int D>
@@ -141,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
       tc::mbar_init(&bars.pv_done[i], 1);
       tc::mbar_init(&bars.p_full[i], 4);
     }
-    tc::mbar_init(&bars.q_full, 4);
+    tc::mbar_init(&bars.q_full, kSoftWarps);
     tc::mbar_init(&bars.merge, kSoftWarps);
     tc::mbar_fence_init();
   }
@@ -167,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
   tc::fence_after_sync();
   const uint32_t tmem = tmem_slot;
   volatile int* ab = &abort_flag;
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_or_abort(bar, parity, ab, a.status); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_ready(bar, parity) || wait_slow(bar, parity, ab, a.status); };
 
   // Every role walks the same parts: f(stream, vs, first unit, end unit, units of the stream, units before it)
   auto parts = [&](auto&& f) {
@@ -217,43 +264,52 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
     });
   } else if (warp == 17) {
     // ---- issuer --------------------------------------------------------------------------------
-    if (lane == 0) {
-      constexpr uint32_t id_qk = idesc_f16(128, kTcUnit, false), id_pv = idesc_f16(128, D, true);
-      const uint32_t sq = tc::smem_u32(smem), sk = tc::smem_u32(smem + L::oK), sv = tc::smem_u32(smem + L::oV);
-      auto swait = [&](uint64_t* bar, uint32_t parity) { return spin_or_abort(bar, parity, ab, a.status); };
-      uint32_t nk = 0, nv = 0, np[2] = {0, 0}, seg = 0;
-      parts([&](const Stream&, int, int ua, int ub, int, int) {
-        const int m = ub - ua;
-        if (!swait(&bars.q_full, seg++ & 1)) return false;
-        for (int i = 0; i <= m; ++i) {
-          if (i < m) {
-            const int t = nk & 1, w = i & 1;
-            if (!swait(&bars.k_full[t], (nk >> 1) & 1)) return false;
-            tc::fence_after_sync();
+    // the whole warp walks the loop, so that addresses stay in uniform registers; one lane issues
+    constexpr uint32_t id_qk = idesc_f16(128, kTcUnit, false), id_pv = idesc_f16(128, D, true);
+    const uint64_t dq = tc::desc_k_sw128(tc::smem_u32(smem)), dk = tc::desc_k_sw128(tc::smem_u32(smem + L::oK)),
+                   dv = desc_mn_sw128(tc::smem_u32(smem + L::oV), L::kHalf);
+    const bool leader = elect_one();
+    uint32_t nk = 0, nv = 0, np[2] = {0, 0}, seg = 0;
+    parts([&](const Stream&, int, int ua, int ub, int, int) {
+      const int m = ub - ua;
+      if (!wait(&bars.q_full, seg++ & 1)) return false;
+      for (int i = 0; i <= m; ++i) {
+        if (i < m) {
+          const int t = nk & 1, w = i & 1;
+          if (!wait(&bars.k_full[t], (nk >> 1) & 1)) return false;
+          tc::fence_after_sync();
+          if (leader) {
+            const uint64_t d = dk + (uint64_t)(t * (L::kTile >> 4));
 #pragma unroll
-            for (int j = 0; j < D / 16; ++j)
-              umma_ss(tmem + w * 128, tc::desc_k_sw128(sq + (j >> 2) * L::kHalf + (j & 3) * 32),
-                      tc::desc_k_sw128(sk + t * L::kTile + (j >> 2) * L::kHalf + (j & 3) * 32), id_qk, j > 0);
+            for (int j = 0; j < D / 16; ++j) {
+              constexpr int step = 32 >> 4;
+              const uint64_t at = (j >> 2) * (L::kHalf >> 4) + (j & 3) * step;
+              umma_ss(tmem + w * 128, dq + at, d + at, id_qk, j > 0);
+            }
             tc::umma_commit(&bars.k_empty[t]);
             tc::umma_commit(&bars.s_full[w]);
-            ++nk;
           }
-          if (i > 0) {
-            const int t = nv & 1, w = (i - 1) & 1;
-            if (!swait(&bars.v_full[t], (nv >> 1) & 1) || !swait(&bars.p_full[w], np[w]++ & 1)) return false;
-            tc::fence_after_sync();
+          __syncwarp();
+          ++nk;
+        }
+        if (i > 0) {
+          const int t = nv & 1, w = (i - 1) & 1;
+          if (!wait(&bars.v_full[t], (nv >> 1) & 1) || !wait(&bars.p_full[w], np[w]++ & 1)) return false;
+          tc::fence_after_sync();
+          if (leader) {
+            const uint64_t d = dv + (uint64_t)(t * (L::kTile >> 4));
 #pragma unroll
             for (int j = 0; j < kTcUnit / 16; ++j)
-              umma_ts(tmem + kColO + w * 128, tmem + w * 128 + 8 * j,
-                      desc_mn_sw128(sv + t * L::kTile + j * 2048, L::kHalf), id_pv, i > 2 || j > 0);
+              umma_ts(tmem + kColO + w * 128, tmem + w * 128 + 8 * j, d + j * (2048 >> 4), id_pv, i > 2 || j > 0);
             tc::umma_commit(&bars.v_empty[t]);
             tc::umma_commit(&bars.pv_done[w]);
-            ++nv;
           }
+          __syncwarp();
+          ++nv;
         }
-        return true;
-      });
-    }
+      }
+      return true;
+    });
   } else if (warp >= kSoftWarps) {
     // ---- decoders ------------------------------------------------------------------------------
     const int kv = (warp - kSoftWarps) >> 2, j = threadIdx.x & 127;
@@ -289,36 +345,37 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
     uint32_t ns = 0, unit0 = 0, seg = 0;  // units of this group and of the CTA so far
     parts([&](const Stream& x, int vs, int ua, int ub, int U, int base) {
       const int m = ub - ua;
-      if (w == 0) {
-        // the query row, brought to [256, 512) by a power of two (bf16 values exact in fp16), with the
-        // scale's sign, so that maxima of dot products are maxima of logits
-        const bool in = rr < x.rows;
-        const int r = x.r0 + rr;
-        const T* qp = static_cast<const T*>(a.q) + x.b * a.qs.b + (in ? r / p.G : 0) * a.qs.t +
-                      (x.h * p.G + (in ? r % p.G : 0)) * a.qs.h;
-        float mx = 0.f;
-        if (in) {
-#pragma unroll 4
-          for (int i = 0; i < D / 8; ++i) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(qp) + i);
-            const T* e = reinterpret_cast<const T*>(&v);
+      {
+        // the query rows, each brought to [256, 512) by a power of two (bf16 values exact in fp16), with the
+        // scale's sign, so that maxima of dot products are maxima of logits. A warp takes 16 rows, D/8 lanes
+        // a row, all of its reads in flight at once.
+        constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // lanes of a row, rows at a time
+        uint4 v[16 / kAt];
+        const int i = lane % kLanes;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(to_f32(e[k])));
-          }
+        for (int k = 0; k < 16 / kAt; ++k) {
+          const int q = warp * 16 + k * kAt + lane / kLanes, r = x.r0 + q;
+          v[k] = make_uint4(0u, 0u, 0u, 0u);
+          if (q < x.rows)
+            v[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + x.b * a.qs.b + (r / p.G) * a.qs.t +
+                                                        (x.h * p.G + r % p.G) * a.qs.h) + i);
         }
-        const int ex = max((int)(__float_as_uint(mx) >> 23), 24);
-        const float mul = copysignf(__uint_as_float((uint32_t)(262 - ex) << 23), a.scale);
-        row_f[rr] = __uint_as_float((uint32_t)(ex - 8) << 23) * (fabsf(a.scale) * kLog2e);
-#pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) {
-          uint32_t o[4] = {0u, 0u, 0u, 0u};
-          if (in) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(qp) + i);
-            const T* e = reinterpret_cast<const T*>(&v);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) o[k] = pack2(to_f32(e[2 * k]) * mul, to_f32(e[2 * k + 1]) * mul);
-          }
-          *reinterpret_cast<uint4*>(smem + (i >> 3) * L::kHalf + rr * 128 + (((i & 7) ^ (rr & 7)) << 4)) =
+        for (int k = 0; k < 16 / kAt; ++k) {
+          const int q = warp * 16 + k * kAt + lane / kLanes;
+          const T* e = reinterpret_cast<const T*>(&v[k]);
+          float mx = 0.f;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) mx = fmaxf(mx, fabsf(to_f32(e[c])));
+#pragma unroll
+          for (int c = kLanes / 2; c; c >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, c));
+          const int ex = max((int)(__float_as_uint(mx) >> 23), 24);
+          const float mul = copysignf(__uint_as_float((uint32_t)(262 - ex) << 23), a.scale);
+          if (i == 0) row_f[q] = __uint_as_float((uint32_t)(ex - 8) << 23) * (fabsf(a.scale) * kLog2e);
+          uint32_t o[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[c] = pack2(to_f32(e[2 * c]) * mul, to_f32(e[2 * c + 1]) * mul);
+          *reinterpret_cast<uint4*>(smem + (i >> 3) * L::kHalf + q * 128 + (((i & 7) ^ (q & 7)) << 4)) =
               make_uint4(o[0], o[1], o[2], o[3]);
         }
         fence_async();
@@ -329,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
       const int minlim = min(max(x.len - x.nq + x.r0 / p.G + 1, 0), x.vis);
       float ref = 0.f, l = 0.f;
       bool none = true;
-      // the query rows' factors: written by group 0 before q_full, which precedes every s_full
+      // the query rows' factors were written before q_full, which precedes every s_full
       float f = 0.f;
       for (int i = w; i < m; i += 2, ++ns) {
         if (!wait(&bars.s_full[w], ns & 1)) return false;
@@ -339,16 +396,26 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
         const uint32_t ok = *reinterpret_cast<volatile uint32_t*>(&unit_ok[(unit0 + i) & 3]);
         const bool masked = tok0 + kTcUnit > minlim || ok != 0xff;
         float mx = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < 4; c += 2) {
+          uint32_t r[2][32];
+          tc::tmem_ld32_async(tS + 32 * c, r[0]);
+          tc::tmem_ld32_async(tS + 32 * c + 32, r[1]);
+          tc::tmem_wait();
+          tc::tmem_regs_ready(r[0]);
+          tc::tmem_regs_ready(r[1]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float v[32];
-          tc::tmem_ld32(tS + 32 * c, v);
-          if (masked) {
+          for (int h = 0; h < 2; ++h) {
+            float v[32];
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (tok0 + 32 * c + k >= lim || !(ok >> (2 * c + (k >> 4)) & 1)) v[k] = -INFINITY;
+            for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[h][k]);
+            if (masked) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (tok0 + 32 * (c + h) + k >= lim || !(ok >> (2 * (c + h) + (k >> 4)) & 1)) v[k] = -INFINITY;
+            }
+            mx = fmaxf(mx, tree_max32_3(v));
           }
-          mx = fmaxf(mx, tree_max32_3(v));
         }
         mx *= f;
         if (mx != mx) mx = -INFINITY;  // -inf * 0
@@ -380,25 +447,52 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
             }
           }
         }
-        // P over S: columns [0, 16 c + 16) are written when S's [0, 32 c + 32) have been read
+        // P over S, 16 tokens at a time with the next 16 logits on their way: columns [0, 8 c + 8) are written
+        // when S's [0, 16 c + 16) have been read
+        const float2 f2 = make_float2(f, f), ref2 = make_float2(-ref, -ref);
+        float2 l2 = make_float2(0.f, 0.f), l3 = l2;
+        uint32_t s0[16], s1[16];
+        auto probabilities = [&](uint32_t (&v)[16], int c, auto with_mask) {
+          uint32_t o[8];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float v[32];
-          tc::tmem_ld32(tS + 32 * c, v);
-          uint32_t o[16];
-#pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            float p0 = ex2(fmaf(v[k], f, -ref)), p1 = ex2(fmaf(v[k + 1], f, -ref));
-            if (masked) {
-              const bool blk = ok >> (2 * c + (k >> 4)) & 1;
-              if (tok0 + 32 * c + k >= lim || !blk) p0 = 0.f;
-              if (tok0 + 32 * c + k + 1 >= lim || !blk) p1 = 0.f;
+          for (int k = 0; k < 8; ++k) {
+            float2 y = fma2(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), f2, ref2);
+            y.x = ex2(y.x);
+            y.y = ex2(y.y);
+            if constexpr (decltype(with_mask)::value) {
+              const bool blk = ok >> c & 1;
+              if (tok0 + 16 * c + 2 * k >= lim || !blk) y.x = 0.f;
+              if (tok0 + 16 * c + 2 * k + 1 >= lim || !blk) y.y = 0.f;
             }
-            l += p0 + p1;
-            o[k / 2] = pack2(p0, p1);
+            if (k & 1)
+              l3 = add2(l3, y);
+            else
+              l2 = add2(l2, y);
+            o[k] = pack2(y.x, y.y);
           }
-          tmem_st16(tS + 16 * c, o);
-        }
+          asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(tS + 8 * c),
+                       "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                       : "memory");
+        };
+        auto sweep = [&](auto with_mask) {
+          tmem_ld16(tS, s0);
+#pragma unroll 1
+          for (int c = 0; c < 8; c += 2) {
+            tc::tmem_wait();
+            tc::tmem_regs_ready(s0);
+            tmem_ld16(tS + 16 * c + 16, s1);
+            probabilities(s0, c, with_mask);
+            tc::tmem_wait();
+            tc::tmem_regs_ready(s1);
+            if (c + 2 < 8) tmem_ld16(tS + 16 * c + 32, s0);
+            probabilities(s1, c + 1, with_mask);
+          }
+        };
+        if (masked)
+          sweep(std::true_type());
+        else
+          sweep(std::false_type());
+        l += (l2.x + l2.y) + (l3.x + l3.y);
         tmem_st_wait();
         tc::fence_before_sync();
         __syncwarp();
