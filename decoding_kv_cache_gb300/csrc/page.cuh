@@ -36,6 +36,19 @@ struct PageTab {
   int32_t* len;            // [S]
 };
 
+// Division of 0 <= n < 2^31 by a fixed d >= 1 (Granlund and Montgomery: with 2^s >= d and m = ceil(2^(31+s) / d)
+// the product n m / 2^(31+s) exceeds n / d by less than 1 / d).
+struct FastDiv {
+  uint32_t m;
+  int sh, d;
+  static FastDiv make(int d) {
+    int s = 0;
+    while ((1LL << s) < d) ++s;
+    return FastDiv{(uint32_t)(((1ULL << (31 + s)) + d - 1) / d), 31 + s, d};
+  }
+  __device__ __forceinline__ int div(int n) const { return (int)(((unsigned long long)(uint32_t)n * m) >> sh); }
+};
+
 // Workspace of the page operators (kvc_page_workspace_size).
 struct PageWs {
   int32_t* head;     // [0] nfree on entry, [1] pages the call took (compaction; -1: too few)

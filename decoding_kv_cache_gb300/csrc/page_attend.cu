@@ -153,8 +153,7 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
       float v[CPL];
       float mx = 0.f;
       if (in) {
-        const T* qp = static_cast<const T*>(a.q) + x.b * a.qs.b + (r / p.G) * a.qs.t + (x.h * p.G + r % p.G) * a.qs.h +
-                      CPL * t;
+        const T* qp = static_cast<const T*>(a.q) + q_row(a, p, x, r) + CPL * t;
         constexpr int per16 = 16 / (int)sizeof(T);
 #pragma unroll
         for (int i = 0; i < CPL / per16; ++i) {
@@ -190,10 +189,10 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
       for (int e = 0; e < 2; ++e) {
         f[nt][e] = __shfl_sync(kFull, inv, 8 * t + 4 * e);
         const int rr = nt * 8 + 2 * t + e;
-        lim[nt][e] = rr < x.rows ? min(max(x.len - x.nq + (x.r0 + rr) / p.G + 1, 0), x.vis) : x.vis;
+        lim[nt][e] = rr < x.rows ? seen_by(p, x, x.r0 + rr) : x.vis;
       }
     }
-    const int minlim = min(max(x.len - x.nq + x.r0 / p.G + 1, 0), x.vis);
+    const int minlim = seen_by(p, x, x.r0);
 
     float o[NT][KS][4];
     float ref[NT][2], l[NT][2];  // reference minus kOff (0 until a token is seen), this lane's part of the sum
@@ -452,8 +451,7 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
           const int rr = nt * 8 + 2 * t + e;
           if (rr >= x.rows) continue;
           if (whole) {
-            const int r = x.r0 + rr;
-            const size_t at = ((size_t)x.b * a.T + r / p.G) * a.Hq + x.h * p.G + r % p.G;
+            const size_t at = out_row(a, p, x, x.r0 + rr);
             const float inv = l[nt][e] == 0.f ? 0.f : a.g.ts[1] / l[nt][e];
             T* op = static_cast<T*>(a.out) + at * D + CPV * g;
 #pragma unroll
@@ -531,13 +529,12 @@ __global__ void __launch_bounds__(kCombThreads) combine_kernel(AttendArgs a, Att
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = SPLIT ? blockIdx.x : blockIdx.x * kCombWarps + warp;
-  const int vs = row / p.rb, rr = row % p.rb;
+  const int vs = row >> p.lrb, rr = row & (p.rb - 1);
   if (vs >= p.nvs) return;
   const int2 span = p.span[vs];  // read beside the length; undefined for a stream without units
   const Stream x = stream_of(a, p, vs, lane == 0 && rr == 0);
   if (rr >= x.rows) return;
-  const int r = x.r0 + rr;
-  const size_t at = ((size_t)x.b * a.T + r / p.G) * a.Hq + x.h * p.G + r % p.G;
+  const size_t at = out_row(a, p, x, x.r0 + rr);
   T* op = static_cast<T*>(a.out) + at * D;
   constexpr int E = D / 32;
   if (x.vis == 0) {
@@ -566,6 +563,47 @@ __global__ void __launch_bounds__(kCombThreads) combine_kernel(AttendArgs a, Att
   if (a.lse && lane == 0) a.lse[at] = y.l == 0.f ? -INFINITY : (y.m + log2f(y.l)) * 0.6931471805599453f;
 }
 
+// The tcgen05 kernel's parts lie with the rows contiguous: a thread a row, 16 channels a CTA.
+template <typename T, int D>
+__global__ void __launch_bounds__(kTcRows) combine_tc_kernel(AttendArgs a, AttendPlan p) {
+  griddep_launch();
+  griddep_wait();
+  constexpr int C = 16, kPer = D / C;
+  const int vs = blockIdx.x / kPer, c0 = blockIdx.x % kPer * C, rr = threadIdx.x;
+  const int2 span = p.span[vs];
+  const Stream x = stream_of(a, p, vs, rr == 0);
+  if (rr >= x.rows || (x.vis && span.x == span.y)) return;
+  float o[C], l = 0.f, m = -INFINITY;
+#pragma unroll
+  for (int e = 0; e < C; ++e) o[e] = 0.f;
+  if (x.vis) {
+    for (int c = span.x; c <= span.y; ++c) {
+      const size_t slot = (size_t)c * 2 + (c == span.x ? 1 : 0);
+      const float2 ml = p.ml[slot * kTcRows + rr];
+      const float* src = p.part + (slot * D + c0) * kTcRows + rr;
+      float y[C];
+#pragma unroll
+      for (int e = 0; e < C; ++e) y[e] = src[e * kTcRows];
+      if (ml.y == 0.f) continue;
+      const float to = l == 0.f ? ml.x : fmaxf(m, ml.x);
+      const float k0 = l == 0.f ? 0.f : ex2(m - to), k1 = ex2(ml.x - to);
+      l = l * k0 + ml.y * k1;
+#pragma unroll
+      for (int e = 0; e < C; ++e) o[e] = o[e] * k0 + y[e] * k1;
+      m = to;
+    }
+  }
+  const size_t at = out_row(a, p, x, x.r0 + rr);
+  const float inv = l == 0.f ? 0.f : a.g.ts[1] / l;
+  alignas(16) T y[C];
+#pragma unroll
+  for (int e = 0; e < C; ++e) y[e] = from_f32<T>(o[e] * inv);
+  uint4* op = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + at * D + c0);
+#pragma unroll
+  for (int e = 0; e < (int)sizeof(y) / 16; ++e) op[e] = reinterpret_cast<const uint4*>(y)[e];
+  if (a.lse && c0 == 0) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
 // Row tiles of 8 a block takes: one covers the decode step of up to 8 query heads per KV head; more rows
 // share the decoding of a chunk. From kTcMin rows on bf16 queries go to the tcgen05 kernel.
 constexpr int kTcMin = 33;
@@ -581,6 +619,10 @@ AttendPlan make_plan(const AttendArgs& a, int parts, int sms, size_t* bytes) {
   p.rb = tc ? kTcRows : 8 * nt;
   p.nrb = (R + p.rb - 1) / p.rb;
   p.nvs = a.t.S * p.nrb;
+  p.by_nrb = FastDiv::make(p.nrb);
+  p.by_hkv = FastDiv::make(a.t.Hkv);
+  p.by_G = FastDiv::make(p.G);
+  while ((1 << p.lrb) < p.rb) ++p.lrb;
   p.grid = (sms < kMaxGridSMs ? sms : kMaxGridSMs) * (tc ? 1 : min_blocks(nt, parts));
   const long long units = (long long)p.nvs * ((((long long)a.t.maxp << a.g.lp) + p.unit - 1) / p.unit);
   if (units < p.grid) p.grid = (int)units;
@@ -618,6 +660,12 @@ int run(const AttendArgs& a, int sms, cudaStream_t s) {
   }
   if (rc) return rc;
   const long long rows = (long long)p.nvs * p.rb;
+  if constexpr (PARTS == 1)
+    if (p.rb == kTcRows)
+      return launch_pdl(combine_tc_kernel<T, D>, dim3((unsigned)(p.nvs * (D / 16))), dim3(kTcRows), 0, s, false, a, p) ==
+                     cudaSuccess
+                 ? KVC_OK
+                 : KVC_ERR_LAUNCH;
   const cudaError_t e =
       p.rb <= 16 ? launch_pdl(combine_kernel<T, D, true>, dim3((unsigned)rows), dim3(kCombThreads), 0, s, false, a, p)
                  : launch_pdl(combine_kernel<T, D, false>, dim3((unsigned)((rows + kCombWarps - 1) / kCombWarps)),

@@ -13,11 +13,12 @@ constexpr float kRaise = 5.f;  // a reference may lag the maximum by 2^5: 2^15 a
 struct AttendPlan {
   int unit;    // tokens of a work unit
   int nrb;     // row blocks per stream
-  int rb;      // rows per block
+  int rb, lrb;  // rows per block (a power of two) and its logarithm
   int G;
   int nvs;     // streams * nrb
+  FastDiv by_nrb, by_hkv, by_G;
   int grid;    // CTAs of the main kernel
-  float* part;  // [grid][2][rb][D]
+  float* part;  // [grid][2][rb][D] (tcgen05 kernel: [grid][2][D][rb])
   float2* ml;   // [grid][2][rb] (reference, sum)
   int2* span;   // [nvs] first and last CTA of a stream's units (streams with units only)
 };
@@ -28,10 +29,10 @@ struct Stream {  // what a (stream, row block) has to see
 
 __device__ __forceinline__ Stream stream_of(const AttendArgs& a, const AttendPlan& p, int vs, bool report) {
   Stream x;
-  x.s = vs / p.nrb;
-  x.r0 = (vs % p.nrb) * p.rb;
-  x.b = x.s / a.t.Hkv;
-  x.h = x.s % a.t.Hkv;
+  x.s = p.by_nrb.div(vs);
+  x.r0 = (vs - x.s * p.nrb) * p.rb;
+  x.b = p.by_hkv.div(x.s);
+  x.h = x.s - x.b * a.t.Hkv;
   x.len = a.t.len[x.s];
   x.nq = a.n_q ? min(max(a.n_q[x.b], 0), a.T) : a.T;
   if (x.len < 0 || x.len > ((long long)a.t.maxp << a.g.lp)) {
@@ -39,9 +40,22 @@ __device__ __forceinline__ Stream stream_of(const AttendArgs& a, const AttendPla
     x.len = 0;
   }
   x.rows = max(0, min(p.rb, x.nq * p.G - x.r0));
-  const int tmax = min((x.r0 + p.rb - 1) / p.G, x.nq - 1);
+  const int tmax = min(p.by_G.div(x.r0 + p.rb - 1), x.nq - 1);
   x.vis = x.rows ? max(0, x.len - x.nq + tmax + 1) : 0;
   return x;
+}
+// Row r of a stream's block: its query token and, with it, offsets in q and out.
+__device__ __forceinline__ long long q_row(const AttendArgs& a, const AttendPlan& p, const Stream& x, int r) {
+  const int t = p.by_G.div(r);
+  return x.b * a.qs.b + t * a.qs.t + (x.h * p.G + r - t * p.G) * a.qs.h;
+}
+__device__ __forceinline__ size_t out_row(const AttendArgs& a, const AttendPlan& p, const Stream& x, int r) {
+  const int t = p.by_G.div(r);
+  return ((size_t)x.b * a.T + t) * a.Hq + x.h * p.G + r - t * p.G;
+}
+// tokens that row r sees
+__device__ __forceinline__ int seen_by(const AttendPlan& p, const Stream& x, int r) {
+  return min(max(x.len - x.nq + p.by_G.div(r) + 1, 0), x.vis);
 }
 __device__ __forceinline__ int units_of(const AttendPlan& p, const Stream& x) { return (x.vis + p.unit - 1) / p.unit; }
 

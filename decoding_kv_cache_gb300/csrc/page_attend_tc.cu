@@ -11,11 +11,11 @@
 //                           128-byte-swizzled layout, two stages each. V's tile [token][channel] is the
 //                           second product's B operand as it lies, channels contiguous (MN-major).
 //   issuer    (warp 17)     S_i = Q K_i, then P_{i-1} V_{i-1}
-//   softmax   (warps 0-7)   two groups, even and odd units, each with its own S, O and running maximum
-//                           and sum (a thread a row), so that one exponentiates while the other's product
-//                           runs, and no rescaling of one O waits for the other. P replaces S in tensor
-//                           memory (fp16, the A operand). O is rescaled in place, and only when a row's
-//                           maximum has risen by more than 2^kRaise.
+//   softmax   (warps 0-7)   two groups, a unit's first and last 64 tokens, each with its own O and running
+//                           maximum and sum (a thread a row): neither waits for the other. S has two
+//                           buffers, so the next unit's logits lie ready. P replaces S in tensor memory
+//                           (fp16, the A operand). O is rescaled in place, and only when a row's maximum
+//                           has risen by more than 2^kRaise.
 //
 // At a part's end the groups' O are merged and written (whole streams) or left for the combine kernel.
 // All waits are bounded; a role that gives up raises KVC_STATUS_TIMEOUT and the others follow.
@@ -32,6 +32,7 @@ constexpr int kThreads = 32 * (kSoftWarps + kDecWarps + 2);
 constexpr int kRaw = 3;   // stages of raw units
 constexpr int kTiles = 2;  // stages of decoded tiles
 constexpr uint32_t kTmemCols = 512, kColO = 256;
+constexpr int kHalfTok = kTcUnit / 2;  // a softmax group's tokens of a unit
 
 template <int D>
 struct Lay {
@@ -44,7 +45,7 @@ struct Lay {
 
 struct Bars {
   uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[kTiles], k_empty[kTiles], v_full[kTiles], v_empty[kTiles];
-  uint64_t s_full[2], p_full[2], pv_done[2], q_full, merge;
+  uint64_t s_full[2], p_full[2][2], pv_done[2], q_full, merge;  // p_full: S buffer, group (a group may be a unit ahead)
 };
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
@@ -186,7 +187,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
       tc::mbar_init(&bars.v_empty[i], 1);
       tc::mbar_init(&bars.s_full[i], 1);
       tc::mbar_init(&bars.pv_done[i], 1);
-      tc::mbar_init(&bars.p_full[i], 4);
+      tc::mbar_init(&bars.p_full[i][0], 4);
+      tc::mbar_init(&bars.p_full[i][1], 4);
     }
     tc::mbar_init(&bars.q_full, kSoftWarps);
     tc::mbar_init(&bars.merge, kSoftWarps);
@@ -269,13 +271,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
     const uint64_t dq = tc::desc_k_sw128(tc::smem_u32(smem)), dk = tc::desc_k_sw128(tc::smem_u32(smem + L::oK)),
                    dv = desc_mn_sw128(tc::smem_u32(smem + L::oV), L::kHalf);
     const bool leader = elect_one();
-    uint32_t nk = 0, nv = 0, np[2] = {0, 0}, seg = 0;
+    uint32_t nk = 0, nv = 0, seg = 0;
     parts([&](const Stream&, int, int ua, int ub, int, int) {
       const int m = ub - ua;
       if (!wait(&bars.q_full, seg++ & 1)) return false;
       for (int i = 0; i <= m; ++i) {
         if (i < m) {
-          const int t = nk & 1, w = i & 1;
+          const int t = nk & 1;
           if (!wait(&bars.k_full[t], (nk >> 1) & 1)) return false;
           tc::fence_after_sync();
           if (leader) {
@@ -284,26 +286,32 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
             for (int j = 0; j < D / 16; ++j) {
               constexpr int step = 32 >> 4;
               const uint64_t at = (j >> 2) * (L::kHalf >> 4) + (j & 3) * step;
-              umma_ss(tmem + w * 128, dq + at, d + at, id_qk, j > 0);
+              umma_ss(tmem + t * 128, dq + at, d + at, id_qk, j > 0);
             }
             tc::umma_commit(&bars.k_empty[t]);
-            tc::umma_commit(&bars.s_full[w]);
+            tc::umma_commit(&bars.s_full[t]);
           }
           __syncwarp();
           ++nk;
         }
         if (i > 0) {
-          const int t = nv & 1, w = (i - 1) & 1;
-          if (!wait(&bars.v_full[t], (nv >> 1) & 1) || !wait(&bars.p_full[w], np[w]++ & 1)) return false;
-          tc::fence_after_sync();
-          if (leader) {
-            const uint64_t d = dv + (uint64_t)(t * (L::kTile >> 4));
+          const int t = nv & 1;
+          if (!wait(&bars.v_full[t], (nv >> 1) & 1)) return false;
 #pragma unroll
-            for (int j = 0; j < kTcUnit / 16; ++j)
-              umma_ts(tmem + kColO + w * 128, tmem + w * 128 + 8 * j, d + j * (2048 >> 4), id_pv, i > 2 || j > 0);
-            tc::umma_commit(&bars.v_empty[t]);
-            tc::umma_commit(&bars.pv_done[w]);
+          for (int w = 0; w < 2; ++w) {
+            if (!wait(&bars.p_full[t][w], (nv >> 1) & 1)) return false;
+            tc::fence_after_sync();
+            if (leader) {
+              const uint64_t d = dv + (uint64_t)(t * (L::kTile >> 4) + w * (kHalfTok * 128 >> 4));
+#pragma unroll
+              for (int j = 0; j < kHalfTok / 16; ++j)
+                umma_ts(tmem + kColO + w * 128, tmem + t * 128 + w * kHalfTok + 8 * j, d + j * (2048 >> 4), id_pv,
+                        i > 1 || j > 0);
+              tc::umma_commit(&bars.pv_done[w]);
+            }
+            __syncwarp();
           }
+          if (leader) tc::umma_commit(&bars.v_empty[t]);
           __syncwarp();
           ++nv;
         }
@@ -341,66 +349,68 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
     // ---- softmax -------------------------------------------------------------------------------
     const int w = warp >> 2, rr = threadIdx.x & 127;  // group, row
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's quarter of the lanes
-    const uint32_t tS = tmem + w * 128 + lanes, tO = tmem + kColO + w * 128 + lanes;
-    uint32_t ns = 0, unit0 = 0, seg = 0;  // units of this group and of the CTA so far
+    const uint32_t tO = tmem + kColO + w * 128 + lanes;
+    uint32_t n = 0, seg = 0;  // units so far
     parts([&](const Stream& x, int vs, int ua, int ub, int U, int base) {
       const int m = ub - ua;
       {
         // the query rows, each brought to [256, 512) by a power of two (bf16 values exact in fp16), with the
         // scale's sign, so that maxima of dot products are maxima of logits. A warp takes 16 rows, D/8 lanes
-        // a row, all of its reads in flight at once.
-        constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // lanes of a row, rows at a time
-        uint4 v[16 / kAt];
+        // a row, four reads in flight.
+        constexpr int kLanes = D / 8, kAt = 32 / kLanes, kBatch = 4;  // lanes of a row, rows at a time, reads in flight
         const int i = lane % kLanes;
+#pragma unroll 1
+        for (int k0 = 0; k0 < 16 / kAt; k0 += kBatch) {
+          uint4 v[kBatch];
 #pragma unroll
-        for (int k = 0; k < 16 / kAt; ++k) {
-          const int q = warp * 16 + k * kAt + lane / kLanes, r = x.r0 + q;
-          v[k] = make_uint4(0u, 0u, 0u, 0u);
-          if (q < x.rows)
-            v[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + x.b * a.qs.b + (r / p.G) * a.qs.t +
-                                                        (x.h * p.G + r % p.G) * a.qs.h) + i);
-        }
+          for (int k = 0; k < kBatch; ++k) {
+            const int q = warp * 16 + (k0 + k) * kAt + lane / kLanes;
+            v[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (q < x.rows)
+              v[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + q_row(a, p, x, x.r0 + q)) + i);
+          }
 #pragma unroll
-        for (int k = 0; k < 16 / kAt; ++k) {
-          const int q = warp * 16 + k * kAt + lane / kLanes;
-          const T* e = reinterpret_cast<const T*>(&v[k]);
-          float mx = 0.f;
+          for (int k = 0; k < kBatch; ++k) {
+            const int q = warp * 16 + (k0 + k) * kAt + lane / kLanes;
+            const T* e = reinterpret_cast<const T*>(&v[k]);
+            float mx = 0.f;
 #pragma unroll
-          for (int c = 0; c < 8; ++c) mx = fmaxf(mx, fabsf(to_f32(e[c])));
+            for (int c = 0; c < 8; ++c) mx = fmaxf(mx, fabsf(to_f32(e[c])));
 #pragma unroll
-          for (int c = kLanes / 2; c; c >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, c));
-          const int ex = max((int)(__float_as_uint(mx) >> 23), 24);
-          const float mul = copysignf(__uint_as_float((uint32_t)(262 - ex) << 23), a.scale);
-          if (i == 0) row_f[q] = __uint_as_float((uint32_t)(ex - 8) << 23) * (fabsf(a.scale) * kLog2e);
-          uint32_t o[4];
+            for (int c = kLanes / 2; c; c >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, c));
+            const int ex = max((int)(__float_as_uint(mx) >> 23), 24);
+            const float mul = copysignf(__uint_as_float((uint32_t)(262 - ex) << 23), a.scale);
+            if (i == 0) row_f[q] = __uint_as_float((uint32_t)(ex - 8) << 23) * (fabsf(a.scale) * kLog2e);
+            uint32_t o[4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) o[c] = pack2(to_f32(e[2 * c]) * mul, to_f32(e[2 * c + 1]) * mul);
-          *reinterpret_cast<uint4*>(smem + (i >> 3) * L::kHalf + q * 128 + (((i & 7) ^ (q & 7)) << 4)) =
-              make_uint4(o[0], o[1], o[2], o[3]);
+            for (int c = 0; c < 4; ++c) o[c] = pack2(to_f32(e[2 * c]) * mul, to_f32(e[2 * c + 1]) * mul);
+            *reinterpret_cast<uint4*>(smem + (i >> 3) * L::kHalf + q * 128 + (((i & 7) ^ (q & 7)) << 4)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+          }
         }
         fence_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.q_full);
       }
-      const int lim = rr < x.rows ? min(max(x.len - x.nq + (x.r0 + rr) / p.G + 1, 0), x.vis) : x.vis;
-      const int minlim = min(max(x.len - x.nq + x.r0 / p.G + 1, 0), x.vis);
+      const int lim = rr < x.rows ? seen_by(p, x, x.r0 + rr) : x.vis;
+      const int minlim = seen_by(p, x, x.r0);
       float ref = 0.f, l = 0.f;
       bool none = true;
       // the query rows' factors were written before q_full, which precedes every s_full
       float f = 0.f;
-      for (int i = w; i < m; i += 2, ++ns) {
-        if (!wait(&bars.s_full[w], ns & 1)) return false;
+      for (int i = 0; i < m; ++i, ++n) {
+        const uint32_t tS = tmem + (n & 1) * 128 + w * kHalfTok + lanes;
+        if (!wait(&bars.s_full[n & 1], (n >> 1) & 1)) return false;
         tc::fence_after_sync();
         f = *reinterpret_cast<volatile float*>(&row_f[rr]);
-        const int tok0 = (ua + i) * kTcUnit;
-        const uint32_t ok = *reinterpret_cast<volatile uint32_t*>(&unit_ok[(unit0 + i) & 3]);
-        const bool masked = tok0 + kTcUnit > minlim || ok != 0xff;
+        const int tok0 = (ua + i) * kTcUnit + w * kHalfTok;
+        const uint32_t ok = *reinterpret_cast<volatile uint32_t*>(&unit_ok[n & 3]) >> (4 * w) & 0xf;
+        const bool masked = tok0 + kHalfTok > minlim || ok != 0xf;
         float mx = -INFINITY;
-#pragma unroll 1
-        for (int c = 0; c < 4; c += 2) {
+        {
           uint32_t r[2][32];
-          tc::tmem_ld32_async(tS + 32 * c, r[0]);
-          tc::tmem_ld32_async(tS + 32 * c + 32, r[1]);
+          tc::tmem_ld32_async(tS, r[0]);
+          tc::tmem_ld32_async(tS + 32, r[1]);
           tc::tmem_wait();
           tc::tmem_regs_ready(r[0]);
           tc::tmem_regs_ready(r[1]);
@@ -412,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
             if (masked) {
 #pragma unroll
               for (int k = 0; k < 32; ++k)
-                if (tok0 + 32 * (c + h) + k >= lim || !(ok >> (2 * (c + h) + (k >> 4)) & 1)) v[k] = -INFINITY;
+                if (tok0 + 32 * h + k >= lim || !(ok >> (2 * h + (k >> 4)) & 1)) v[k] = -INFINITY;
             }
             mx = fmaxf(mx, tree_max32_3(v));
           }
@@ -429,8 +439,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
             ref = to;
             l *= c;
           }
-          if (i >= 2 && __any_sync(kFull, c != 1.f)) {  // O holds the group's earlier units
-            if (!wait(&bars.pv_done[w], (ns - 1) & 1)) return false;
+          if (i > 0 && __any_sync(kFull, c != 1.f)) {  // O holds the part's earlier units
+            if (!wait(&bars.pv_done[w], (n - 1) & 1)) return false;
             tc::fence_after_sync();
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
@@ -477,14 +487,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
         auto sweep = [&](auto with_mask) {
           tmem_ld16(tS, s0);
 #pragma unroll 1
-          for (int c = 0; c < 8; c += 2) {
+          for (int c = 0; c < kHalfTok / 16; c += 2) {
             tc::tmem_wait();
             tc::tmem_regs_ready(s0);
             tmem_ld16(tS + 16 * c + 16, s1);
             probabilities(s0, c, with_mask);
             tc::tmem_wait();
             tc::tmem_regs_ready(s1);
-            if (c + 2 < 8) tmem_ld16(tS + 16 * c + 32, s0);
+            if (c + 2 < kHalfTok / 16) tmem_ld16(tS + 16 * c + 32, s0);
             probabilities(s1, c + 1, with_mask);
           }
         };
@@ -496,13 +506,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
         tmem_st_wait();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.p_full[w]);
+        if (lane == 0) mbar_arrive(&bars.p_full[n & 1][w]);
       }
-      unit0 += m;
       // ---- the groups' results together
-      if (m > w) {
-        if (!wait(&bars.pv_done[w], (ns - 1) & 1)) return false;
-      }
+      if (!wait(&bars.pv_done[w], (n - 1) & 1)) return false;
       tc::fence_after_sync();
       row_ml[w][rr] = make_float2(ref, l);
       tc::fence_before_sync();
@@ -511,47 +518,40 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
       if (!wait(&bars.merge, seg & 1)) return false;
       tc::fence_after_sync();
       const float2 y0 = row_ml[0][rr], y1 = row_ml[1][rr];
-      const bool two = m > 1;
       const float mm = y1.y > 0.f ? (y0.y > 0.f ? fmaxf(y0.x, y1.x) : y1.x) : y0.x;
-      float c0 = y0.y > 0.f ? ex2(y0.x - mm) : 0.f, c1 = two && y1.y > 0.f ? ex2(y1.x - mm) : 0.f;
+      float c0 = y0.y > 0.f ? ex2(y0.x - mm) : 0.f, c1 = y1.y > 0.f ? ex2(y1.x - mm) : 0.f;
       if (y0.y != y0.y || y1.y != y1.y) c0 = NAN;
-      const float ll = y0.y * c0 + (two ? y1.y * c1 : 0.f);
+      const float ll = y0.y * c0 + y1.y * c1;
       const bool whole = ua == 0 && ub == U;
       if (ua == 0 && threadIdx.x == 0)
         p.span[vs] = make_int2(blockIdx.x, whole ? (int)blockIdx.x : split.owner(base + U - 1));
-      const int r = x.r0 + rr;
-      const size_t at = ((size_t)x.b * a.T + r / p.G) * a.Hq + x.h * p.G + r % p.G;
-      const size_t prow = ((size_t)blockIdx.x * 2 + (ua == 0 ? 1 : 0)) * kTcRows + rr;
+      const size_t at = out_row(a, p, x, x.r0 + rr);
+      const size_t slot = (size_t)blockIdx.x * 2 + (ua == 0 ? 1 : 0), prow = slot * kTcRows + rr;
       const float inv = ll == 0.f ? 0.f : a.g.ts[1] / ll;
       constexpr int kCols = D / 2;  // each group writes half of the channels
+#pragma unroll 1
+      for (int k = w * kCols; k < (w + 1) * kCols; k += 16) {
+        uint32_t o0[16], o1[16];
+        tmem_ld16(tmem + kColO + lanes + k, o0);
+        tmem_ld16(tmem + kColO + lanes + k + 128, o1);
+        tc::tmem_wait();
+        tc::tmem_regs_ready(o0);
+        tc::tmem_regs_ready(o1);
+        float o[16];
 #pragma unroll
-      for (int k = 0; k < kCols; k += 32) {
-        const uint32_t col = tmem + kColO + lanes + w * kCols + k;
-        float o0[32];
-        tc::tmem_ld32(col, o0);
-#pragma unroll
-        for (int e = 0; e < 32; ++e) o0[e] *= c0;
-        if (two) {
-          float o1[32];
-          tc::tmem_ld32(col + 128, o1);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o0[e] = c1 == 0.f ? o0[e] : fmaf(o1[e], c1, o0[e]);
-        }
+        for (int e = 0; e < 16; ++e) o[e] = fmaf(__uint_as_float(o1[e]), c1, __uint_as_float(o0[e]) * c0);
         if (rr < x.rows) {
           if (whole) {
-            T* op = static_cast<T*>(a.out) + at * D + w * kCols + k;
+            alignas(16) T y[16];
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              alignas(16) T y[8];
+            for (int e = 0; e < 16; ++e) y[e] = from_f32<T>(o[e] * inv);
+            uint4* op = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + at * D + k);
+            op[0] = reinterpret_cast<const uint4*>(y)[0];
+            op[1] = reinterpret_cast<const uint4*>(y)[1];
+          } else {  // rows contiguous: a warp's store is one line
+            float* op = p.part + (slot * D + k) * kTcRows + rr;
 #pragma unroll
-              for (int i = 0; i < 8; ++i) y[i] = from_f32<T>(ll == 0.f ? 0.f : o0[e + i] * inv);
-              *reinterpret_cast<uint4*>(op + e) = *reinterpret_cast<const uint4*>(y);
-            }
-          } else {
-            float* op = p.part + prow * D + w * kCols + k;
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4*>(op + e) = make_float4(o0[e], o0[e + 1], o0[e + 2], o0[e + 3]);
+            for (int e = 0; e < 16; ++e) op[e * kTcRows] = o[e];
           }
         }
       }

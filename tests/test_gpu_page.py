@@ -365,6 +365,45 @@ def test_attend_long(dt, D, B, Hkv, G, T, n):
     check_attend(x, q, dt)
 
 
+@pytest.mark.parametrize("dt,D,G,T,n", [("bf16", 128, 4, 33, 120000), ("bf16", 64, 8, 20, 150000), ("bf16", 128, 5, 1, 60000),
+                                         ("f32", 64, 2, 3, 40000)])
+def test_attend_many_units_a_cta(dt, D, G, T, n):
+    """Long streams: dozens of work units for every CTA, the model's product formed on the GPU in 64 bits."""
+    from decoding_kv_cache_gb300 import kvc
+    B, Hkv, page = 2, 1, 256
+    maxp = R.npg(n, page)
+    pool, pages = kvc.Pool.empty(2 * maxp + 3, D, page, device=DEV), kvc.Pages.empty(1, B, Hkv, maxp, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    start = torch.zeros((1, B, Hkv), dtype=torch.int32, device=DEV)
+    lens = torch.tensor([n, n - 777], dtype=torch.int32, device=DEV)
+    kvc.kvc_page_extend(pool, pages, add=lens, start=start, status=status)
+    g = torch.Generator(device=DEV).manual_seed(n)
+    k, v = (torch.randn((B, n, Hkv, D), generator=g, device=DEV).to(DT[dt]) for _ in range(2))
+    kvc.kvc_page_store(pool, pages, k, v, start, n=lens, status=status)
+    q = (2 * torch.randn((B, T, Hkv * G, D), generator=g, device=DEV)).to(DT[dt])
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:3], device=DEV)
+    kvc.kvc_page_attend(pool, pages, q, out, lse=lse, status=status)
+    K = torch.zeros((1, B, Hkv, n, D), device=DEV)
+    V = torch.zeros_like(K)
+    kvc.kvc_page_read(pool, pages, K, V, status=status)
+    assert int(status.item()) == 0
+    for b in range(B):
+        m = int(lens[b])
+        kk, vv = K[0, b, 0, :m].double(), V[0, b, 0, :m].double()
+        for i in (0, T // 2, T - 1):
+            seen = m - T + i + 1
+            qq = q[b, i].double()
+            s = qq @ kk[:seen].T / D ** 0.5
+            z = torch.logsumexp(s, -1)
+            p = torch.exp(s - z[:, None])
+            ref = dict(out=p @ vv[:seen], lse=z, mass=p @ vv[:seen].abs(), vmax=vv[:seen].abs().amax(0) + 0 * qq,
+                       logit=(qq.abs() @ kk[:seen].abs().T / D ** 0.5).amax(-1))
+            ref = {name: x.cpu().numpy() for name, x in ref.items()}
+            tol, ltol = R.tolerances(dt, seen, D, ref)
+            assert (np.abs(out[b, i].double().cpu().numpy() - ref["out"]) <= tol).all()
+            assert (np.abs(lse[b, i].double().cpu().numpy() - ref["lse"]) <= ltol).all()
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_attend_strided_ragged_scaled(dt):
     x, q0 = make_attend(dt, 128, 4, 2, 3, 6, 32, [90, 80, 3, 4, 50, 60, 0, 0], seed=5, k_scale=0.3, v_scale=7.0)
