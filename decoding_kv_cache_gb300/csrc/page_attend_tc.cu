@@ -132,31 +132,30 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 
 // A token's codes and scales to a row of fp16 in the swizzled tile; zero: the row stands for nothing.
+// Lanes hold neighbouring tokens, whose 16-byte code vectors lie D/2 bytes apart: each lane begins at another
+// vector of its row, so that eight lanes' reads fall on eight different bank groups (with all lanes at the
+// same vector, four of them met on one: the shared memory, which the first product reads too, is what
+// bounds this kernel). Their stores, of different chunks, still differ in every chunk's low bits.
 template <int D>
 __device__ __forceinline__ void decode_row(const uint8_t* codes, const uint8_t* scales, uint8_t* tile, int j, bool zero) {
-  uint32_t sc[D / 16];
-  if constexpr (D == 128) {
-    const uint2 v = *reinterpret_cast<const uint2*>(scales);
+  constexpr int V = D / 32;  // code vectors of a row
+  // the tile is 1024-byte aligned: 16-byte chunk c of row j lies at (row + (j & 7) 16) ^ c 16
+  const uint32_t row = tc::smem_u32(tile) + j * 128 + ((j & 7) << 4);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sc[i] = (i < 4 ? v.x : v.y) >> (8 * (i & 3)) & 0xff;
-  } else {
-    const uint32_t v = *reinterpret_cast<const uint32_t*>(scales);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sc[i] = v >> (8 * i) & 0xff;
-  }
-#pragma unroll
-  for (int q = 0; q < D / 32; ++q) {  // 16 bytes of codes: two scale groups
-    const uint4 w4 = reinterpret_cast<const uint4*>(codes)[q];
+  for (int q = 0; q < V; ++q) {
+    const int c = (q + (D == 128 ? j >> 1 : j >> 2)) & (V - 1);  // 32 channels: two scale groups, four chunks
+    const uint4 w4 = reinterpret_cast<const uint4*>(codes)[c];
     const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-    const uint32_t two = zero ? 0u : e4m3x2_f16x2(sc[2 * q] | sc[2 * q + 1] << 8);
+    const uint32_t two = zero ? 0u : e4m3x2_f16x2(reinterpret_cast<const uint16_t*>(scales)[c]);
     const uint32_t s2[2] = {__byte_perm(two, two, 0x1010), __byte_perm(two, two, 0x3232)};
+    const uint32_t at = (row ^ ((c & 1) << 6)) + (c >> 1) * Lay<D>::kHalf;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t r[4];
       e2m1x8_f16(w[i], r);
-      const int chunk = 4 * q + i;  // of 8 channels
-      *reinterpret_cast<uint4*>(tile + (chunk >> 3) * Lay<D>::kHalf + j * 128 + (((chunk & 7) ^ (j & 7)) << 4)) =
-          make_uint4(hmul2(r[0], s2[i >> 1]), hmul2(r[1], s2[i >> 1]), hmul2(r[2], s2[i >> 1]), hmul2(r[3], s2[i >> 1]));
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(at ^ (i << 4)), "r"(hmul2(r[0], s2[i >> 1])),
+                   "r"(hmul2(r[1], s2[i >> 1])), "r"(hmul2(r[2], s2[i >> 1])), "r"(hmul2(r[3], s2[i >> 1]))
+                   : "memory");
     }
   }
 }
