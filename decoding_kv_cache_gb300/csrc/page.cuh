@@ -95,7 +95,11 @@ __device__ __forceinline__ float2 f16x2_f32(uint32_t h) {
 }
 __device__ __forceinline__ float e4m3_f32(uint32_t b) { return f16x2_f32(e4m3x2_f16x2(b)).x; }
 
+enum { kCompactBad = 1, kCompactMoves = 2 };  // PageWs::plan.w
+
 // ---- launchers (arguments already validated) ---------------------------------------------------
+int page_push(const PoolGeom& g, const PageWs& w, cudaStream_t s);                              // marked pages to the free list
+int page_finish_compact(const PoolGeom& g, const PageTab& t, const PageWs& w, cudaStream_t s);  // and what a compaction leaves
 int launch_page_init(const PoolGeom& g, const PageTab* t, cudaStream_t s);
 int launch_page_extend(const PoolGeom& g, const PageTab& t, const int32_t* add, int add_all, int32_t* start,
                        int32_t* status, const PageWs& w, cudaStream_t s);

@@ -73,27 +73,41 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
   griddep_wait();
 
   // this CTA's units, and the stream its first one lies in
-  const int per = (p.nvs + 32 * kWarps - 1) / (32 * kWarps);
-  int W;
-  int before = scan_units<32 * kWarps>(a, p, sm_scan, per, &W);
-  const Split split(W, p.grid);
-  const int w0 = split.first(blockIdx.x), w1 = split.first(blockIdx.x + 1);
-  if (w0 >= w1) return;
-  for (int i = 0; i < per; ++i) {
-    const int vs = threadIdx.x * per + i;
-    if (vs >= p.nvs) break;
-    const int u = units_of(p, stream_of(a, p, vs, false));
-    if (before <= w0 && w0 < before + u) {
-      sm_first[0] = vs;
-      sm_first[1] = before;
+  int vs = blockIdx.x, base = 0, ua = 0, left = 1;  // whole: `left` becomes the stream's units
+  Split split(0, 1);
+  if (!p.whole) {
+    const int per = (p.nvs + 32 * kWarps - 1) / (32 * kWarps);
+    int W;
+    int before = scan_units<32 * kWarps>(a, p, sm_scan, per, &W);
+    split = Split(W, p.grid);
+    const int w0 = split.first(blockIdx.x), w1 = split.first(blockIdx.x + 1);
+    if (w0 >= w1) return;
+    for (int i = 0; i < per; ++i) {
+      const int v = threadIdx.x * per + i;
+      if (v >= p.nvs) break;
+      const int u = units_of(p, stream_of(a, p, v, false));
+      if (before <= w0 && w0 < before + u) {
+        sm_first[0] = v;
+        sm_first[1] = before;
+      }
+      before += u;
     }
-    before += u;
+    __syncthreads();
+    vs = sm_first[0];
+    base = sm_first[1];  // units before the stream
+    ua = w0 - base;      // first unit of this CTA in the stream
+    left = w1 - w0;
+  } else {
+    const Stream x = stream_of(a, p, vs, threadIdx.x == 0);
+    left = units_of(p, x);
+    if (left == 0)  // rows that see nothing
+      for (int e = threadIdx.x; e < x.rows * D; e += 32 * kWarps) {
+        const size_t at = out_row(a, p, x, x.r0 + e / D);
+        static_cast<T*>(a.out)[at * D + e % D] = from_f32<T>(0.f);
+        if (a.lse && e % D == 0) a.lse[at] = -INFINITY;
+      }
+    __syncwarp();  // the barriers of this warp's ring are visible to its lanes
   }
-  __syncthreads();
-  int vs = sm_first[0];
-  int base = sm_first[1];     // units before the stream
-  int ua = w0 - base;         // first unit of this CTA in the stream
-  int left = w1 - w0;
   uint32_t n = 0;  // chunks this warp has waited for
   bool alive = true;
 
@@ -442,7 +456,7 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
     if (warp == 0) {
       const bool whole = ua == 0 && ub == U;
       // who holds the stream's parts, for the combine kernel
-      if (ua == 0 && lane == 0) p.span[vs] = make_int2(blockIdx.x, whole ? (int)blockIdx.x : split.owner(base + U - 1));
+      if (!p.whole && ua == 0 && lane == 0) p.span[vs] = make_int2(blockIdx.x, whole ? (int)blockIdx.x : split.owner(base + U - 1));
       const size_t slot = (size_t)blockIdx.x * 2 + (ua == 0 ? 1 : 0);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -607,6 +621,10 @@ __global__ void __launch_bounds__(kTcRows) combine_tc_kernel(AttendArgs a, Atten
 // Row tiles of 8 a block takes: one covers the decode step of up to 8 query heads per KV head; more rows
 // share the decoding of a chunk. From kTcMin rows on bf16 queries go to the tcgen05 kernel.
 constexpr int kTcMin = 33;
+// Tables of at most kWholeCap tokens: a CTA takes a whole stream, which saves the search for its units and the
+// second kernel (8 heads x 256 tokens: 6.9 us split, 5.9 whole; x 2048: 8.5 and 18.7). With two streams an SM
+// and more that pays up to kWholeCapMany tokens (512 heads x 256: 16.8 and 9.3 us; x 2048: 43 and 37.5).
+constexpr int kWholeCap = 512, kWholeCapMany = 2048;
 constexpr int tiles_for(int R, int parts) { return R <= 8 ? 1 : (R <= 16 || parts == 2) ? 2 : 4; }
 constexpr int min_blocks(int nt, int parts) { return nt * parts == 1 ? 4 : nt * parts == 2 ? 3 : 2; }
 
@@ -623,9 +641,16 @@ AttendPlan make_plan(const AttendArgs& a, int parts, int sms, size_t* bytes) {
   p.by_hkv = FastDiv::make(a.t.Hkv);
   p.by_G = FastDiv::make(p.G);
   while ((1 << p.lrb) < p.rb) ++p.lrb;
-  p.grid = (sms < kMaxGridSMs ? sms : kMaxGridSMs) * (tc ? 1 : min_blocks(nt, parts));
-  const long long units = (long long)p.nvs * ((((long long)a.t.maxp << a.g.lp) + p.unit - 1) / p.unit);
+  sms = sms < kMaxGridSMs ? sms : kMaxGridSMs;
+  p.grid = sms * (tc ? 1 : min_blocks(nt, parts));
+  const long long cap = (long long)a.t.maxp << a.g.lp, units = (long long)p.nvs * ((cap + p.unit - 1) / p.unit);
   if (units < p.grid) p.grid = (int)units;
+  if (!tc && cap <= (p.nvs >= 2 * sms ? kWholeCapMany : kWholeCap)) {
+    p.whole = 1;
+    p.grid = p.nvs;
+    if (bytes) *bytes = 256;
+    return p;
+  }
   const size_t slots = (size_t)p.grid * 2 * p.rb;
   const size_t ml = (slots * sizeof(float2) + 255) & ~(size_t)255;
   const size_t span = ((size_t)p.nvs * sizeof(int2) + 255) & ~(size_t)255;
@@ -658,7 +683,7 @@ int run(const AttendArgs& a, int sms, cudaStream_t s) {
       if constexpr (PARTS == 1) rc = launch_attend_tc(a, p, s);
       break;
   }
-  if (rc) return rc;
+  if (rc || p.whole) return rc;
   const long long rows = (long long)p.nvs * p.rb;
   if constexpr (PARTS == 1)
     if (p.rb == kTcRows)

@@ -11,21 +11,17 @@
 //   plan   a CTA per stream clears its share of the bitmap, checks the list, finds the first row that moves and lists the destination
 //          pages (marking those to be replaced); refs are read here only, before any stream's change
 //   move   a CTA per stream and per K or V numbers the fresh pages (in stream order) and sweeps
-//   finish rows and lengths take their new values, pages are counted down
-//   push   the pages nobody holds any more join the free list (page_ops.cu)
+//   finish rows and lengths take their new values, pages are counted down, and those nobody holds any
+//          more join the free list (page_ops.cu)
 #include "page.cuh"
 
 namespace kvc {
 
-int page_push(const PoolGeom& g, const PageWs& w, cudaStream_t s);
-
 namespace {
 
-constexpr int kPlanThreads = 128;
+constexpr int kPlanThreads = 256;
 constexpr int kMoveThreads = 128;
-constexpr int kTile = 64;  // tokens moved at a time
-
-enum { kBad = 1, kMoves = 2 };  // plan.w
+constexpr int kTile = 64;  // tokens moved at a time (36 layers x 8 heads: 36 us a cycle; 32 tokens 42, 128 tokens 41)
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PoolGeom g, PageTab t, const int32_t* kept_idx,
                                                            const int32_t* kept_len, int stride, int per_seq,
@@ -52,7 +48,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PoolGeom g, PageTab 
   bool bad = sm_bad;
   int k0 = m;
   if (!bad) {
-    for (int k = threadIdx.x; k < m; k += kPlanThreads) {
+#pragma unroll 4
+    for (int k = threadIdx.x; k < m; k += kPlanThreads) {  // four reads in flight
       const int v = idx[k], next = k + 1 < m ? idx[k + 1] : n;
       if (v < k || v >= next) bad = true;
       if (v != k && k < k0) k0 = k;
@@ -70,7 +67,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PoolGeom g, PageTab 
     // every page the sweep reads must exist, and every page dropped
     const int e = pages_of(n, g.lp);
     for (int i = (k0 >> g.lp) + (int)threadIdx.x; i < e; i += kPlanThreads)
-      if (!page_ok(g, row[i])) sm_bad = 1 | kBad << 1;
+      if (!page_ok(g, row[i])) sm_bad = 1 | kCompactBad << 1;
     if (k0 < m) {
       const int pe = pages_of(m, g.lp);
       int need = 0;
@@ -92,22 +89,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PoolGeom g, PageTab 
     // the first row written: with its page replaced, the page's unmoved rows go along
     int first = k0;
     if (!bad && k0 < m && to[k0 >> g.lp] < 0) first = k0 >> g.lp << g.lp;
-    w.plan[s] = make_int4(first, m, n, bad ? kBad : k0 < m ? kMoves : 0);
+    w.plan[s] = make_int4(first, m, n, bad ? kCompactBad : k0 < m ? kCompactMoves : 0);
   }
-}
-
-__device__ __forceinline__ void drop_one(const PoolGeom& g, const PageWs& w, int p) {
-  const int old = atomicSub(&g.refs[p], 1);
-  if (old == 1)
-    atomicOr(&w.gone[p >> 5], 1u << (p & 31));
-  else if (old < 1)
-    atomicAdd(&g.refs[p], 1);
 }
 
 // A CTA moves the K or the V rows of a stream, kTile destinations at a time: a thread carries U code
 // vectors (16 bytes) and, the first ones, a token's scales (D/16 bytes). Three reads hang on one another
-// (list -> page number -> row), so each runs a tile further ahead: while tile i is written, rows of tiles
-// i+1 to i+3, page numbers of i+4 and list entries of i+5 are in flight. (With rows one tile ahead a tile
+// (list -> page number -> row), so each runs two tiles further ahead: while tile i is written, rows of tiles
+// i+1 to i+3, page numbers of i+5 and list entries of i+7 are on their way. (With rows one tile ahead a tile
 // takes a memory latency, whatever the rest: 24.5 us for 36 layers x 8 heads x 1792 kept of 2048.)
 template <int D>
 struct Move {
@@ -154,7 +143,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(PoolGeom g, PageTab 
     if (none) status_or(status, KVC_STATUS_NO_PAGES);
     w.head[1] = none ? -1 : total;  // for the kernels behind
   }
-  if (none || (plan.w & kBad)) return;
+  if (none || (plan.w & kCompactBad)) return;
   const int first = plan.x, m = plan.y;
   const int32_t* row = t.table + (size_t)s * t.maxp;
   int32_t* to = w.newtab + ((size_t)kv * t.S + s) * t.maxp;
@@ -175,7 +164,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(PoolGeom g, PageTab 
     }
     __syncthreads();
   }
-  if (!(plan.w & kMoves)) return;
+  if (!(plan.w & kCompactMoves)) return;
 
   const int32_t* idx = kept_idx + (size_t)(per_seq ? s / t.Hkv % t.B : s) * stride;
   const int lmask = (1 << g.lp) - 1;
@@ -240,59 +229,27 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(PoolGeom g, PageTab 
     }
   };
 
-  Ahead x[2];
+  Ahead x[4];
   Rows r[4];
 #pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    read_list(first + i * kTile, x[0]);
-    read_pages(x[0]);
-    read_rows(x[0], r[i]);
-  }
-  read_list(first + 3 * kTile, x[1]);
-  read_pages(x[1]);
-  read_list(first + 4 * kTile, x[0]);
+  for (int i = 0; i < 4; ++i) read_list(first + i * kTile, x[i]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) read_pages(x[i]);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) read_rows(x[i], r[i]);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) read_list(first + (4 + i) * kTile, x[i]);
+  read_pages(x[0]);
   for (int t0 = first; t0 < m; t0 += 4 * kTile)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {  // tile i = t0 / kTile + j
       const int ti = t0 + j * kTile;
-      read_rows(x[(j + 1) & 1], r[(j + 3) & 3]);      // tile i + 3
-      read_pages(x[j & 1]);                           // i + 4
-      read_list(ti + 5 * kTile, x[(j + 1) & 1]);      // i + 5
-      __syncthreads();                                // every thread's rows of tile i are read
+      read_rows(x[(j + 3) & 3], r[(j + 3) & 3]);   // tile i + 3
+      read_pages(x[(j + 1) & 3]);                  // i + 5
+      read_list(ti + 7 * kTile, x[(j + 3) & 3]);   // i + 7
+      __syncthreads();                             // every thread's rows of tile i are read
       write_rows(ti, r[j]);
     }
-}
-
-// After the moves: rows and lengths of a stream (a warp each), its replaced pages and those behind the
-// kept rows counted down.
-__global__ void __launch_bounds__(256) finish_kernel(PoolGeom g, PageTab t, PageWs w) {
-  griddep_launch();
-  griddep_wait();
-  const int s = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
-  const int total = w.head[1];
-  if (s >= t.S) return;
-  if (total < 0) {  // too few pages: nothing happened, and nothing is taken
-    return;
-  }
-  const int4 plan = w.plan[s];
-  if (plan.w & kBad) return;
-  int32_t* row = t.table + (size_t)s * t.maxp;
-  const int32_t* to = w.newtab + (size_t)s * t.maxp;
-  const int pe = pages_of(plan.y, g.lp);
-  if (w.need[s])
-    for (int i = (plan.x >> g.lp) + lane; i < pe; i += 32) {
-      const int old = row[i], p = to[i];
-      if (p != old) {
-        row[i] = p;
-        g.refs[p] = 1;
-        drop_one(g, w, old);
-      }
-    }
-  for (int i = pe + lane; i < pages_of(plan.z, g.lp); i += 32) {
-    drop_one(g, w, row[i]);
-    row[i] = -1;
-  }
-  if (lane == 0) t.len[s] = plan.y;
 }
 
 }  // namespace
@@ -305,9 +262,7 @@ int launch_page_compact(const PoolGeom& g, const PageTab& t, const int32_t* kept
   if (launch_pdl(g.D == 128 ? move_kernel<128> : move_kernel<64>, dim3(2 * t.S), dim3(kMoveThreads), 0, s, false, g, t,
                  kept_idx, stride, per_seq, status, w) != cudaSuccess)
     return KVC_ERR_LAUNCH;
-  if (launch_pdl(finish_kernel, dim3((t.S + 7) / 8), dim3(256), 0, s, false, g, t, w) != cudaSuccess)
-    return KVC_ERR_LAUNCH;
-  return page_push(g, w, s);
+  return page_finish_compact(g, t, w, s);
 }
 
 }  // namespace kvc

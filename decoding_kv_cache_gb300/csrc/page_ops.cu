@@ -69,10 +69,39 @@ __device__ __forceinline__ bool extend_wants(const PoolGeom& g, const PageTab& t
   return true;
 }
 
-// Pages each stream takes: the fresh ones behind its last page and, when that page is partly filled
-// and shared, a copy of it. Of the streams that share a page and all write to it, the lowest sequence
-// keeps it; the sharers of a page are sequences of the same layer and head (forks keep it so), found
-// by comparing that page's number over the sequences, for shared last pages only.
+// Pages stream s takes (kCopyFlag when its last page is copied), -1 where the request cannot stand: the fresh
+// ones behind its last page and, when that page is partly filled and shared, a copy of it. Of the streams
+// that share a page and all write to it, the lowest sequence keeps it; the sharers of a page are sequences
+// of the same layer and head (forks keep it so), found by comparing that page's number over the sequences,
+// for shared last pages only.
+__device__ __forceinline__ int extend_need(const PoolGeom& g, const PageTab& t, int s, const int32_t* add, int add_all,
+                                           int32_t* status) {
+  const int h = s % t.Hkv, b = s / t.Hkv % t.B, l = s / (t.Hkv * t.B);
+  const int a = add ? add[b] : add_all;
+  int n;
+  if (!extend_wants(g, t, s, a, &n, status)) return -1;
+  if (a == 0) return 0;
+  const int need = pages_of(n + a, g.lp) - pages_of(n, g.lp);
+  if (!(n & ((1 << g.lp) - 1))) return need;
+  const int p = t.table[(size_t)s * t.maxp + (n >> g.lp)];
+  if (!page_ok(g, p)) {
+    status_or(status, KVC_STATUS_BAD_PAGE);
+    return -1;
+  }
+  const int r = g.refs[p];
+  if (r <= 1) return need;
+  int writers = 0, lowest = b;
+  for (int o = 0; o < t.B; ++o) {
+    const int so = (l * t.B + o) * t.Hkv + h;
+    const int ao = add ? add[o] : add_all, no = t.len[so];
+    if (ao <= 0 || no <= 0 || no + (long long)ao > ((long long)t.maxp << g.lp) || !(no & ((1 << g.lp) - 1))) continue;
+    if (t.table[(size_t)so * t.maxp + (no >> g.lp)] != p) continue;
+    ++writers;
+    if (o < lowest) lowest = o;
+  }
+  return lowest == b && writers >= r ? need : (need + 1) | kCopyFlag;
+}
+
 __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(PoolGeom g, PageTab t, const int32_t* add,
                                                                   int add_all, int32_t* status, PageWs w) {
   __shared__ int sm[8];
@@ -81,35 +110,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(PoolGeom g, P
   const int s = blockIdx.x * kPlanThreads + threadIdx.x;
   int need = 0;
   if (s < t.S) {
-    const int h = s % t.Hkv, b = s / t.Hkv % t.B, l = s / (t.Hkv * t.B);
-    const int a = add ? add[b] : add_all;
-    int n;
-    if (!extend_wants(g, t, s, a, &n, status)) {
-      need = -1;
-    } else if (a > 0) {
-      need = pages_of(n + a, g.lp) - pages_of(n, g.lp);
-      if (n & ((1 << g.lp) - 1)) {
-        const int p = t.table[(size_t)s * t.maxp + (n >> g.lp)];
-        if (!page_ok(g, p)) {
-          status_or(status, KVC_STATUS_BAD_PAGE);
-          need = -1;
-        } else {
-          const int r = g.refs[p];
-          if (r > 1) {
-            int writers = 0, lowest = b;
-            for (int o = 0; o < t.B; ++o) {
-              const int so = (l * t.B + o) * t.Hkv + h;
-              const int ao = add ? add[o] : add_all, no = t.len[so];
-              if (ao <= 0 || no <= 0 || no + (long long)ao > ((long long)t.maxp << g.lp) || !(no & ((1 << g.lp) - 1))) continue;
-              if (t.table[(size_t)so * t.maxp + (no >> g.lp)] != p) continue;
-              ++writers;
-              if (o < lowest) lowest = o;
-            }
-            if (!(lowest == b && writers >= r)) need = (need + 1) | kCopyFlag;
-          }
-        }
-      }
-    }
+    need = extend_need(g, t, s, add, add_all, status);
     w.need[s] = need;
   }
   const int sum = block_sum(need < 0 ? 0 : need & ~kCopyFlag, sm);
@@ -156,28 +157,10 @@ __device__ __forceinline__ void copy_page(const PoolGeom& g, int dst, int src, i
   }
 }
 
-// The pages handed out: a warp per stream, which also copies its page.
-__global__ void __launch_bounds__(kAssignThreads) extend_assign_kernel(PoolGeom g, PageTab t, const int32_t* add,
-                                                                      int add_all, int32_t* start, int32_t* status,
-                                                                      PageWs w) {
-  __shared__ int sm[8];
-  griddep_launch();
-  griddep_wait();
-  const int s0 = blockIdx.x * kAssignStreams, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int before, total;
-  need_before(w, t.S, s0, sm, &before, &total);
-  const int nfree = w.head[0];
-  const bool none = total > nfree || nfree > g.npages;
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    if (none)
-      status_or(status, KVC_STATUS_NO_PAGES);
-    else
-      *g.nfree = nfree - total;
-  }
-  const int s = s0 + warp;
-  if (s >= t.S) return;
-  for (int i = s0; i < s; ++i) before += need_of(w, i);
-  const int need = w.need[s];
+// A warp hands stream s its pages (`before` pages go to the streams before it) and copies its page.
+__device__ __forceinline__ void extend_stream(const PoolGeom& g, const PageTab& t, int s, int need, int before, bool none,
+                                              int nfree, const int32_t* add, int add_all, int32_t* start) {
+  const int lane = threadIdx.x & 31;
   if (none || need < 0) {
     if (lane == 0 && start) start[s] = -1;
     return;
@@ -207,6 +190,30 @@ __global__ void __launch_bounds__(kAssignThreads) extend_assign_kernel(PoolGeom 
     t.len[s] = n + a;
     if (start) start[s] = n;
   }
+}
+
+// The pages handed out: a warp per stream.
+__global__ void __launch_bounds__(kAssignThreads) extend_assign_kernel(PoolGeom g, PageTab t, const int32_t* add,
+                                                                      int add_all, int32_t* start, int32_t* status,
+                                                                      PageWs w) {
+  __shared__ int sm[8];
+  griddep_launch();
+  griddep_wait();
+  const int s0 = blockIdx.x * kAssignStreams, warp = threadIdx.x >> 5;
+  int before, total;
+  need_before(w, t.S, s0, sm, &before, &total);
+  const int nfree = w.head[0];
+  const bool none = total > nfree || nfree > g.npages;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    if (none)
+      status_or(status, KVC_STATUS_NO_PAGES);
+    else
+      *g.nfree = nfree - total;
+  }
+  const int s = s0 + warp;
+  if (s >= t.S) return;
+  for (int i = s0; i < s; ++i) before += need_of(w, i);
+  extend_stream(g, t, s, w.need[s], before, none, nfree, add, add_all, start);
 }
 
 // Counted down; a page whose last reference goes is marked.
@@ -492,6 +499,49 @@ __global__ void __cluster_dims__(kOneCtas, 1, 1) __launch_bounds__(kOneThreads)
   cluster_push(cl, g, w, nfree);
 }
 
+// Up to kOneStreams streams extended in one launch: every CTA of the cluster plans all of them (a thread each),
+// the barrier stands between the reads and the changes, then a warp takes a stream.
+constexpr int kOneStreams = 256;
+__global__ void __cluster_dims__(kOneCtas, 1, 1) __launch_bounds__(kOneThreads)
+    extend_one_kernel(PoolGeom g, PageTab t, const int32_t* add, int add_all, int32_t* start, int32_t* status) {
+  __shared__ int sm_need[kOneStreams], sm_before[kOneStreams], sm_sum[kOneThreads / 32];
+  griddep_launch();
+  griddep_wait();
+  cg::cluster_group cl = cg::this_cluster();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nfree = *g.nfree;
+  int need = 0;
+  if ((int)threadIdx.x < t.S) need = extend_need(g, t, threadIdx.x, add, add_all, cl.block_rank() == 0 ? status : nullptr);
+  const int mine = need < 0 ? 0 : need & ~kCopyFlag;
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) sm_sum[warp] = incl;
+  __syncthreads();
+  int before = incl - mine, total = 0;
+#pragma unroll
+  for (int i = 0; i < kOneStreams / 32; ++i) {
+    if (i < warp) before += sm_sum[i];
+    total += sm_sum[i];
+  }
+  if (threadIdx.x < kOneStreams) {
+    sm_need[threadIdx.x] = need;
+    sm_before[threadIdx.x] = before;
+  }
+  cl.sync();
+  const bool none = total > nfree || nfree > g.npages;
+  if (cl.block_rank() == 0 && threadIdx.x == 0) {
+    if (none)
+      status_or(status, KVC_STATUS_NO_PAGES);
+    else
+      *g.nfree = nfree - total;
+  }
+  const int s = warp * kOneCtas + cl.block_rank();  // neighbours on different SMs
+  if (s < t.S) extend_stream(g, t, s, sm_need[s], sm_before[s], none, nfree, add, add_all, start);
+}
+
 bool one_fits(const PoolGeom& g, const PageTab& t, const PageTab& o) {
   return g.npages <= kOnePages && (long long)t.S * t.maxp <= kOneEntries && (long long)o.S * o.maxp <= kOneEntries &&
          t.B <= kOneSeqs && o.B <= kOneSeqs;
@@ -499,7 +549,63 @@ bool one_fits(const PoolGeom& g, const PageTab& t, const PageTab& o) {
 
 int push_grid(const PoolGeom& g) { return ((g.npages + 31) / 32 + kPushWords - 1) / kPushWords; }
 
+// After a compaction's moves: rows and lengths of a stream, by a warp; its replaced pages and those behind the
+// kept rows counted down.
+__device__ __forceinline__ void compact_finish(const PoolGeom& g, const PageTab& t, const PageWs& w, int s) {
+  const int lane = threadIdx.x & 31;
+  const int4 plan = w.plan[s];  // first row written, kept, length, flags
+  if (plan.w & kCompactBad) return;
+  int32_t* row = t.table + (size_t)s * t.maxp;
+  const int32_t* to = w.newtab + (size_t)s * t.maxp;
+  const int pe = pages_of(plan.y, g.lp);
+  if (w.need[s])
+    for (int i = (plan.x >> g.lp) + lane; i < pe; i += 32) {
+      const int old = row[i], p = to[i];
+      if (p != old) {
+        row[i] = p;
+        g.refs[p] = 1;
+        drop_page(g, w, old, nullptr);
+      }
+    }
+  for (int i = pe + lane; i < pages_of(plan.z, g.lp); i += 32) {
+    drop_page(g, w, row[i], nullptr);
+    row[i] = -1;
+  }
+  if (lane == 0) t.len[s] = plan.y;
+}
+
+// head[1] < 0: too few pages, nothing happened.
+__global__ void __launch_bounds__(256) finish_kernel(PoolGeom g, PageTab t, PageWs w) {
+  griddep_launch();
+  griddep_wait();
+  const int s = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  if (s < t.S && w.head[1] >= 0) compact_finish(g, t, w, s);
+}
+
+__global__ void __cluster_dims__(kOneCtas, 1, 1) __launch_bounds__(kOneThreads)
+    finish_one_kernel(PoolGeom g, PageTab t, PageWs w) {
+  griddep_launch();
+  griddep_wait();
+  cg::cluster_group cl = cg::this_cluster();
+  const int total = w.head[1];
+  if (total < 0) return;
+  for (int s = (threadIdx.x >> 5) * kOneCtas + cl.block_rank(); s < t.S; s += kOneCtas * kOneThreads / 32)
+    compact_finish(g, t, w, s);
+  cl.sync();
+  cluster_push(cl, g, w, w.head[0] - total);
+}
 }  // namespace
+
+int page_finish_compact(const PoolGeom& g, const PageTab& t, const PageWs& w, cudaStream_t s) {
+  constexpr int kStreams = 64;  // one launch less; with 288 streams the eight SMs take 11.5 us, the two kernels 10
+  if (t.S <= kStreams && g.npages <= kOnePages)
+    return launch_pdl(finish_one_kernel, dim3(kOneCtas), dim3(kOneThreads), 0, s, false, g, t, w) == cudaSuccess
+               ? KVC_OK
+               : KVC_ERR_LAUNCH;
+  if (launch_pdl(finish_kernel, dim3((t.S + 7) / 8), dim3(256), 0, s, false, g, t, w) != cudaSuccess)
+    return KVC_ERR_LAUNCH;
+  return page_push(g, w, s);
+}
 
 int page_push(const PoolGeom& g, const PageWs& w, cudaStream_t s) {
   return launch_pdl(push_kernel, dim3(push_grid(g)), dim3(kPushThreads), 0, s, false, g, w) == cudaSuccess ? KVC_OK
@@ -520,6 +626,11 @@ int launch_page_init(const PoolGeom& g, const PageTab* t, cudaStream_t s) {
 
 int launch_page_extend(const PoolGeom& g, const PageTab& t, const int32_t* add, int add_all, int32_t* start,
                        int32_t* status, const PageWs& w, cudaStream_t s) {
+  if (t.S <= kOneStreams)
+    return launch_pdl(extend_one_kernel, dim3(kOneCtas), dim3(kOneThreads), 0, s, false, g, t, add, add_all, start,
+                      status) == cudaSuccess
+               ? KVC_OK
+               : KVC_ERR_LAUNCH;
   if (launch_pdl(extend_plan_kernel, dim3((t.S + kPlanThreads - 1) / kPlanThreads), dim3(kPlanThreads), 0, s, false, g,
                  t, add, add_all, status, w) != cudaSuccess)
     return KVC_ERR_LAUNCH;
