@@ -119,6 +119,8 @@ struct StoreArgs {
   const void* x[2];  // K, V rows
   RowStrides xs[2];
   int T;
+  FastDiv by_T, by_hkv;
+  float inv6[2];  // 1 / (6 k_scale), 1 / (6 v_scale)
   const int32_t* n;      // [B] or null
   const int32_t* start;  // [S]
   int32_t* status;
@@ -130,6 +132,7 @@ struct ReadArgs {
   void* out[2];  // K, V: [S][ncap][D], either may be null
   const int32_t* first;
   int first_all, count;
+  FastDiv by_count;
   long long ncap;
   int32_t* status;
 };

@@ -189,6 +189,9 @@ int kvc_page_store(const kvc_pool* pool, const kvc_pages* pages, int32_t dtype, 
   a.x[0] = k;
   a.x[1] = v;
   a.T = T;
+  a.by_T = FastDiv::make(T);
+  for (int i = 0; i < 2; ++i) a.inv6[i] = 1.f / (6.f * a.g.ts[i]);
+  a.by_hkv = FastDiv::make(a.t.Hkv);
   a.n = n;
   a.start = start;
   a.status = status;
@@ -208,6 +211,7 @@ int kvc_page_read(const kvc_pool* pool, const kvc_pages* pages, int32_t dtype, c
   a.first = first;
   a.first_all = first_all;
   a.count = count;
+  a.by_count = FastDiv::make(count);
   a.ncap = ncap;
   a.status = status;
   return launch_page_read(a, dtype, static_cast<cudaStream_t>(stream));

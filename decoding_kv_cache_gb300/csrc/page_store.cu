@@ -8,12 +8,12 @@
 // the scale's quotient is truncated and its lowest bit set when anything was cut off (so rounding it
 // again to e4m3 is the exact quotient's rounding); the code is found by halving, each border b by the
 // sign of fma(-b, scale ts, |x|), which is that of the exact difference.
-// For bf16 rows and ts a power of two there is a shorter way: x = X 2^k and scale ts = m 2^e with
-// integers X <= 255, m <= 15, so the quotient X 2^(k-e) / m either is a border B or misses it by more
-// than 2^-8.2 B >= 2^-10.2. The product with the step's rounded reciprocal, off by less than 2^-20, rounded
-// to a multiple of 2^-13 (an fma onto 1536, taken off again) is then on the quotient's side of every
-// border, and on it where the quotient is; the hardware's e2m1 conversion does the rest: 3.5 operations
-// a value against 13 (4 sequences x 4096 rows x 8 heads: 46 -> 26 us of the store).
+// For bf16 rows and ts a power of two there is a shorter way. With integers X <= 255 and m <= 15 every
+// quotient decided here is X 2^k / 6 (a scale) or X 2^k / m (a code): it either is a border or misses it by
+// more than 2^-10.7 of it, and the borders between codes are multiples of 1/4. So products with rounded
+// reciprocals (off by less than 2^-20), rounded to 12 bits for the scale and to a multiple of 2^-13 for the
+// codes (an fma onto 1536, taken off again), lie on the quotient's side of every border, and on it where the
+// quotient does; the hardware's e4m3 and e2m1 conversions then decide as the exact quotients would.
 // A thread owns a group: two 16-byte loads (bf16), 8 bytes of codes, 1 of scale. Memory-bound:
 // 2.56 bytes a value moved for bf16.
 #include "page.cuh"
@@ -41,19 +41,14 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // a NaN wins
   return r;
 }
 
-// codes (8 bytes, even channel in the low nibble) and scale of one group; x's NaNs become 0
-template <bool SNAP>
+// Codes (8 bytes, even channel in the low nibble) and scale of one group; NaNs count as 0, and what rounds to
+// zero has no sign.
 __device__ __forceinline__ uint2 quantise16(float (&x)[16], float ts, uint32_t* scale) {
   float amax = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) amax = max_nan(amax, fabsf(x[i]));
-  if (amax != amax) {
-    amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      if (x[i] != x[i]) x[i] = 0.f;
-      amax = fmaxf(amax, fabsf(x[i]));
-    }
+  for (int i = 0; i < 16; ++i) {
+    if (x[i] != x[i]) x[i] = 0.f;
+    amax = fmaxf(amax, fabsf(x[i]));
   }
   const float den = 6.f * ts;
   float want = __fdiv_rz(amax, den);
@@ -63,31 +58,59 @@ __device__ __forceinline__ uint2 quantise16(float (&x)[16], float ts, uint32_t* 
   *scale = sb;
   const float step = e4m3_f32(sb) * ts;
   uint32_t w[2] = {0u, 0u};
-  if constexpr (SNAP) {
-    const float r = __frcp_rn(step);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float y[8];
+  for (int i = 0; i < 16; ++i) {
+    const float v = fabsf(x[i]);
+    const bool c2 = __fmaf_rn(-1.75f, step, v) >= 0.f;
+    const bool c1 = __fmaf_rn(c2 ? -3.5f : -0.75f, step, v) >= 0.f;
+    const bool c0 = __fmaf_rn(c2 ? (c1 ? -5.f : -2.5f) : (c1 ? -1.25f : -0.25f), step, v) > 0.f;
+    uint32_t c = (c2 ? 4u : 0u) | (c1 ? 2u : 0u) | (c0 ? 1u : 0u);
+    if (c) c |= __float_as_uint(x[i]) >> 28 & 8u;
+    w[i / 8] |= c << (4 * (i % 8));
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// The short way (see above): inv6 = 1 / (6 ts), ts a power of two.
+__device__ __forceinline__ uint2 quantise16_snap(const uint4 (&raw)[2], float ts, float inv6, uint32_t* scale) {
+  uint32_t h[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
+  auto pair = [](uint32_t v) { return *reinterpret_cast<const __nv_bfloat162*>(&v); };
+  __nv_bfloat162 m = __habs2(pair(h[0]));
 #pragma unroll
-      for (int u = 0; u < 8; ++u)  // the sign of a value that rounds to zero stays
-        y[u] = copysignf(__fsub_rn(__fmaf_rn(fabsf(x[8 * i + u]), r, 1536.f), 1536.f), x[8 * i + u]);
-      asm("{\n .reg .b8 b0, b1, b2, b3;\n cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n"
-          " cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n"
-          " cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n mov.b32 %0, {b0, b1, b2, b3};\n}\n"
-          : "=r"(w[i])
-          : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+  for (int i = 1; i < 8; ++i) m = __hmax2_nan(m, __habs2(pair(h[i])));
+  float amax = max_nan(__low2float(m), __high2float(m));
+  if (amax != amax) {
+    amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if ((h[i] & 0x7fffu) > 0x7f80u) h[i] &= 0xffff0000u;
+      if ((h[i] & 0x7fff0000u) > 0x7f800000u) h[i] &= 0xffffu;
+      amax = fmaxf(amax, fmaxf(fabsf(__low2float(pair(h[i]))), fabsf(__high2float(pair(h[i])))));
     }
-  } else {
+  }
+  float want = fminf(fmaxf(amax * inv6, 0.001953125f), 448.f);
+  want = __uint_as_float((__float_as_uint(want) + 0x400u) & ~0x7ffu);
+  const uint32_t sb = __nv_cvt_float_to_fp8(want, __NV_SATFINITE, __NV_E4M3);
+  *scale = sb;
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(e4m3_f32(sb) * ts));
+  uint32_t w[2];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float v = fabsf(x[i]);
-      const bool c2 = __fmaf_rn(-1.75f, step, v) >= 0.f;
-      const bool c1 = __fmaf_rn(c2 ? -3.5f : -0.75f, step, v) >= 0.f;
-      const bool c0 = __fmaf_rn(c2 ? (c1 ? -5.f : -2.5f) : (c1 ? -1.25f : -0.25f), step, v) > 0.f;
-      uint32_t c = (c2 ? 4u : 0u) | (c1 ? 2u : 0u) | (c0 ? 1u : 0u);
-      c |= __float_as_uint(x[i]) >> 28 & 8u;
-      w[i / 8] |= c << (4 * (i % 8));
+  for (int i = 0; i < 2; ++i) {
+    float y[8];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t v = h[4 * i + u];
+      y[2 * u] = __fadd_rn(__fmaf_rn(__uint_as_float(v << 16), r, 1536.f), -1536.f);
+      y[2 * u + 1] = __fadd_rn(__fmaf_rn(__uint_as_float(v & 0xffff0000u), r, 1536.f), -1536.f);
     }
+    asm("{\n .reg .b8 b0, b1, b2, b3;\n cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n mov.b32 %0, {b0, b1, b2, b3};\n}\n"
+        : "=r"(w[i])
+        : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+    const uint32_t some = (w[i] | w[i] >> 1 | w[i] >> 2) & 0x11111111u;  // codes that are not zero
+    w[i] &= 0x77777777u | some << 3;
   }
   return make_uint2(w[0], w[1]);
 }
@@ -96,16 +119,16 @@ __device__ __forceinline__ uint2 quantise16(float (&x)[16], float ts, uint32_t* 
 template <typename Index>
 struct Item {
   int kv, s, tok;
-  __device__ __forceinline__ Item(Index item, Index rows, int T, bool both, int only) {
+  __device__ __forceinline__ Item(Index item, Index rows, const FastDiv& by_T, bool both, int only) {
     kv = both ? item >= rows : only;
     const Index r = both && kv ? item - rows : item;
-    s = (int)(r / (Index)T);
-    tok = (int)(r - (Index)s * (Index)T);
+    s = sizeof(Index) == 4 ? by_T.div((int)r) : (int)(r / by_T.d);
+    tok = (int)(r - (Index)s * (Index)by_T.d);
   }
 };
 
 // A thread takes group `grp` of N rows, whose reads are all in flight before the first is used. Index: 32
-// bits wherever the rows fit (a 64-bit division costs as much as a group's codes).
+// bits wherever the rows fit, where no division is left.
 template <typename T, int D, int N, bool SNAP, typename Index>
 __global__ void __launch_bounds__(kThreads) store_kernel(StoreArgs a) {
   griddep_launch();
@@ -122,8 +145,8 @@ __global__ void __launch_bounds__(kThreads) store_kernel(StoreArgs a) {
     kvs[i] = in16[i] = 0;
     const Index item = item0 + i * kRows;
     if (item >= 2 * rows) continue;
-    const Item<Index> it(item, rows, a.T, true, 0);
-    const int h = it.s % a.t.Hkv, b = it.s / a.t.Hkv;
+    const Item<Index> it(item, rows, a.by_T, true, 0);
+    const int b = a.by_hkv.div(it.s), h = it.s - b * a.t.Hkv;
     const RowStrides& xs = it.kv ? a.xs[1] : a.xs[0];
     const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(it.kv ? a.x[1] : a.x[0]) + b * xs.b +
                                                       it.tok * xs.t + h * xs.h + 16 * grp);
@@ -150,10 +173,16 @@ __global__ void __launch_bounds__(kThreads) store_kernel(StoreArgs a) {
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     if (!at[i]) continue;
-    float x[16];
-    unpack16<T>(raw[i], x);
     uint32_t sc;
-    const uint2 c = quantise16<SNAP>(x, kvs[i] ? a.g.ts[1] : a.g.ts[0], &sc);
+    uint2 c;
+    const float ts = kvs[i] ? a.g.ts[1] : a.g.ts[0];
+    if constexpr (SNAP) {
+      c = quantise16_snap(raw[i].v, ts, kvs[i] ? a.inv6[1] : a.inv6[0], &sc);
+    } else {
+      float x[16];
+      unpack16<T>(raw[i], x);
+      c = quantise16(x, ts, &sc);
+    }
     *reinterpret_cast<uint2*>(at[i] + (kvs[i] ? piece_off(D, 2) : 0) + in16[i] * (D / 2) + 8 * grp) = c;
     at[i][(kvs[i] ? piece_off(D, 3) : piece_off(D, 1)) + in16[i] * (D / 16) + grp] = (uint8_t)sc;
   }
@@ -177,7 +206,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(ReadArgs a) {
     to[i] = nullptr;
     const Index item = item0 + i * kRows;
     if (item >= items) continue;
-    const Item<Index> it(item, rows, a.count, both, a.out[0] == nullptr);
+    const Item<Index> it(item, rows, a.by_count, both, a.out[0] == nullptr);
     const int f = a.first ? a.first[it.s] : a.first_all;
     const long long pos = (long long)f + it.tok;
     if (f < 0 || pos >= a.t.len[it.s] || pos >= ((long long)a.t.maxp << a.g.lp)) continue;

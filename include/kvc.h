@@ -479,9 +479,9 @@ KVC_API int kvc_page_extend(const kvc_pool* pool, const kvc_pages* pages, const 
  * stream (b, h) becomes token start[b,h] + t, for t < n[b] (all T when n is NULL); streams with
  * start < 0 are skipped. Per group of 16 channels x:
  *   scale = e4m3(clamp(max|x| / (6 ts), 2^-9, 448)); code = e2m1 nearest to x / (scale ts), ties to
- *   the even code, larger quotients saturate, the sign is x's; both roundings are those of the exact
- *   quotients by the fp32 numbers 6 ts and scale ts. A NaN is stored as 0, an infinity as 6 * 448 ts
- *   with its sign.
+ *   the even code, larger quotients saturate, what rounds to zero has no sign; both roundings are those
+ *   of the exact quotients by the fp32 numbers 6 ts and scale ts. A NaN is stored as 0, an infinity as
+ *   6 * 448 ts with its sign.
  * A row past the stream's length (KVC_STATUS_BAD_INDEX) or in a page that is missing or shared
  * (KVC_STATUS_BAD_PAGE) is skipped.
  *

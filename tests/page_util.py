@@ -37,7 +37,7 @@ def quantise(x, ts):
         code = np.zeros(g.shape, np.uint8)
         for k, border in enumerate((0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0)):
             code += ((y > border) if k % 2 == 0 else (y >= border)).astype(np.uint8)
-        code += np.where(np.signbit(g) & ~np.isnan(g), 8, 0).astype(np.uint8)
+        code += np.where(np.signbit(g) & (code > 0), 8, 0).astype(np.uint8)  # what rounds to zero has no sign
     code = code.reshape(x.shape)
     return code[..., 0::2] | (code[..., 1::2] << 4), sb
 
