@@ -93,7 +93,7 @@ def rand_rows(shape, dt, seed):
 @pytest.mark.parametrize("dt,D,page,T,scales", [
     ("bf16", 128, 64, 1, (1.0, 1.0)), ("bf16", 128, 16, 37, (0.5, 2.0)), ("bf16", 64, 32, 130, (1.0, 0.25)),
     ("f32", 128, 256, 300, (1.0, 1.0)), ("f32", 64, 16, 16, (0.125, 1.0)), ("bf16", 128, 128, 1000, (1.0, 1.0)),
-    ("bf16", 128, 64, 8000, (1.0, 2.0)), ("f32", 64, 64, 13100, (1.0, 1.0)),  # several rows a thread
+    ("bf16", 128, 64, 8000, (1.0, 2.0)), ("f32", 64, 64, 13100, (1.0, 1.0)),
     ("bf16", 64, 64, 13100, (0.7, 1.0)),                                      # a tensor scale that is no power of two
 ])
 def test_store_and_read_match_bit_for_bit(dt, D, page, T, scales):
