@@ -234,7 +234,7 @@ int kvc_page_attend(const kvc_pool* pool, const kvc_pages* pages, int32_t dtype,
   if (rc || (rc = check_pages(pages, a.g.lp, &a.t))) return rc;
   const int es = elem_size(dtype);
   if (!es) return KVC_ERR_UNSUPPORTED_DTYPE;
-  if (a.t.L != 1 || Hq < 1 || T < 1 || !out || !isfinite(scale)) return KVC_ERR_INVALID_ARG;
+  if (a.t.L != 1 || Hq < 1 || T < 1 || !out || !isfinite(scale * a.g.ts[0])) return KVC_ERR_INVALID_ARG;
   if (Hq % a.t.Hkv) return KVC_ERR_NOT_DIVISIBLE;
   if ((long long)a.t.B * Hq > (1LL << 30) || (long long)a.t.B * Hq * T > (1LL << 30)) return KVC_ERR_TOO_LARGE;
   a.Hq = Hq;

@@ -551,7 +551,7 @@ KVC_API int kvc_page_compact(const kvc_pool* pool, const kvc_pages* pages, const
  *
  *   dtype      kvc_dtype of q and out
  *   q          [B][T][Hq][D] rows (device, 16-byte aligned), strides as kvc_page_store's
- *   scale      finite; 1/sqrt(D) is usual
+ *   scale      finite, and so its product with k_scale; 1/sqrt(D) is usual
  *   out, lse   [B,T,Hq,D] and [B,T,Hq] fp32 (device); lse may be NULL
  *   workspace  at least kvc_page_attend_workspace_size() bytes, 256-byte aligned
  */

@@ -404,13 +404,13 @@ def test_attend_many_units_a_cta(dt, D, G, T, n):
             assert (np.abs(lse[b, i].double().cpu().numpy() - ref["lse"]) <= ltol).all()
 
 
-@pytest.mark.parametrize("dt", ["bf16", "f32"])
-def test_attend_strided_ragged_scaled(dt):
-    x, q0 = make_attend(dt, 128, 4, 2, 3, 6, 32, [90, 80, 3, 4, 50, 60, 0, 0], seed=5, k_scale=0.3, v_scale=7.0)
-    fused = torch.zeros((4, 6, 11, 128), dtype=DT[dt], device=DEV)  # the query part of a fused projection's row
+@pytest.mark.parametrize("dt,T", [("bf16", 6), ("bf16", 30), ("f32", 6)])
+def test_attend_strided_ragged_scaled(dt, T):
+    x, q0 = make_attend(dt, 128, 4, 2, 3, T, 32, [90, 80, 3, 4, 50, 60, 0, 0], seed=5, k_scale=0.3, v_scale=7.0)
+    fused = torch.zeros((4, T, 11, 128), dtype=DT[dt], device=DEV)  # the query part of a fused projection's row
     fused[:, :, 2:8] = q0.to(DEV)
     q = fused[:, :, 2:8]
-    for n_q in ([6, 4, 0, 6], [1, 6, 99, -3]):
+    for n_q in ([6, 4, 0, 6], [1, T, 99, -3]):
         run = lambda out, lse: x.kvc.kvc_page_attend(x.pool, x.pages, q, out, lse=lse, scale=0.37, status=x.status,
                                                      n_q=up(np.array(n_q, np.int32)))
         check_attend(x, q0, dt, scale=0.37, n_q=n_q, run=run)
@@ -419,10 +419,10 @@ def test_attend_strided_ragged_scaled(dt):
     check_attend(x, q0, dt, run=run)
 
 
-@pytest.mark.parametrize("dt", ["bf16", "f32"])
-def test_attend_extreme_logits(dt):
+@pytest.mark.parametrize("dt,T", [("bf16", 2), ("bf16", 20), ("f32", 2)])
+def test_attend_extreme_logits(dt, T):
     """Large and negative scales, one dominant key, zero queries: the running maximum has to follow."""
-    x, q = make_attend(dt, 64, 2, 2, 2, 2, 16, [300, 40, 16, 129], seed=11)
+    x, q = make_attend(dt, 64, 2, 2, 2, T, 16, [300, 40, 16, 129], seed=11)
     for scale in (0.0, -0.5, 4.0, 30.0, 1e-6):
         check_attend(x, q, dt, scale=scale)
     q[0] = 0
@@ -432,22 +432,30 @@ def test_attend_extreme_logits(dt):
     check_attend(x, q, dt, scale=0.125)
 
 
-def test_attend_bad_pages_take_no_part():
-    x, q = make_attend("bf16", 128, 2, 1, 2, 1, 16, [64, 40], seed=2)
-    x.pages.table[0, 0, 0, 1] = 12345678
-    x.pages.table[0, 1, 0, 2] = -1
-    out = torch.zeros((2, 1, 2, 128), dtype=torch.bfloat16, device=DEV)
-    x.kvc.kvc_page_attend(x.pool, x.pages, q.to(DEV), out, status=x.status)
+@pytest.mark.parametrize("T,cap", [(1, 4), (1, 40), (20, 4)])
+def test_attend_bad_pages_take_no_part(T, cap):
+    """On each of the kernels (short tables, long tables, many rows)."""
+    x, q = make_attend("bf16", 128, 2, 1, 2, T, 16, [64, 40], seed=2)
+    table = torch.full((1, 2, 1, cap), -1, dtype=torch.int32, device=DEV)
+    table[..., :4] = x.pages.table
+    table[0, 0, 0, 1] = 12345678
+    table[0, 1, 0, 1] = -1
+    pages = x.kvc.Pages(table, x.pages.len)
+    out, lse = torch.zeros((2, T, 2, 128), dtype=torch.bfloat16, device=DEV), torch.zeros((2, T, 2), device=DEV)
+    x.kvc.kvc_page_attend(x.pool, pages, q.to(DEV), out, lse=lse, status=x.status)
     assert int(x.status.item()) == R.BAD_PAGE
-    for b, gone in ((0, slice(16, 32)), (1, slice(32, 40))):
+    for b, n in ((0, 64), (1, 40)):
         K, V = R.rows(x.p, x.t, (0, b, 0), 0), R.rows(x.p, x.t, (0, b, 0), 1)
-        K, V = np.delete(K, gone, 0), np.delete(V, gone, 0)
-        ref = R.attend_rows(q[b, 0].double().numpy(), K, V, 128 ** -0.5)
-        tol, _ = R.tolerances("bf16", 64, 128, ref)
-        assert (np.abs(out[b, 0].double().cpu().numpy() - ref["out"]) <= tol).all()
+        for i in range(T):
+            seen = np.setdiff1d(np.arange(n - T + i + 1), np.arange(16, 32))
+            ref = R.attend_rows(q[b, i].double().numpy(), K[seen], V[seen], 128 ** -0.5)
+            tol, ltol = R.tolerances("bf16", 64, 128, ref)
+            assert (np.abs(out[b, i].double().cpu().numpy() - ref["out"]) <= tol).all()
+            assert (np.abs(lse[b, i].double().cpu().numpy() - ref["lse"]) <= ltol).all()
     x.pages.len[0, 1, 0] = 1 << 20  # a length beyond the table: an empty stream
-    x.kvc.kvc_page_attend(x.pool, x.pages, q.to(DEV), out, status=x.status)
-    assert (out[1] == 0).all()
+    x.status.zero_()
+    x.kvc.kvc_page_attend(x.pool, pages, q.to(DEV), out, lse=lse, status=x.status)
+    assert (out[1] == 0).all() and torch.isneginf(lse[1]).all() and int(x.status.item()) == R.BAD_PAGE
 
 
 def test_offsets_past_32_bits():
@@ -605,24 +613,25 @@ def test_captured_and_replayed_with_new_lengths():
         assert (np.abs(lse[1, 0, 4:].double().cpu().numpy() - ref["lse"]) <= ltol).all()
 
 
-def test_two_streams_with_their_own_workspaces():
+def test_streams_with_their_own_workspaces():
     from decoding_kv_cache_gb300 import kvc
     a, qa = make_attend("bf16", 128, 4, 4, 4, 1, 64, [900] * 16, seed=31)
     b, qb = make_attend("bf16", 128, 2, 2, 8, 3, 16, [333, 500, 7, 64], seed=32)
-    ref = [torch.empty_like(q, device=DEV) for q in (qa, qb)]
-    got = [torch.empty_like(q, device=DEV) for q in (qa, qb)]
-    qs = [qa.to(DEV), qb.to(DEV)]
-    for x, q, o in zip((a, b), qs, ref):
+    c, qc = make_attend("bf16", 128, 2, 2, 2, 40, 64, [900, 1200, 70, 400], seed=33)
+    ref = [torch.empty_like(q, device=DEV) for q in (qa, qb, qc)]
+    got = [torch.empty_like(q, device=DEV) for q in (qa, qb, qc)]
+    qs = [qa.to(DEV), qb.to(DEV), qc.to(DEV)]
+    for x, q, o in zip((a, b, c), qs, ref):
         kvc.kvc_page_attend(x.pool, x.pages, q, o)
     torch.cuda.synchronize()
-    st = [torch.cuda.Stream(), torch.cuda.Stream()]
+    st = [torch.cuda.Stream() for _ in qs]
     ws = [torch.empty(kvc.kvc_page_attend_workspace_size(x.pool, x.pages, q.shape[2], q.shape[1]), dtype=torch.uint8,
-                      device=DEV) for x, q in zip((a, b), qs)]
+                      device=DEV) for x, q in zip((a, b, c), qs)]
     for _ in range(20):
-        for x, q, o, s, w in zip((a, b), qs, got, st, ws):
+        for x, q, o, s, w in zip((a, b, c), qs, got, st, ws):
             kvc.kvc_page_attend(x.pool, x.pages, q, o, workspace=w, stream=s)
     torch.cuda.synchronize()
-    assert torch.equal(ref[0], got[0]) and torch.equal(ref[1], got[1])
+    assert all(torch.equal(r, o) for r, o in zip(ref, got))
 
 
 def test_binding_refuses_wrong_tensors():

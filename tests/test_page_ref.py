@@ -146,3 +146,5 @@ def test_rows_refused(lib):
     assert attend(scale=float("nan")) == -1 and attend(out=None) == -1 and attend(out=0x2008) == -8
     assert attend(lse=0x3001) == -8 and attend(ws=None) == -7 and attend(nb=8) == -7 and attend(ws=0x1000010) == -7
     assert attend(t=_pages(kvc, L=3)) == -1 and attend(T=1 << 30) == -9
+    p.k_scale = 1e20
+    assert attend(scale=1e30) == -1  # their product is no finite number
