@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
 
     float o[NT][KS][4];
     float ref[NT][2], l[NT][2];  // reference minus kOff (0 until a token is seen), this lane's part of the sum
-    bool none[NT][2];
+    float top[NT][2];            // how far over it a logit may lie: -inf until a token is seen
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -221,20 +221,19 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
       for (int e = 0; e < 2; ++e) {
         ref[nt][e] = 0.f;
         l[nt][e] = 0.f;
-        none[nt][e] = true;
+        top[nt][e] = -INFINITY;
       }
     }
 
     for (int i = 0; i < mine && alive; ++i, ++n) {
       const int st = n % kStages;
-      if (!tc::mbar_wait(&bars[warp][st], (n / kStages) & 1)) {
+      if (!__all_sync(kFull, mbar_ready(&bars[warp][st], (n / kStages) & 1)) &&
+          !__all_sync(kFull, mbar_wait_far(&bars[warp][st], (n / kStages) & 1))) {
+        // nothing more is issued; the copies in flight get a second, bounded wait
         if (lane == 0) status_or(a.status, KVC_STATUS_TIMEOUT);
         alive = false;
-      }
-      alive = __all_sync(kFull, alive);
-      if (!alive) {  // nothing more is issued; the copies in flight get a second, bounded wait
         for (int k = 1; k < kStages && i + k < mine; ++k)
-          (void)tc::mbar_wait(&bars[warp][(n + k) % kStages], ((n + k) / kStages) & 1);
+          (void)mbar_wait_far(&bars[warp][(n + k) % kStages], ((n + k) / kStages) & 1);
         break;
       }
       const uint8_t* buf = ring + st * SM::kStage;
@@ -286,54 +285,61 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
         }
       }
 
-      // logits in base 2; what a row does not see is -inf
+      // logits in base 2 over the reference; what a row does not see is -inf
       const bool masked = tok0 + kChunk32 > minlim || ok != 3;
+      float2 y[2][NT][2];  // rows 2t, 2t+1 of token g (first) and g + 8
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[blk][nt][e] *= f[nt][e & 1];
+          for (int h = 0; h < 2; ++h)
+            y[blk][nt][h] = fma2(make_float2(sc[blk][nt][2 * h], sc[blk][nt][2 * h + 1]), make_float2(f[nt][0], f[nt][1]),
+                                 make_float2(-ref[nt][0], -ref[nt][1]));
       if (masked) {
 #pragma unroll
         for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int tok = tok0 + 16 * blk + g + (e >= 2 ? 8 : 0);
-              if (tok >= lim[nt][e & 1] || !(ok >> blk & 1)) sc[blk][nt][e] = -INFINITY;
+            for (int h = 0; h < 2; ++h) {
+              const int tok = tok0 + 16 * blk + g + 8 * h;
+              if (tok >= lim[nt][0] || !(ok >> blk & 1)) y[blk][nt][h].x = -INFINITY;
+              if (tok >= lim[nt][1] || !(ok >> blk & 1)) y[blk][nt][h].y = -INFINITY;
             }
       }
-      // raise the references where a logit passes them by more than 2^kRaise
-      float mx[NT][2];
+      // raise the references where a logit passes them by more than 2^(kOff + kRaise)
+      float2 mx[NT];
       bool raise = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          mx[nt][e] = fmaxf(fmaxf(sc[0][nt][e], sc[0][nt][e + 2]), fmaxf(sc[1][nt][e], sc[1][nt][e + 2]));
-          raise |= none[nt][e] ? mx[nt][e] > -INFINITY : mx[nt][e] > ref[nt][e] + (kOff + kRaise);
-        }
+      for (int nt = 0; nt < NT; ++nt) {
+        mx[nt].x = fmaxf(fmaxf(y[0][nt][0].x, y[0][nt][1].x), fmaxf(y[1][nt][0].x, y[1][nt][1].x));
+        mx[nt].y = fmaxf(fmaxf(y[0][nt][0].y, y[0][nt][1].y), fmaxf(y[1][nt][0].y, y[1][nt][1].y));
+        raise |= mx[nt].x > top[nt][0] || mx[nt].y > top[nt][1];
+      }
       if (__any_sync(kFull, raise)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float m = mx[nt][e];
+            float m = e ? mx[nt].y : mx[nt].x;
             m = fmaxf(m, __shfl_xor_sync(kFull, m, 4));
             m = fmaxf(m, __shfl_xor_sync(kFull, m, 8));
             m = fmaxf(m, __shfl_xor_sync(kFull, m, 16));
-            if (m > -INFINITY && (none[nt][e] || m > ref[nt][e] + kOff)) {
-              const float to = m - kOff, c = none[nt][e] ? 1.f : ex2(ref[nt][e] - to);
-              none[nt][e] = false;
-              ref[nt][e] = to;
+            if (m > top[nt][e] - kRaise) {
+              const float up = m - kOff, c = top[nt][e] == -INFINITY ? 1.f : ex2(-up);
+              ref[nt][e] += up;
+              top[nt][e] = kOff + kRaise;
               l[nt][e] *= c;
 #pragma unroll
               for (int k = 0; k < KS; ++k) {
                 o[nt][k][e] *= c;
                 o[nt][k][e + 2] *= c;
               }
+#pragma unroll
+              for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) (e ? y[blk][nt][h].y : y[blk][nt][h].x) -= up;
             }
           }
       }
@@ -345,14 +351,15 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            const float p0 = ex2(sc[blk][nt][2 * half] - ref[nt][0]), p1 = ex2(sc[blk][nt][2 * half + 1] - ref[nt][1]);
-            l[nt][0] += p0;
-            l[nt][1] += p1;
-            const uint32_t w = pack2(p0, p1);
+            const float2 pr = make_float2(ex2(y[blk][nt][half].x), ex2(y[blk][nt][half].y));
+            const float2 sum = add2(make_float2(l[nt][0], l[nt][1]), pr);
+            l[nt][0] = sum.x;
+            l[nt][1] = sum.y;
+            const uint32_t w = pack2(pr.x, pr.y);
             pf[blk][nt][0][half] = transpose8x8(w);
             if constexpr (PARTS == 2) {
               const float2 b = f16x2_f32(w);
-              pf[blk][nt][1][half] = transpose8x8(pack2(p0 - b.x, p1 - b.y));
+              pf[blk][nt][1][half] = transpose8x8(pack2(pr.x - b.x, pr.y - b.y));
             }
           }
 
@@ -374,10 +381,13 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
             w[e][0] = *reinterpret_cast<const uint32_t*>(vr);
             s[e] = sb[tk * 4 + (g >> 1)];
           }
-          // behind the last visible token lies anything: a zero scale keeps it out of 0 * NaN
-          if (masked && (tok0 + 16 * blk + tk >= x.vis || !(ok >> blk & 1))) s[e] = 0;
         }
-        const uint32_t s01 = e4m3x2_f16x2(s[0] | s[1] << 8), s23 = e4m3x2_f16x2(s[2] | s[3] << 8);
+        if (masked) {  // behind the last visible token lies anything: a zero scale keeps it out of 0 * NaN
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (tok0 + 16 * blk + 2 * t + (e & 1) + (e >= 2 ? 8 : 0) >= x.vis || !(ok >> blk & 1)) s[e] = 0;
+        }
+        const uint32_t s01 = e4m3x2_f16x2(__byte_perm(s[0], s[1], 0x3340)), s23 = e4m3x2_f16x2(__byte_perm(s[2], s[3], 0x3340));
 #pragma unroll
         for (int j = 0; j < CPV / 8; ++j) {
           uint32_t e01[4], o01[4], e23[4], o23[4];
