@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
   }
 }
 
-// One row's parts merged by one warp, from part `first` on every `step`-th, four at a time; E channels a lane.
+// A row's merged parts, E channels a lane.
 template <int E>
 struct Merged {
   float o[E], l = 0.f, m = -INFINITY;
@@ -513,78 +513,68 @@ struct Merged {
     for (int e = 0; e < E; ++e) o[e] = o[e] * c0 + y[e] * c1;
     m = to;
   }
-  __device__ __forceinline__ void parts(const AttendPlan& p, int2 span, int first, int step, int rr, int D) {
-    constexpr int N = 4;
-    const int lane = threadIdx.x & 31;
-    for (int c0 = span.x + first; c0 <= span.y; c0 += N * step) {
-      float2 ml[N];
-      float y[N][E];
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int c = c0 + i * step;
-        ml[i] = make_float2(0.f, 0.f);
-        if (c > span.y) continue;
-        // the first CTA's part begins at the stream's first unit, the others' behind it
-        const size_t row = ((size_t)c * 2 + (c == span.x ? 1 : 0)) * p.rb + rr;
-        ml[i] = p.ml[row];
-        const float* src = p.part + row * D + lane * E;
-        if constexpr (E == 4) {
-          const float4 v = *reinterpret_cast<const float4*>(src);
-          y[i][0] = v.x, y[i][1] = v.y, y[i][2] = v.z, y[i][3] = v.w;
-        } else {
-          const float2 v = *reinterpret_cast<const float2*>(src);
-          y[i][0] = v.x, y[i][1] = v.y;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < N; ++i) add(ml[i].x, ml[i].y, y[i]);
-    }
-  }
 };
 
-// Rows whose stream several CTAs shared, and rows of streams without tokens. Few rows a block (SPLIT): a CTA
-// per row, its warps taking every fourth part. Many rows, whose streams fewer CTAs share: a warp per row.
+// Rows whose stream several CTAs shared, and rows of streams without tokens: a CTA per row, its warps taking
+// every fourth part, four at a time.
 constexpr int kCombThreads = 128, kCombWarps = kCombThreads / 32;
-template <typename T, int D, bool SPLIT>
+template <typename T, int D>
 __global__ void __launch_bounds__(kCombThreads) combine_kernel(AttendArgs a, AttendPlan p) {
   __shared__ float sm_o[kCombWarps][D];
   __shared__ float2 sm_ml[kCombWarps];
   griddep_launch();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = SPLIT ? blockIdx.x : blockIdx.x * kCombWarps + warp;
-  const int vs = row >> p.lrb, rr = row & (p.rb - 1);
-  if (vs >= p.nvs) return;
+  const int vs = blockIdx.x >> p.lrb, rr = blockIdx.x & (p.rb - 1);
   const int2 span = p.span[vs];  // read beside the length; undefined for a stream without units
-  const Stream x = stream_of(a, p, vs, lane == 0 && rr == 0);
+  const Stream x = stream_of(a, p, vs, threadIdx.x == 0 && rr == 0);
   if (rr >= x.rows) return;
   const size_t at = out_row(a, p, x, x.r0 + rr);
   T* op = static_cast<T*>(a.out) + at * D;
-  constexpr int E = D / 32;
+  constexpr int E = D / 32, N = 4;
   if (x.vis == 0) {
-    if (!SPLIT || warp == 0) {
+    if (warp) return;
 #pragma unroll
-      for (int e = 0; e < E; ++e) op[lane * E + e] = from_f32<T>(0.f);
-      if (a.lse && lane == 0) a.lse[at] = -INFINITY;
-    }
+    for (int e = 0; e < E; ++e) op[lane * E + e] = from_f32<T>(0.f);
+    if (a.lse && lane == 0) a.lse[at] = -INFINITY;
     return;
   }
   if (span.x == span.y) return;  // written by that CTA
-  Merged<E> y;
-  y.parts(p, span, SPLIT ? warp : 0, SPLIT ? kCombWarps : 1, rr, D);
-  if constexpr (SPLIT) {
+  Merged<E> r;
+  for (int c0 = span.x + warp; c0 <= span.y; c0 += N * kCombWarps) {
+    float2 ml[N];
+    float y[N][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) sm_o[warp][lane * E + e] = y.o[e];
-    if (lane == 0) sm_ml[warp] = make_float2(y.m, y.l);
-    __syncthreads();
-    if (warp) return;
+    for (int i = 0; i < N; ++i) {
+      const int c = c0 + i * kCombWarps;
+      ml[i] = make_float2(0.f, 0.f);
+      if (c > span.y) continue;
+      // the first CTA's part begins at the stream's first unit, the others' behind it
+      const size_t row = ((size_t)c * 2 + (c == span.x ? 1 : 0)) * p.rb + rr;
+      ml[i] = p.ml[row];
+      const float* src = p.part + row * D + lane * E;
+      if constexpr (E == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(src);
+        y[i][0] = v.x, y[i][1] = v.y, y[i][2] = v.z, y[i][3] = v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(src);
+        y[i][0] = v.x, y[i][1] = v.y;
+      }
+    }
 #pragma unroll
-    for (int w = 1; w < kCombWarps; ++w) y.add(sm_ml[w].x, sm_ml[w].y, &sm_o[w][lane * E]);
+    for (int i = 0; i < N; ++i) r.add(ml[i].x, ml[i].y, y[i]);
   }
-  const float inv = y.l == 0.f ? 0.f : a.g.ts[1] / y.l;
 #pragma unroll
-  for (int e = 0; e < E; ++e) op[lane * E + e] = from_f32<T>(y.o[e] * inv);
-  if (a.lse && lane == 0) a.lse[at] = y.l == 0.f ? -INFINITY : (y.m + log2f(y.l)) * 0.6931471805599453f;
+  for (int e = 0; e < E; ++e) sm_o[warp][lane * E + e] = r.o[e];
+  if (lane == 0) sm_ml[warp] = make_float2(r.m, r.l);
+  __syncthreads();
+  if (warp) return;
+#pragma unroll
+  for (int w = 1; w < kCombWarps; ++w) r.add(sm_ml[w].x, sm_ml[w].y, &sm_o[w][lane * E]);
+  const float inv = r.l == 0.f ? 0.f : a.g.ts[1] / r.l;
+#pragma unroll
+  for (int e = 0; e < E; ++e) op[lane * E + e] = from_f32<T>(r.o[e] * inv);
+  if (a.lse && lane == 0) a.lse[at] = r.l == 0.f ? -INFINITY : (r.m + log2f(r.l)) * 0.6931471805599453f;
 }
 
 // The tcgen05 kernel's parts lie with the rows contiguous: a thread a row, 16 channels a CTA.
@@ -601,20 +591,29 @@ __global__ void __launch_bounds__(kTcRows) combine_tc_kernel(AttendArgs a, Atten
 #pragma unroll
   for (int e = 0; e < C; ++e) o[e] = 0.f;
   if (x.vis) {
-    for (int c = span.x; c <= span.y; ++c) {
-      const size_t slot = (size_t)c * 2 + (c == span.x ? 1 : 0);
-      const float2 ml = p.ml[slot * kTcRows + rr];
-      const float* src = p.part + (slot * D + c0) * kTcRows + rr;
-      float y[C];
+    constexpr int N = 4;  // parts whose reads are in flight at once
+    for (int c1 = span.x; c1 <= span.y; c1 += N) {
+      float2 ml[N];
+      float y[N][C];
 #pragma unroll
-      for (int e = 0; e < C; ++e) y[e] = src[e * kTcRows];
-      if (ml.y == 0.f) continue;
-      const float to = l == 0.f ? ml.x : fmaxf(m, ml.x);
-      const float k0 = l == 0.f ? 0.f : ex2(m - to), k1 = ex2(ml.x - to);
-      l = l * k0 + ml.y * k1;
+      for (int i = 0; i < N; ++i) {
+        const int c = min(c1 + i, span.y);
+        const size_t slot = (size_t)c * 2 + (c == span.x ? 1 : 0);
+        ml[i] = p.ml[slot * kTcRows + rr];
+        const float* src = p.part + (slot * D + c0) * kTcRows + rr;
 #pragma unroll
-      for (int e = 0; e < C; ++e) o[e] = o[e] * k0 + y[e] * k1;
-      m = to;
+        for (int e = 0; e < C; ++e) y[i][e] = src[e * kTcRows];
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (c1 + i > span.y || ml[i].y == 0.f) continue;
+        const float to = l == 0.f ? ml[i].x : fmaxf(m, ml[i].x);
+        const float k0 = l == 0.f ? 0.f : ex2(m - to), k1 = ex2(ml[i].x - to);
+        l = l * k0 + ml[i].y * k1;
+#pragma unroll
+        for (int e = 0; e < C; ++e) o[e] = o[e] * k0 + y[i][e] * k1;
+        m = to;
+      }
     }
   }
   const size_t at = out_row(a, p, x, x.r0 + rr);
@@ -629,19 +628,20 @@ __global__ void __launch_bounds__(kTcRows) combine_tc_kernel(AttendArgs a, Atten
 }
 
 // Row tiles of 8 a block takes: one covers the decode step of up to 8 query heads per KV head; more rows
-// share the decoding of a chunk. From kTcMin rows on bf16 queries go to the tcgen05 kernel.
-constexpr int kTcMin = 33;
+// share the decoding of a chunk. From kTcMin rows on bf16 queries go to the tcgen05 kernel (32 streams of 8192
+// tokens: 16 rows 24.4 us here and 36.6 there, 24 rows 39.2 and 37.3 with four tiles a block here).
+constexpr int kTcMin = 17;
 // Tables of at most kWholeCap tokens: a CTA takes a whole stream, which saves the search for its units and the
 // second kernel (8 heads x 256 tokens: 6.9 us split, 5.9 whole; x 2048: 8.5 and 18.7). With two streams an SM
 // and more that pays up to kWholeCapMany tokens (512 heads x 256: 16.8 and 9.3 us; x 2048: 43 and 37.5).
 constexpr int kWholeCap = 512, kWholeCapMany = 2048;
-constexpr int tiles_for(int R, int parts) { return R <= 8 ? 1 : (R <= 16 || parts == 2) ? 2 : 4; }
+constexpr int tiles_for(int R) { return R <= 8 ? 1 : 2; }
 constexpr int min_blocks(int nt, int parts) { return nt * parts == 1 ? 4 : nt * parts == 2 ? 3 : 2; }
 
 AttendPlan make_plan(const AttendArgs& a, int parts, int sms, size_t* bytes) {
   AttendPlan p = {};
   p.G = a.Hq / a.t.Hkv;
-  const int R = p.G * a.T, nt = tiles_for(R, parts);
+  const int R = p.G * a.T, nt = tiles_for(R);
   const bool tc = parts == 1 && R >= kTcMin;
   p.unit = tc ? kTcUnit : kUnit;
   p.rb = tc ? kTcRows : 8 * nt;
@@ -686,9 +686,6 @@ int run(const AttendArgs& a, int sms, cudaStream_t s) {
   switch (p.rb / 8) {
     case 1: rc = go<T, D, 1, PARTS>(a, p, s); break;
     case 2: rc = go<T, D, 2, PARTS>(a, p, s); break;
-    case 4:
-      if constexpr (PARTS == 1) rc = go<T, D, 4, PARTS>(a, p, s);
-      break;
     case kTcRows / 8:
       if constexpr (PARTS == 1) rc = launch_attend_tc(a, p, s);
       break;
@@ -701,23 +698,17 @@ int run(const AttendArgs& a, int sms, cudaStream_t s) {
                      cudaSuccess
                  ? KVC_OK
                  : KVC_ERR_LAUNCH;
-  const cudaError_t e =
-      p.rb <= 16 ? launch_pdl(combine_kernel<T, D, true>, dim3((unsigned)rows), dim3(kCombThreads), 0, s, false, a, p)
-                 : launch_pdl(combine_kernel<T, D, false>, dim3((unsigned)((rows + kCombWarps - 1) / kCombWarps)),
-                              dim3(kCombThreads), 0, s, false, a, p);
-  return e == cudaSuccess ? KVC_OK : KVC_ERR_LAUNCH;
+  return launch_pdl(combine_kernel<T, D>, dim3((unsigned)rows), dim3(kCombThreads), 0, s, false, a, p) == cudaSuccess
+             ? KVC_OK
+             : KVC_ERR_LAUNCH;
 }
 
 }  // namespace
 
 bool attend_fits(const AttendArgs& a) {  // work units and rows are counted in 32 bits
-  for (int parts = 1; parts <= 2; ++parts) {
-    const int R = a.Hq / a.t.Hkv * a.T, rb = 8 * tiles_for(R, parts);
-    const long long nvs = (long long)a.t.S * ((R + rb - 1) / rb);
-    if (nvs * rb > 0x7fffffffLL || nvs * ((((long long)a.t.maxp << a.g.lp) + kUnit - 1) / kUnit) > 0x7fffffffLL)
-      return false;
-  }
-  return true;
+  const int R = a.Hq / a.t.Hkv * a.T, rb = 8 * tiles_for(R);
+  const long long nvs = (long long)a.t.S * ((R + rb - 1) / rb);
+  return nvs * rb <= 0x7fffffffLL && nvs * ((((long long)a.t.maxp << a.g.lp) + kUnit - 1) / kUnit) <= 0x7fffffffLL;
 }
 
 size_t attend_ws_bytes(const PoolGeom& g, const PageTab& t, int Hq, int T) {
