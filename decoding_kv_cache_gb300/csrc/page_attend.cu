@@ -17,10 +17,11 @@
 // issue; masks and shifts to 4-bit integers with an fma 27 ns.)
 //
 // Work is split by tokens over all CTAs of one wave, whatever the streams' lengths: the 64-token units of
-// all streams form one list, CTA i takes units [W i/grid, W (i+1)/grid). A stream cut by a CTA border leaves
-// partial (max, sum, O) rows in the workspace; the combine kernel merges them (and writes the rows of empty
-// streams). In a CTA each of the four warps takes every fourth 32-token chunk with its own two-stage
-// ring of bulk copies; nothing but the end of a stream's part synchronises them.
+// all streams form one list, each stream led by a few units' worth of starting cost, and every CTA takes an
+// equal run of it. A stream cut by a CTA border leaves partial (max, sum, O) rows in the workspace; the combine
+// kernel merges them (and writes the rows of empty streams). In a CTA each of the four warps takes every fourth
+// 32-token chunk with its own two-stage ring of bulk copies; nothing but the end of a stream's part
+// synchronises them.
 #include "page_attend.cuh"
 
 namespace kvc {
@@ -73,7 +74,7 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
   griddep_wait();
 
   // this CTA's units, and the stream its first one lies in
-  int vs = blockIdx.x, base = 0, ua = 0, left = 1;  // whole: `left` becomes the stream's units
+  int vs = blockIdx.x, base = 0, ca = 0, left = 1;  // whole: `left` becomes the stream's units
   Split split(0, 1);
   if (!p.whole) {
     const int per = (p.nvs + 32 * kWarps - 1) / (32 * kWarps);
@@ -85,7 +86,7 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
     for (int i = 0; i < per; ++i) {
       const int v = threadIdx.x * per + i;
       if (v >= p.nvs) break;
-      const int u = units_of(p, stream_of(a, p, v, false));
+      const int u = cost_of(p, stream_of(a, p, v, false));
       if (before <= w0 && w0 < before + u) {
         sm_first[0] = v;
         sm_first[1] = before;
@@ -94,8 +95,8 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
     }
     __syncthreads();
     vs = sm_first[0];
-    base = sm_first[1];  // units before the stream
-    ua = w0 - base;      // first unit of this CTA in the stream
+    base = sm_first[1];  // cost before the stream
+    ca = w0 - base;
     left = w1 - w0;
   } else {
     const Stream x = stream_of(a, p, vs, threadIdx.x == 0);
@@ -111,12 +112,13 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
   uint32_t n = 0;  // chunks this warp has waited for
   bool alive = true;
 
-  for (int U; left > 0; ++vs, ua = 0, base += U) {
+  for (int C; left > 0; ++vs, ca = 0, base += C) {
     const Stream x = stream_of(a, p, vs, true);
-    U = units_of(p, x);
-    if (U == 0) continue;
-    const int ub = min(U, ua + left);
-    left -= ub - ua;
+    C = cost_of(p, x);
+    if (C == 0) continue;
+    const int cb = min(C, ca + left), ua = max(ca - p.lead, 0), ub = max(cb - p.lead, 0), U = C - p.lead;
+    left -= cb - ca;
+    if (ub == ua) continue;  // only the stream's leading cost
     const int c1 = min(2 * ub, (x.vis + kChunk32 - 1) / kChunk32);  // chunks [2 ua, c1) of the stream
     const int c0 = 2 * ua + warp;
     const int mine = c1 > c0 ? (c1 - c0 + kWarps - 1) / kWarps : 0;
@@ -466,7 +468,7 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
     if (warp == 0) {
       const bool whole = ua == 0 && ub == U;
       // who holds the stream's parts, for the combine kernel
-      if (!p.whole && ua == 0 && lane == 0) p.span[vs] = make_int2(blockIdx.x, whole ? (int)blockIdx.x : split.owner(base + U - 1));
+      if (!p.whole && ua == 0 && lane == 0) p.span[vs] = make_int2(blockIdx.x, whole ? (int)blockIdx.x : split.owner(base + C - 1));
       const size_t slot = (size_t)blockIdx.x * 2 + (ua == 0 ? 1 : 0);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -631,6 +633,10 @@ __global__ void __launch_bounds__(kTcRows) combine_tc_kernel(AttendArgs a, Atten
 // share the decoding of a chunk. From kTcMin rows on bf16 queries go to the tcgen05 kernel (32 streams of 8192
 // tokens: 16 rows 24.4 us here and 36.6 there, 24 rows 39.2 and 37.3 with four tiles a block here).
 constexpr int kTcMin = 17;
+// What beginning a stream's part costs, in units (query rows read, the ring or pipeline filled, results merged):
+// counted when the work is split, so that a CTA with two parts gets less (64 new tokens over 4 x 8192: 46.7 us
+// with none, 43.1 with 5; 16 x 8 heads of up to 1000 tokens 13.0 and 10.8 us with 3).
+constexpr int kTcLead = 5, kLead = 3;
 // Tables of at most kWholeCap tokens: a CTA takes a whole stream, which saves the search for its units and the
 // second kernel (8 heads x 256 tokens: 6.9 us split, 5.9 whole; x 2048: 8.5 and 18.7). With two streams an SM
 // and more that pays up to kWholeCapMany tokens (512 heads x 256: 16.8 and 9.3 us; x 2048: 43 and 37.5).
@@ -644,6 +650,7 @@ AttendPlan make_plan(const AttendArgs& a, int parts, int sms, size_t* bytes) {
   const int R = p.G * a.T, nt = tiles_for(R);
   const bool tc = parts == 1 && R >= kTcMin;
   p.unit = tc ? kTcUnit : kUnit;
+  p.lead = tc ? kTcLead : kLead;
   p.rb = tc ? kTcRows : 8 * nt;
   p.nrb = (R + p.rb - 1) / p.rb;
   p.nvs = a.t.S * p.nrb;
@@ -653,10 +660,12 @@ AttendPlan make_plan(const AttendArgs& a, int parts, int sms, size_t* bytes) {
   while ((1 << p.lrb) < p.rb) ++p.lrb;
   sms = sms < kMaxGridSMs ? sms : kMaxGridSMs;
   p.grid = sms * (tc ? 1 : min_blocks(nt, parts));
-  const long long cap = (long long)a.t.maxp << a.g.lp, units = (long long)p.nvs * ((cap + p.unit - 1) / p.unit);
-  if (units < p.grid) p.grid = (int)units;
+  const long long cap = (long long)a.t.maxp << a.g.lp;
+  const long long cost = (long long)p.nvs * ((cap + p.unit - 1) / p.unit + p.lead);  // if every stream is full
+  if (cost < p.grid) p.grid = (int)cost;
   if (!tc && cap <= (p.nvs >= 2 * sms ? kWholeCapMany : kWholeCap)) {
     p.whole = 1;
+    p.lead = 0;
     p.grid = p.nvs;
     if (bytes) *bytes = 256;
     return p;
@@ -708,7 +717,7 @@ int run(const AttendArgs& a, int sms, cudaStream_t s) {
 bool attend_fits(const AttendArgs& a) {  // work units and rows are counted in 32 bits
   const int R = a.Hq / a.t.Hkv * a.T, rb = 8 * tiles_for(R);
   const long long nvs = (long long)a.t.S * ((R + rb - 1) / rb);
-  return nvs * rb <= 0x7fffffffLL && nvs * ((((long long)a.t.maxp << a.g.lp) + kUnit - 1) / kUnit) <= 0x7fffffffLL;
+  return nvs * rb <= 0x7fffffffLL && nvs * ((((long long)a.t.maxp << a.g.lp) + kUnit - 1) / kUnit + kTcLead) <= 0x7fffffffLL;
 }
 
 size_t attend_ws_bytes(const PoolGeom& g, const PageTab& t, int Hq, int T) {

@@ -12,6 +12,7 @@ constexpr float kRaise = 5.f;  // a reference may lag the maximum by 2^5: 2^15 a
 
 struct AttendPlan {
   int unit;    // tokens of a work unit
+  int lead;    // units that beginning a stream's part counts for, when the work is split
   int nrb;     // row blocks per stream
   int rb, lrb;  // rows per block (a power of two) and its logarithm
   int G;
@@ -59,14 +60,15 @@ __device__ __forceinline__ int seen_by(const AttendPlan& p, const Stream& x, int
   return min(max(x.len - x.nq + p.by_G.div(r) + 1, 0), x.vis);
 }
 __device__ __forceinline__ int units_of(const AttendPlan& p, const Stream& x) { return (x.vis + p.unit - 1) / p.unit; }
+__device__ __forceinline__ int cost_of(const AttendPlan& p, const Stream& x) { return x.vis ? units_of(p, x) + p.lead : 0; }
 
-// Units before each thread's run of streams and in all (block of kThr threads; every thread calls).
+// Cost, in units, before each thread's run of streams and in all (block of kThr threads; every thread calls).
 template <int kThr>
 __device__ __forceinline__ int scan_units(const AttendArgs& a, const AttendPlan& p, int* sm, int per, int* total) {
   int mine = 0;
   for (int i = 0; i < per; ++i) {
     const int vs = threadIdx.x * per + i;
-    if (vs < p.nvs) mine += units_of(p, stream_of(a, p, vs, false));
+    if (vs < p.nvs) mine += cost_of(p, stream_of(a, p, vs, false));
   }
   int incl = mine;
 #pragma unroll
@@ -87,7 +89,7 @@ __device__ __forceinline__ int scan_units(const AttendArgs& a, const AttendPlan&
   return base + incl - mine;
 }
 
-// CTA i of `grid` takes units [first(i), first(i + 1)) of W: the first W % grid CTAs one more than the others.
+// CTA i of `grid` takes [first(i), first(i + 1)) of the cost W, units and streams' leads: the first W % grid CTAs one more than the others.
 struct Split {
   int q, rem;
   __device__ __forceinline__ Split(int W, int grid) : q(W / grid), rem(W % grid) {}

@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
   for (int i = 0; i < per; ++i) {
     const int vs = threadIdx.x * per + i;
     if (vs >= p.nvs) break;
-    const int u = units_of(p, stream_of(a, p, vs, false));
+    const int u = cost_of(p, stream_of(a, p, vs, false));
     if (before <= w0 && w0 < before + u) {
       sm_first[0] = vs;
       sm_first[1] = before;
@@ -190,16 +190,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
   volatile int* ab = &abort_flag;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_ready(bar, parity) || wait_slow(bar, parity, ab, a.status); };
 
-  // Every role walks the same parts: f(stream, vs, first unit, end unit, units of the stream, units before it)
+  // Every role walks the same parts: f(stream, vs, first unit, end unit, units of the stream, cost before them).
+  // A stream begins with `lead` units of cost and no work, so that a CTA that begins another stream gets less.
   auto parts = [&](auto&& f) {
-    int vs = sm_first[0], base = sm_first[1], left = w1 - w0, ua = w0 - base;
-    for (int U; left > 0; ++vs, ua = 0, base += U) {
+    int vs = sm_first[0], base = sm_first[1], left = w1 - w0, ca = w0 - base;
+    for (int C; left > 0; ++vs, ca = 0, base += C) {
       const Stream x = stream_of(a, p, vs, false);
-      U = units_of(p, x);
-      if (U == 0) continue;
-      const int ub = min(U, ua + left);
-      left -= ub - ua;
-      if (!f(x, vs, ua, ub, U, base)) return;
+      C = cost_of(p, x);
+      if (C == 0) continue;
+      const int cb = min(C, ca + left), ua = max(ca - p.lead, 0), ub = max(cb - p.lead, 0);
+      left -= cb - ca;
+      if (ub > ua && !f(x, vs, ua, ub, C - p.lead, base + p.lead)) return;
     }
   };
 
@@ -328,8 +329,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
       {
         // the query rows, each brought to [256, 512) by a power of two (bf16 values exact in fp16), with the
         // scale's sign, so that maxima of dot products are maxima of logits. A warp takes 16 rows, D/8 lanes
-        // a row, four reads in flight.
-        constexpr int kLanes = D / 8, kAt = 32 / kLanes, kBatch = 4;  // lanes of a row, rows at a time, reads in flight
+        // a row, all of its reads in flight at once.
+        constexpr int kLanes = D / 8, kAt = 32 / kLanes, kBatch = 16 / kAt;  // lanes of a row, rows at a time, reads in flight
         const int i = lane % kLanes;
 #pragma unroll 1
         for (int k0 = 0; k0 < 16 / kAt; k0 += kBatch) {

@@ -495,7 +495,8 @@ def _rows(x: torch.Tensor, shape, pool: Pool, what: str):
     s = x.stride()
     if x.device != pool.device or x.shape != shape or s[3] != 1:
         raise ValueError(f"{what} must be a {tuple(shape)} tensor on {pool.device} with contiguous channels")
-    return x.data_ptr(), _Strides(s[0], s[1], s[2])
+    # a dimension of one row has no stride that counts
+    return x.data_ptr(), _Strides(s[0] if shape[0] > 1 else 0, s[1] if shape[1] > 1 else 0, s[2] if shape[2] > 1 else 0)
 
 
 def kvc_page_store(pool: Pool, pages: Pages, k: torch.Tensor, v: torch.Tensor, start: torch.Tensor,
