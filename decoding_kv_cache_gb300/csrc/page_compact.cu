@@ -8,8 +8,9 @@
 // that another stream shares is not written: the stream takes a fresh page in its place, and the old
 // page stays as the source. And the pages behind the kept rows are given back.
 //
-//   plan   a CTA per stream clears its share of the bitmap, checks the list, finds the first row that moves and lists the destination
-//          pages (marking those to be replaced); refs are read here only, before any stream's change
+//   plan   a CTA per stream clears its share of the bitmap, checks the list, finds the first row that moves and
+//          lists the destination pages (marking those to be replaced); refs are read here only, before any
+//          stream's change
 //   move   a CTA per stream and per K or V numbers the fresh pages (in stream order) and sweeps
 //   finish rows and lengths take their new values, pages are counted down, and those nobody holds any
 //          more join the free list (page_ops.cu)

@@ -404,6 +404,18 @@ def test_attend_many_units_a_cta(dt, D, G, T, n):
             assert (np.abs(lse[b, i].double().cpu().numpy() - ref["lse"]) <= ltol).all()
 
 
+@pytest.mark.parametrize("dt,D,G,T", [("bf16", 128, 4, 1), ("bf16", 64, 2, 10), ("f32", 64, 4, 3), ("bf16", 128, 4, 40)])
+@pytest.mark.parametrize("seed", [0, 1])
+def test_attend_many_short_streams(dt, D, G, T, seed):
+    """Streams of no, one and few units between long ones: shares that hold only a stream's beginning."""
+    rng = np.random.default_rng(seed)
+    B, Hkv = 12, 5
+    lens = rng.choice([0, 1, 2, 63, 64, 65, 127, 128, 129, 200, 600], B * Hkv).tolist()
+    lens[int(rng.integers(B * Hkv))] = 1500
+    x, q = make_attend(dt, D, B, Hkv, G, T, 64, lens, seed=seed)
+    check_attend(x, q, dt)
+
+
 @pytest.mark.parametrize("dt,T", [("bf16", 6), ("bf16", 30), ("f32", 6)])
 def test_attend_strided_ragged_scaled(dt, T):
     x, q0 = make_attend(dt, 128, 4, 2, 3, T, 32, [90, 80, 3, 4, 50, 60, 0, 0], seed=5, k_scale=0.3, v_scale=7.0)
