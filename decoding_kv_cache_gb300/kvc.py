@@ -418,10 +418,13 @@ def _page_call(name: str, pool: Pool, pages: Optional[Pages], stream, args):
         _check(rc)
 
 
-def _page_ws(nbytes, pool: Pool, workspace):
+def _page_ws(nbytes, pool: Pool, workspace, stream):
     """(pointer, bytes, tensor) of the caller's workspace, or of one of nbytes() made for this call."""
     if workspace is None:
         workspace = torch.empty(max(nbytes(), 256), dtype=torch.uint8, device=pool.device)
+        if stream is not None:  # it belongs to the current stream: not given out again before `stream` is done
+            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
+                                    torch.cuda.ExternalStream(_stream(stream), device=pool.device))
     elif workspace.device != pool.device or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous and on the pool's device")
     return workspace.data_ptr(), workspace.nbytes, workspace
@@ -450,7 +453,7 @@ def kvc_page_extend(pool: Pool, pages: Pages, add: Optional[torch.Tensor] = None
     """Room for ``add`` [B] (or ``add_all``) more tokens in every stream; ``start`` [L, B, Hkv] receives the
     old lengths (see kvc.h)."""
     dev = pool.device
-    wp, wb, ws = _page_ws(lambda: kvc_page_workspace_size(pool, pages), pool, workspace)
+    wp, wb, ws = _page_ws(lambda: kvc_page_workspace_size(pool, pages), pool, workspace, stream)
     _page_call("kvc_page_extend", pool, pages, stream,
                (_ints(add, (pages.shape[1],), dev, "add"), int(add_all), _ints(start, pages.shape, dev, "start"),
                 _word(status, pool), wp, wb))
@@ -459,7 +462,7 @@ def kvc_page_extend(pool: Pool, pages: Pages, add: Optional[torch.Tensor] = None
 def kvc_page_free(pool: Pool, pages: Pages, drop: Optional[torch.Tensor] = None, drop_all: int = 0,
                   status: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
     """The last ``drop`` [B] (or ``drop_all``) tokens of every stream go, with the pages they leave empty."""
-    wp, wb, ws = _page_ws(lambda: kvc_page_workspace_size(pool, pages), pool, workspace)
+    wp, wb, ws = _page_ws(lambda: kvc_page_workspace_size(pool, pages), pool, workspace, stream)
     _page_call("kvc_page_free", pool, pages, stream,
                (_ints(drop, (pages.shape[1],), pool.device, "drop"), int(drop_all), _word(status, pool), wp, wb))
 
@@ -469,7 +472,7 @@ def kvc_page_fork(pool: Pool, pages: Pages, parent: torch.Tensor, out: Pages, st
     """``out``'s sequence c becomes a copy of ``pages``' sequence ``parent[c]``; ``pages`` is given up."""
     if out.device != pool.device:
         raise ValueError("the pool and its pages are on different devices")
-    wp, wb, ws = _page_ws(lambda: kvc_page_workspace_size(pool, pages), pool, workspace)
+    wp, wb, ws = _page_ws(lambda: kvc_page_workspace_size(pool, pages), pool, workspace, stream)
     _page_call("kvc_page_fork", pool, pages, stream,
                (_ints(parent, (out.shape[1],), pool.device, "parent"), out.ref, _word(status, pool), wp, wb))
 
@@ -480,7 +483,7 @@ def kvc_page_compact(pool: Pool, pages: Pages, kept_idx: torch.Tensor, kept_len:
     kvc_select's) or per sequence ([B, n] and [B], as kvc_epikv_evict's)."""
     per_seq = kept_idx.dim() == 2
     lead = (pages.shape[1],) if per_seq else pages.shape
-    wp, wb, ws = _page_ws(lambda: kvc_page_workspace_size(pool, pages), pool, workspace)
+    wp, wb, ws = _page_ws(lambda: kvc_page_workspace_size(pool, pages), pool, workspace, stream)
     _page_call("kvc_page_compact", pool, pages, stream,
                (_ints(kept_idx, lead + (kept_idx.shape[-1],), pool.device, "kept_idx"),
                 _ints(kept_len, lead, pool.device, "kept_len"), kept_idx.shape[-1], int(per_seq), _word(status, pool),
@@ -544,7 +547,7 @@ def kvc_page_attend(pool: Pool, pages: Pages, q: torch.Tensor, out: torch.Tensor
         raise ValueError("q must be a [B, T, Hq, D] tensor")
     _, T, Hq, D = q.shape
     qp, qs = _rows(q, (B, T, Hq, pool.D), pool, "q")
-    wp, wb, ws = _page_ws(lambda: kvc_page_attend_workspace_size(pool, pages, Hq, T), pool, workspace)
+    wp, wb, ws = _page_ws(lambda: kvc_page_attend_workspace_size(pool, pages, Hq, T), pool, workspace, stream)
     _page_call("kvc_page_attend", pool, pages, stream,
                (_dtype_code(q), Hq, T, qp, qs, _ints(n_q, (B,), pool.device, "n_q"),
                 float(D ** -0.5 if scale is None else scale), _ints(out, q.shape, pool.device, "out", q.dtype),

@@ -646,6 +646,28 @@ def test_streams_with_their_own_workspaces():
     assert all(torch.equal(r, o) for r, o in zip(ref, got))
 
 
+@pytest.mark.parametrize("handle", [False, True])
+def test_a_calls_own_workspace_outlives_it_on_another_stream(handle):
+    from decoding_kv_cache_gb300 import kvc
+    x, q = make_attend("bf16", 128, 2, 2, 4, 1, 64, [900, 30, 700, 0], seed=34)
+    qd = q.to(DEV)
+    ref, got = torch.empty_like(qd), torch.empty_like(qd)
+    kvc.kvc_page_attend(x.pool, x.pages, qd, ref)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(50_000_000)  # some 25 ms
+    stream = s.cuda_stream if handle else s
+    n = 3 << 20
+    p, size, ws = kvc._page_ws(lambda: n, x.pool, None, stream)
+    assert size == n
+    del ws
+    assert torch.empty(n, dtype=torch.uint8, device=DEV).data_ptr() != p
+    kvc.kvc_page_attend(x.pool, x.pages, qd, got, stream=stream)
+    torch.cuda.synchronize()
+    assert torch.equal(ref, got)
+
+
 def test_binding_refuses_wrong_tensors():
     from decoding_kv_cache_gb300 import kvc
     pool, pages = kvc.Pool.empty(8, 64, 16, device=DEV), kvc.Pages.empty(2, 2, 2, 4, device=DEV)
