@@ -684,7 +684,9 @@ template <typename T, int D, int NT, int PARTS>
 int go(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
   auto k = attend_kernel<T, D, NT, PARTS, min_blocks(NT, PARTS)>;
   constexpr int smem = Smem<D, NT>::bytes;
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return KVC_ERR_LAUNCH;
+  if (smem > 47 * 1024 &&  // beyond the default, beside the kernel's static part
+      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return KVC_ERR_LAUNCH;
   return launch_pdl(k, dim3(p.grid), dim3(32 * kWarps), smem, s, false, a, p) == cudaSuccess ? KVC_OK : KVC_ERR_LAUNCH;
 }
 

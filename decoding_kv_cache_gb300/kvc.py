@@ -8,6 +8,7 @@ Names and argument order follow the C entry points.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 from typing import Optional, Sequence, Union
 
@@ -409,7 +410,7 @@ def _page_call(name: str, pool: Pool, pages: Optional[Pages], stream, args):
         raise ValueError("the pool and its pages are on different devices")
     stream = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream(stream)
     f = getattr(_lib or lib(), name)
-    if dev.index == torch.cuda.current_device():
+    if dev.index == torch._C._cuda_getDevice():
         rc = f(pool.ref, None if pages is None else pages.ref, *args, stream)
     else:
         with torch.cuda.device(dev):
@@ -493,13 +494,18 @@ def kvc_page_compact(pool: Pool, pages: Pages, kept_idx: torch.Tensor, kept_len:
 _Strides = C.c_int64 * 3
 
 
+@functools.lru_cache(maxsize=256)
+def _strides(b: int, t: int, h: int):
+    return _Strides(b, t, h)  # read by the call only
+
+
 def _rows(x: torch.Tensor, shape, pool: Pool, what: str):
     """The pointer and strides of [B, T, heads, D] rows with contiguous channels."""
     s = x.stride()
     if x.device != pool.device or x.shape != shape or s[3] != 1:
         raise ValueError(f"{what} must be a {tuple(shape)} tensor on {pool.device} with contiguous channels")
     # a dimension of one row has no stride that counts
-    return x.data_ptr(), _Strides(s[0] if shape[0] > 1 else 0, s[1] if shape[1] > 1 else 0, s[2] if shape[2] > 1 else 0)
+    return x.data_ptr(), _strides(s[0] if shape[0] > 1 else 0, s[1] if shape[1] > 1 else 0, s[2] if shape[2] > 1 else 0)
 
 
 def kvc_page_store(pool: Pool, pages: Pages, k: torch.Tensor, v: torch.Tensor, start: torch.Tensor,
@@ -507,7 +513,7 @@ def kvc_page_store(pool: Pool, pages: Pages, k: torch.Tensor, v: torch.Tensor, s
     """One layer's new rows ``k``, ``v`` [B, T, Hkv, D] (any batch, token and head strides that are multiples of
     16 bytes) into tokens ``start`` [1, B, Hkv] and on; ``n`` [B] rows of them (default all T)."""
     _, B, Hkv = pages.shape
-    if k.dim() != 4 or v.dtype != k.dtype:
+    if k.dim() != 4 or v.dtype is not k.dtype:
         raise ValueError("k and v must be [B, T, Hkv, D] tensors of one dtype")
     shape = (B, k.shape[1], Hkv, pool.D)
     kp, ks = _rows(k, shape, pool, "k")
@@ -525,16 +531,14 @@ def kvc_page_read(pool: Pool, pages: Pages, k: Optional[torch.Tensor] = None, v:
     x = k if k is not None else v
     if x is None:
         raise ValueError("kvc_page_read needs k or v")
-    if x.dim() != 5 or tuple(x.shape[:3]) != pages.shape or x.shape[4] != pool.D:
+    shape = x.shape
+    if len(shape) != 5 or shape[:3] != pages.shape or shape[4] != pool.D:
         raise ValueError("k and v must be [L, B, Hkv, ncap, D] tensors")
-    for t in (k, v):
-        if t is not None and (t.shape != x.shape or t.dtype != x.dtype or t.device != pool.device or not t.is_contiguous()):
-            raise ValueError("k and v must be contiguous [L, B, Hkv, ncap, D] tensors of one dtype on the pool's device")
-    ncap = x.shape[3]
+    ncap = shape[3]
     _page_call("kvc_page_read", pool, pages, stream,
                (_dtype_code(x), _ints(first, pages.shape, pool.device, "first"), int(first_all),
-                ncap if count is None else int(count), None if k is None else k.data_ptr(),
-                None if v is None else v.data_ptr(), ncap, _word(status, pool)))
+                ncap if count is None else int(count), _ints(k, shape, pool.device, "k", x.dtype),
+                _ints(v, shape, pool.device, "v", x.dtype), ncap, _word(status, pool)))
 
 
 def kvc_page_attend(pool: Pool, pages: Pages, q: torch.Tensor, out: torch.Tensor, lse: Optional[torch.Tensor] = None,
@@ -543,12 +547,13 @@ def kvc_page_attend(pool: Pool, pages: Pages, q: torch.Tensor, out: torch.Tensor
     """Attention of ``q`` [B, T, Hq, D] (strided like kvc_page_store's rows), the newest T tokens' queries, over
     one layer of the cache; ``out`` [B, T, Hq, D], ``lse`` [B, T, Hq] fp32; ``scale`` defaults to 1/sqrt(D)."""
     B = pages.shape[1]
-    if q.dim() != 4:
+    shape = q.shape
+    if len(shape) != 4:
         raise ValueError("q must be a [B, T, Hq, D] tensor")
-    _, T, Hq, D = q.shape
+    _, T, Hq, D = shape
     qp, qs = _rows(q, (B, T, Hq, pool.D), pool, "q")
     wp, wb, ws = _page_ws(lambda: kvc_page_attend_workspace_size(pool, pages, Hq, T), pool, workspace, stream)
     _page_call("kvc_page_attend", pool, pages, stream,
                (_dtype_code(q), Hq, T, qp, qs, _ints(n_q, (B,), pool.device, "n_q"),
-                float(D ** -0.5 if scale is None else scale), _ints(out, q.shape, pool.device, "out", q.dtype),
+                float(D ** -0.5 if scale is None else scale), _ints(out, shape, pool.device, "out", q.dtype),
                 _ints(lse, (B, T, Hq), pool.device, "lse", torch.float32), _word(status, pool), wp, wb))
