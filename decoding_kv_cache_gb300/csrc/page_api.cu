@@ -47,7 +47,8 @@ int check_pages(const kvc_pages* p, int lp, PageTab* t) {
       (long long)p->L * p->B * p->Hkv > most)
     return KVC_ERR_TOO_LARGE;
   const long long S = (long long)p->L * p->B * p->Hkv;
-  if (((long long)p->maxp << lp) > (1LL << 30) || S * p->maxp > (1LL << 31)) return KVC_ERR_TOO_LARGE;
+  // page totals of a call are 32-bit sums: every entry filled at once has to fit
+  if (((long long)p->maxp << lp) > (1LL << 30) || S * p->maxp >= (1LL << 31)) return KVC_ERR_TOO_LARGE;
   if (!at4(p->table) || !at4(p->len)) return KVC_ERR_ALIGNMENT;
   *t = PageTab{p->L, p->B, p->Hkv, (int)S, p->maxp, p->table, p->len};
   return KVC_OK;

@@ -444,7 +444,7 @@ typedef struct {
 
 typedef struct {
   int32_t L, B, Hkv; /* L * B * Hkv <= 2^20 streams */
-  int32_t maxp;      /* pages a stream can hold; maxp * page <= 2^30 */
+  int32_t maxp;      /* pages a stream can hold; maxp * page <= 2^30, L * B * Hkv * maxp < 2^31 */
   int32_t* table;    /* [L,B,Hkv,maxp] page numbers (device) */
   int32_t* len;      /* [L,B,Hkv] tokens (device) */
 } kvc_pages;

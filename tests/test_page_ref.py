@@ -148,3 +148,18 @@ def test_rows_refused(lib):
     assert attend(t=_pages(kvc, L=3)) == -1 and attend(T=1 << 30) == -9
     p.k_scale = 1e20
     assert attend(scale=1e30) == -1  # their product is no finite number
+
+
+def test_page_totals_stay_in_32_bits(lib):
+    """2^20 streams of 2^11 entries: a call could ask for 2^31 pages, one more than its 32-bit sums hold."""
+    from decoding_kv_cache_gb300 import kvc
+    p, o = _pool(kvc, page=16), _pages(kvc, L=16, B=256, Hkv=256, maxp=1 << 11, table=0x900000000, len=0xf00000000)
+    ws, nb = 0x1000000, 1 << 50
+    t = _pages(kvc, L=16, B=256, Hkv=256, maxp=(1 << 11) - 1)
+    assert lib.kvc_page_workspace_size(C.byref(p), C.byref(t)) > 0
+    assert lib.kvc_page_workspace_size(C.byref(p), C.byref(o)) == 0
+    assert lib.kvc_page_init(C.byref(p), C.byref(o), None) == -9
+    assert lib.kvc_page_extend(C.byref(p), C.byref(o), None, 16, None, None, ws, nb, None) == -9
+    assert lib.kvc_page_free(C.byref(p), C.byref(o), None, 16, None, ws, nb, None) == -9
+    assert lib.kvc_page_fork(C.byref(p), C.byref(t), 0x1000, C.byref(o), None, ws, nb, None) == -9
+    assert lib.kvc_page_compact(C.byref(p), C.byref(o), 0x1000, 0x1000, 8, 0, None, ws, nb, None) == -9
