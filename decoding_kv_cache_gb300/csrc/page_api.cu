@@ -156,8 +156,9 @@ int kvc_page_fork(const kvc_pool* pool, const kvc_pages* pages, const int32_t* p
   int rc = check_pool(pool, &g);
   if (rc || (rc = check_pages(pages, g.lp, &t)) || (rc = check_pages(out, g.lp, &o))) return rc;
   if (!parent || o.L != t.L || o.Hkv != t.Hkv || o.maxp != t.maxp) return KVC_ERR_INVALID_ARG;
-  const size_t nt = (size_t)t.S * t.maxp * 4, no = (size_t)o.S * o.maxp * 4;
-  if (overlap(t.table, nt, o.table, no) || overlap(t.len, (size_t)t.S * 4, o.len, (size_t)o.S * 4))
+  const size_t nt = (size_t)t.S * t.maxp * 4, no = (size_t)o.S * o.maxp * 4, lt = (size_t)t.S * 4, lo = (size_t)o.S * 4;
+  if (overlap(t.table, nt, o.table, no) || overlap(t.len, lt, o.len, lo) || overlap(t.table, nt, o.len, lo) ||
+      overlap(t.len, lt, o.table, no) || overlap(o.table, no, o.len, lo))
     return KVC_ERR_INVALID_ARG;
   if ((rc = check_ws(g, t, workspace, ws_bytes, &w))) return rc;
   return launch_page_fork(g, t, parent, o, status, w, static_cast<cudaStream_t>(stream));

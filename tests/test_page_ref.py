@@ -163,3 +163,13 @@ def test_page_totals_stay_in_32_bits(lib):
     assert lib.kvc_page_free(C.byref(p), C.byref(o), None, 16, None, ws, nb, None) == -9
     assert lib.kvc_page_fork(C.byref(p), C.byref(t), 0x1000, C.byref(o), None, ws, nb, None) == -9
     assert lib.kvc_page_compact(C.byref(p), C.byref(o), 0x1000, 0x1000, 8, 0, None, ws, nb, None) == -9
+
+
+def test_fork_refuses_arrays_that_overlap_crosswise(lib):
+    """The children's table in the parents' lengths, or their lengths in the parents' table."""
+    from decoding_kv_cache_gb300 import kvc
+    p, t = _pool(kvc), _pages(kvc)  # table: 2 * 2 * 8 words at 0x100000, len: 4 words at 0x200000
+    for kw in (dict(table=0x200000 - 64, len=0xa00000), dict(table=0x900000, len=0x100000 + 124),
+               dict(table=0x900000, len=0x900000 + 64)):
+        o = _pages(kvc, **kw)
+        assert lib.kvc_page_fork(C.byref(p), C.byref(t), 0x1000, C.byref(o), None, 0x1000000, 1 << 40, None) == -1
