@@ -85,7 +85,7 @@ int check_queries(const kvc_cache* c, const void* q_recent, int n_r, const void*
 }
 
 namespace {
-std::atomic<int> g_debug_fault{0};  // test-only fault switch, read at each scoring launch
+std::atomic<int> g_debug_fault{0};  // test-only fault switch, read at each scoring launch and paged attention
 }
 
 // Rotary angles of step t in fp64 (BeaconKV write-up, "打分时的 RoPE 对齐": beacons are turned
@@ -134,6 +134,9 @@ void fill_score_args(ScoreArgs* a, const CacheGeom& g, int dtype, const LayerPtr
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 }  // namespace
+
+int debug_fault_mode() { return g_debug_fault.load(); }
+
 }  // namespace kvc
 
 using namespace kvc;
@@ -143,7 +146,7 @@ extern "C" {
 int kvc_abi_version(void) { return KVC_ABI_VERSION; }
 
 int kvc_debug_fault(int32_t mode) {
-  if (mode < 0 || mode > 1) return KVC_ERR_INVALID_ARG;
+  if (mode < 0 || mode > 2) return KVC_ERR_INVALID_ARG;
   g_debug_fault.store(mode);
   return KVC_OK;
 }

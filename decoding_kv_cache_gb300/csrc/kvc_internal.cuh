@@ -104,6 +104,7 @@ struct AppendArgs {         // kvc_append, flattened over query heads
   int ring_slot;            // t mod n_r
   float2 rope[64];          // (cos, sin) of t * theta^(-2i/D), i < D/2, from fp64 (when q_post is null)
 };
+int debug_fault_mode();  // of kvc_debug_fault
 int launch_append(const AppendArgs& a, int dtype, int D, cudaStream_t s);
 
 int launch_fps_update(int dtype, int nheads_q, int D, void* qbuf, int qmax, int32_t* count, int32_t* picks,

@@ -150,6 +150,7 @@ struct AttendArgs {
   float scale;         // of the dot products, k_scale included
   int32_t* status;
   void* ws;
+  int fault;  // kvc_debug_fault 2 (0 in normal use)
 };
 bool attend_fits(const AttendArgs& a);
 size_t attend_ws_bytes(const PoolGeom& g, const PageTab& t, int Hq, int T);

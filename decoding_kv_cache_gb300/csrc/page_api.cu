@@ -254,6 +254,7 @@ int kvc_page_attend(const kvc_pool* pool, const kvc_pages* pages, int32_t dtype,
   a.scale = scale * a.g.ts[0];
   a.status = status;
   a.ws = workspace;
+  a.fault = debug_fault_mode() == 2;
   return launch_page_attend(a, dtype, static_cast<cudaStream_t>(stream));
 }
 

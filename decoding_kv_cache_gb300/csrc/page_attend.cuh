@@ -139,8 +139,15 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
-// One poll of a barrier in line; the waiting (bounded, false when it gives up) out of line, so that the loops
-// stay short.
+// One poll of a barrier in line; the waiting out of line, so that the loops stay short. A poll suspends the
+// thread for as long as the hardware likes, so the waits are bounded by the clock (false when they give up), and
+// the vote keeps a warp together: no lane may leave a loop whose other lanes then wait for it.
+constexpr uint64_t kWaitNs = 1000000000;
+__device__ __forceinline__ uint64_t clock_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %globaltimer;\n" : "=l"(t));
+  return t;
+}
 __device__ __forceinline__ bool mbar_ready(uint64_t* bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
@@ -150,7 +157,22 @@ __device__ __forceinline__ bool mbar_ready(uint64_t* bar, uint32_t parity) {
       : "memory");
   return done;
 }
-__device__ __noinline__ static bool mbar_wait_far(uint64_t* bar, uint32_t parity) { return tc::mbar_wait(bar, parity); }
+// by whole warps; gave_up() says that nothing will come any more
+template <typename F>
+__device__ __forceinline__ bool mbar_wait_until(uint64_t* bar, uint32_t parity, F&& gave_up) {
+  uint64_t since = 0;
+  while (!__any_sync(kFull, gave_up())) {
+    for (int i = 0; i < 256; ++i)
+      if (__all_sync(kFull, mbar_ready(bar, parity))) return true;
+    const uint64_t now = clock_ns();
+    if (since == 0) since = now;
+    if (__any_sync(kFull, now - since > kWaitNs)) return false;
+  }
+  return false;
+}
+__device__ __noinline__ static bool mbar_wait_far(uint64_t* bar, uint32_t parity) {
+  return mbar_wait_until(bar, parity, [] { return false; });
+}
 
 // The kernel for many query rows (tcgen05, 128 rows a block).
 constexpr int kTcRows = 128, kTcUnit = 128;

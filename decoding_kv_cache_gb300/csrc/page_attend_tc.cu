@@ -52,9 +52,12 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(tc::smem_u32(bar)) : "memory");
 }
 // The first poll in line, the waiting out of it (the roles' loops stay short: five warps of different roles
-// share an SM quarter's instruction cache).
+// share an SM quarter's instruction cache). Gives up as soon as another role has.
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
-  return wait_or_abort(bar, parity, abort_flag, status);
+  if (mbar_wait_until(bar, parity, [&] { return *abort_flag != 0; })) return true;
+  if (!*abort_flag) status_or(status, KVC_STATUS_TIMEOUT);
+  *abort_flag = 1;
+  return false;
 }
 __device__ __forceinline__ bool elect_one() {
   uint32_t e;
@@ -188,7 +191,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
   tc::fence_after_sync();
   const uint32_t tmem = tmem_slot;
   volatile int* ab = &abort_flag;
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_ready(bar, parity) || wait_slow(bar, parity, ab, a.status); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(kFull, mbar_ready(bar, parity)) || wait_slow(bar, parity, ab, a.status);
+  };
 
   // Every role walks the same parts: f(stream, vs, first unit, end unit, units of the stream, cost before them).
   // A stream begins with `lead` units of cost and no work, so that a CTA that begins another stream gets less.

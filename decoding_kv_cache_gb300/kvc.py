@@ -220,7 +220,8 @@ def kvc_evict_launch_count(cache: Cache, n_r: int, n_b: int) -> int:
 
 
 def kvc_debug_fault(mode: int) -> None:
-    """Test-only fault switch (see include/kvc.h): 1 makes the scoring exchange wait run out."""
+    """Test-only fault switch (see include/kvc.h): 1 makes the scoring exchange wait run out, 2 a wait of
+    the paged attention."""
     _check(lib().kvc_debug_fault(int(mode)))
 
 

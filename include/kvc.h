@@ -576,6 +576,9 @@ KVC_API int kvc_abi_version(void);
  * (bf16 caches with 128-row observation tiles) withholds its exchange partials, so its group's
  * bounded waits give up after about 50 ms: those heads' scores are left unset,
  * KVC_STATUS_TIMEOUT is raised in the status word of kvc_evict, and the launch still returns.
+ * mode 2: from the next kvc_page_attend on, the first CTA of the attention kernel waits for an arrival
+ * that nothing makes and gives up after about a second: KVC_STATUS_TIMEOUT, the rows it had a share in
+ * are incomplete, the call returns.
  * mode 0 restores normal behaviour. Process-wide, not thread-safe against concurrent calls.
  * Returns KVC_OK or KVC_ERR_INVALID_ARG for any other mode. */
 KVC_API int kvc_debug_fault(int32_t mode);
