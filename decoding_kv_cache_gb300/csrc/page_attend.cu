@@ -589,11 +589,12 @@ __global__ void __launch_bounds__(kTcRows) combine_tc_kernel(AttendArgs a, Atten
   const int vs = blockIdx.x / kPer, c0 = blockIdx.x % kPer * C, rr = threadIdx.x;
   const int2 span = p.span[vs];
   const Stream x = stream_of(a, p, vs, rr == 0);
-  if (rr >= x.rows || (x.vis && span.x == span.y)) return;
+  const bool given_up = x.vis && span.x < 0;
+  if (rr >= x.rows || (x.vis && span.x == span.y && !given_up)) return;
   float o[C], l = 0.f, m = -INFINITY;
 #pragma unroll
   for (int e = 0; e < C; ++e) o[e] = 0.f;
-  if (x.vis) {
+  if (x.vis && !given_up) {
     constexpr int N = 4;  // parts whose reads are in flight at once
     for (int c1 = span.x; c1 <= span.y; c1 += N) {
       float2 ml[N];

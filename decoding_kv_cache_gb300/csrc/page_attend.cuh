@@ -22,7 +22,7 @@ struct AttendPlan {
   int whole;   // a CTA takes a whole stream: no parts, no second kernel
   float* part;  // [grid][2][rb][D] (tcgen05 kernel: [grid][2][D][rb])
   float2* ml;   // [grid][2][rb] (reference, sum)
-  int2* span;   // [nvs] first and last CTA of a stream's units (streams with units only)
+  int2* span;   // [nvs] first and last CTA of a stream's units (streams with units only; negative: that CTA gave up)
 };
 
 struct Stream {  // what a (stream, row block) has to see

@@ -144,13 +144,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
   __shared__ Bars bars;
   __shared__ uint32_t tmem_slot, raw_ok[kRaw], unit_ok[4];
   __shared__ int sm_scan[kThreads / 32], sm_first[2];
-  __shared__ int abort_flag;
+  __shared__ int abort_flag, parts_done;
   __shared__ float row_f[kTcRows];
   __shared__ float2 row_ml[2][kTcRows];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    abort_flag = 0;
+    abort_flag = parts_done = 0;
     for (int i = 0; i < kRaw; ++i) {
       tc::mbar_init(&bars.raw_full[i], 1);
       tc::mbar_init(&bars.raw_empty[i], kDecWarps);
@@ -160,7 +160,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
       tc::mbar_init(&bars.v_full[i], kDecWarps / 2);
       tc::mbar_init(&bars.k_empty[i], 1);
       tc::mbar_init(&bars.v_empty[i], 1);
-      tc::mbar_init(&bars.s_full[i], 1);
+      // test-only fault (kvc_debug_fault 2): the first CTA's second unit waits for an arrival that nothing makes
+      tc::mbar_init(&bars.s_full[i], a.fault && blockIdx.x == 0 && i == 1 ? 2 : 1);
       tc::mbar_init(&bars.pv_done[i], 1);
       tc::mbar_init(&bars.p_full[i][0], 4);
       tc::mbar_init(&bars.p_full[i][1], 4);
@@ -546,13 +547,25 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
       if (lane == 0) mbar_arrive(&bars.merge);
       if (!wait(&bars.merge, (seg & 1) ^ 1)) return false;
       seg += 2;
+      if (threadIdx.x == 0) parts_done = seg / 2;
       return true;
     });
   }
   if (*ab) __nanosleep(1000000);  // copies and products under way end before their memory goes
   __syncwarp();
   tc::fence_before_sync();
-  __syncthreads();
+  if (__syncthreads_or(*ab)) {
+    // a role gave up and the others followed: what this CTA leaves undone must not be taken for what lay in the
+    // workspace. Streams that begin here hold no part at all, those that began before nothing of this CTA's.
+    int i = 0;
+    parts([&](const Stream&, int vs, int ua, int, int, int) {
+      if (i++ < parts_done) return true;
+      if (ua == 0 && threadIdx.x == 0) p.span[vs] = make_int2(-1, -1);
+      if (threadIdx.x < kTcRows)
+        p.ml[((size_t)blockIdx.x * 2 + (ua == 0 ? 1 : 0)) * kTcRows + threadIdx.x] = make_float2(0.f, 0.f);
+      return true;
+    });
+  }
   if (warp == 17) tc::tmem_dealloc(tmem, kTmemCols);
 }
 

@@ -548,6 +548,7 @@ KVC_API int kvc_page_compact(const kvc_pool* pool, const kvc_pages* pages, const
  * probabilities are fp16, in two terms each when dtype is KVC_F32). A query that sees no token gets
  * out = 0 and lse = -inf; queries i >= n_q[b] are not written. Tokens of a bad page take no part, and a
  * stream of bad length counts as empty (KVC_STATUS_BAD_PAGE).
+ * After KVC_STATUS_TIMEOUT (a device-side wait gave up) rows may lack tokens or be empty.
  *
  *   dtype      kvc_dtype of q and out
  *   q          [B][T][Hq][D] rows (device, 16-byte aligned), strides as kvc_page_store's

@@ -61,3 +61,33 @@ def run_out(dt, D, B, Hkv, G, T, n, page):
 def test_a_copy_that_never_lands(dt, D, T, n):
     """Whole streams a CTA, and streams split over CTAs."""
     run_out(dt, D, 2, 3, 4, T, n, 64)
+
+
+@pytest.mark.parametrize("D,T", [(128, 32), (64, 20)])
+def test_many_rows_kernel_gives_up_in_a_long_stream(D, T):
+    """The stream's first CTA gives up: the rows that need it hold nothing, not what an earlier call left."""
+    out, lse = run_out(torch.bfloat16, D, 2, 3, 4, T, 32768, 64)
+    assert (out[0, :, :4] == 0).all() and torch.isneginf(lse[0, :, :4]).all()
+
+
+def test_many_rows_kernel_gives_up_between_short_streams():
+    """Streams of one unit: the first CTA has finished one and gives up on its second."""
+    B, Hkv, G, T = 40, 8, 4, 5
+    kvc, pool, pages, q = cache(torch.bfloat16, 128, B, Hkv, G, T, 128, 64)
+    ws = torch.empty(kvc.kvc_page_attend_workspace_size(pool, pages, Hkv * G, T), dtype=torch.uint8, device=DEV)
+    good, glse = torch.empty_like(q), torch.empty(q.shape[:3], device=DEV)
+    kvc.kvc_page_attend(pool, pages, q, good, lse=glse, workspace=ws)
+    out, lse = torch.full_like(q, 9.0), torch.full_like(glse, 9.0)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    torch.cuda.synchronize()
+    kvc.kvc_debug_fault(2)
+    try:
+        kvc.kvc_page_attend(pool, pages, q, out, lse=lse, status=status, workspace=ws)
+        torch.cuda.synchronize()
+    finally:
+        kvc.kvc_debug_fault(0)
+    assert int(status.item()) == kvc.KVC_STATUS_TIMEOUT
+    bad = slice(G, 2 * G)  # of sequence 0: its second KV head
+    assert (out[0, :, bad] == 0).all() and torch.isneginf(lse[0, :, bad]).all()
+    out[0, :, bad], lse[0, :, bad] = good[0, :, bad], glse[0, :, bad]
+    assert torch.equal(out, good) and torch.equal(lse, glse)
