@@ -45,7 +45,7 @@ struct Lay {
 
 struct Bars {
   uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[kTiles], k_empty[kTiles], v_full[kTiles], v_empty[kTiles];
-  uint64_t s_full[2], p_full[2][2], pv_done[2], q_full, merge;  // p_full: S buffer, group (a group may be a unit ahead)
+  uint64_t s_full[2], p_full[2][2], pv_done[2], q_full, merge, drain;  // p_full: S buffer, group (a group may be a unit ahead)
 };
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
@@ -145,6 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
   __shared__ uint32_t tmem_slot, raw_ok[kRaw], unit_ok[4];
   __shared__ int sm_scan[kThreads / 32], sm_first[2];
   __shared__ int abort_flag, parts_done;
+  __shared__ uint32_t raw_issued;  // units the producer has asked for
   __shared__ float row_f[kTcRows];
   __shared__ float2 row_ml[2][kTcRows];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -168,6 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
     }
     tc::mbar_init(&bars.q_full, kSoftWarps);
     tc::mbar_init(&bars.merge, kSoftWarps);
+    tc::mbar_init(&bars.drain, 1);
     tc::mbar_fence_init();
   }
   griddep_wait();
@@ -243,6 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
       }
       return true;
     });
+    if (lane == 0) raw_issued = n;
   } else if (warp == 17) {
     // ---- issuer --------------------------------------------------------------------------------
     // the whole warp walks the loop, so that addresses stay in uniform registers; one lane issues
@@ -551,7 +554,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
       return true;
     });
   }
-  if (*ab) __nanosleep(1000000);  // copies and products under way end before their memory goes
   __syncwarp();
   tc::fence_before_sync();
   if (__syncthreads_or(*ab)) {
@@ -565,6 +567,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
         p.ml[((size_t)blockIdx.x * 2 + (ua == 0 ? 1 : 0)) * kTcRows + threadIdx.x] = make_float2(0.f, 0.f);
       return true;
     });
+    // copies and products under way end before their memory goes
+    if (warp == 16)
+      for (uint32_t n = raw_issued > kRaw ? raw_issued - kRaw : 0; n < raw_issued; ++n)
+        (void)mbar_wait_far(&bars.raw_full[n % kRaw], (n / kRaw) & 1);
+    if (warp == 17) {
+      if (elect_one()) tc::umma_commit(&bars.drain);  // the lane that issued the products
+      __syncwarp();
+      (void)mbar_wait_far(&bars.drain, 0);
+    }
+    __syncthreads();
   }
   if (warp == 17) tc::tmem_dealloc(tmem, kTmemCols);
 }
