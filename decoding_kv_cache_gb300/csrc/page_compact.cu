@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(PoolGeom g, PageTab 
   int32_t* to = w.newtab + ((size_t)kv * t.S + s) * t.maxp;
   const int need = w.need[s], pe = pages_of(m, g.lp);
   if (need) {  // the marked pages' numbers: what the streams before left, this row in order
+    bool lost = false;
     if (threadIdx.x < 32) {
       int at = nfree - 1 - before;
       for (int i0 = first >> g.lp; i0 < pe; i0 += 32) {
@@ -170,12 +171,18 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(PoolGeom g, PageTab 
         const unsigned mask = __ballot_sync(kFull, want);
         if (want) {
           const int p = g.free_list[at - __popc(mask & ((1u << threadIdx.x) - 1))];
-          to[i] = page_ok(g, p) ? p : row[i];
+          if (page_ok(g, p))
+            to[i] = p;
+          else
+            lost = true;  // the mark stays: the stream is left alone, here and by the finishing kernel
         }
         at -= __popc(mask);
       }
     }
-    __syncthreads();
+    if (__syncthreads_or(lost)) {
+      if (threadIdx.x == 0) status_or(status, KVC_STATUS_BAD_PAGE);
+      return;
+    }
   }
   if (!(plan.w & kCompactMoves)) return;
 

@@ -558,7 +558,10 @@ __device__ __forceinline__ void compact_finish(const PoolGeom& g, const PageTab&
   int32_t* row = t.table + (size_t)s * t.maxp;
   const int32_t* to = w.newtab + (size_t)s * t.maxp;
   const int pe = pages_of(plan.y, g.lp);
-  if (w.need[s])
+  if (w.need[s]) {
+    bool lost = false;  // a mark that the free list held no page for
+    for (int i = (plan.x >> g.lp) + lane; i < pe; i += 32) lost |= to[i] < 0;
+    if (__any_sync(kFull, lost)) return;
     for (int i = (plan.x >> g.lp) + lane; i < pe; i += 32) {
       const int old = row[i], p = to[i];
       if (p != old) {
@@ -567,6 +570,7 @@ __device__ __forceinline__ void compact_finish(const PoolGeom& g, const PageTab&
         drop_page(g, w, old, nullptr);
       }
     }
+  }
   for (int i = pe + lane; i < pages_of(plan.z, g.lp); i += 32) {
     drop_page(g, w, row[i], nullptr);
     row[i] = -1;

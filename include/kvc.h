@@ -427,7 +427,8 @@ KVC_API int kvc_epikv_evict(const kvc_cache* c, const void* hA, const void* hB, 
  * are taken from its end, streams in (l, b, h) order, and join it in the order of their numbers, so
  * results never depend on timing. The arrays start from kvc_page_init and only these operators
  * change them; streams of one pool are changed by one call at a time (order the calls on a stream).
- * A page number out of range is reported (KVC_STATUS_BAD_PAGE), never followed.
+ * A page number out of range is reported (KVC_STATUS_BAD_PAGE), never followed; a stream that would get
+ * one from a damaged free list is left alone, the other pages meant for it are lost to the pool.
  */
 typedef struct {
   int32_t D;          /* head dimension, 64 or 128 */

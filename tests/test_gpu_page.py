@@ -275,6 +275,27 @@ def test_bad_pages_are_reported_not_followed():
         x.pool.free_list.copy_(up(x.p.free))
 
 
+@pytest.mark.parametrize("bad", [-1, 400, 1 << 30])
+@pytest.mark.parametrize("Hkv,at", [(1, 0), (1, 1), (40, 0), (40, 1)])  # one finishing launch, and two
+def test_compaction_with_a_damaged_free_list(Hkv, at, bad):
+    """A free list that holds no page's number where a shared page has to be replaced: that stream stays as it
+    was, shared pages are not written, the others take theirs."""
+    x = Both(400, 64, 16, 1, 2, Hkv, 4, seed=at)
+    x.extend([40, 0])
+    x.fork([0, 0])
+    x.check("fork")
+    top = x.p.nfree - 1
+    x.pool.free_list[top - at] = bad
+    lists = {s: list(range(1, 40, 2)) for s in x.t.streams()}
+    lists[(0, 0, 0)] = None  # two shared pages of each stream are replaced: the first stream's two are off the list
+    idx = up(np.tile(np.arange(1, 40, 2, dtype=np.int32), (1, 2, Hkv, 1)))
+    x.kvc.kvc_page_compact(x.pool, x.pages, idx, up(np.full((1, 2, Hkv), 20, np.int32)), status=x.status)
+    x.p.nfree -= 2
+    R.compact(x.p, x.t, lists)
+    x.p.status = R.BAD_PAGE
+    x.check("compaction")
+
+
 # ---- attention -----------------------------------------------------------------------------------
 def make_attend(dt, D, B, Hkv, G, T, page, lens, seed=0, k_scale=1.0, v_scale=1.0):
     lens = np.asarray(lens, np.int32).reshape(1, B, Hkv)
