@@ -159,7 +159,8 @@ __device__ __forceinline__ void copy_page(const PoolGeom& g, int dst, int src, i
 
 // A warp hands stream s its pages (`before` pages go to the streams before it) and copies its page.
 __device__ __forceinline__ void extend_stream(const PoolGeom& g, const PageTab& t, int s, int need, int before, bool none,
-                                              int nfree, const int32_t* add, int add_all, int32_t* start) {
+                                              int nfree, const int32_t* add, int add_all, int32_t* start,
+                                              int32_t* status) {
   const int lane = threadIdx.x & 31;
   if (none || need < 0) {
     if (lane == 0 && start) start[s] = -1;
@@ -170,19 +171,28 @@ __device__ __forceinline__ void extend_stream(const PoolGeom& g, const PageTab& 
   const int k = need & ~kCopyFlag, copy = need & kCopyFlag ? 1 : 0;
   const int at = nfree - 1 - before;  // free-list slot of the stream's first page
   int32_t* row = t.table + (size_t)s * t.maxp;
-  const int first = pages_of(n, g.lp);
-  for (int j = lane; j < k - copy; j += 32) {
-    const int p = g.free_list[at - copy - j];
-    row[first + j] = p;
-    if (page_ok(g, p)) g.refs[p] = 1;
+  const int mine = lane < k ? g.free_list[at - lane] : 0;  // its first 32 pages
+  bool lost = !page_ok(g, mine);
+  for (int j = lane + 32; j < k; j += 32) lost |= !page_ok(g, g.free_list[at - j]);
+  if (__any_sync(kFull, lost)) {  // no page's number in the free list
+    if (lane == 0) {
+      status_or(status, KVC_STATUS_BAD_PAGE);
+      if (start) start[s] = -1;
+    }
+    return;
+  }
+  const int first = pages_of(n, g.lp) - copy;
+  for (int j = lane; j < k; j += 32) {
+    const int p = j < 32 ? mine : g.free_list[at - j];
+    if (j >= copy) row[first + j] = p;
+    g.refs[p] = 1;
   }
   if (copy) {
-    const int old = row[n >> g.lp], p = g.free_list[at];
-    if (page_ok(g, p)) copy_page(g, p, old, lane);
+    const int old = row[n >> g.lp], p = __shfl_sync(kFull, mine, 0);
+    copy_page(g, p, old, lane);
     __syncwarp();
     if (lane == 0) {
       row[n >> g.lp] = p;
-      if (page_ok(g, p)) g.refs[p] = 1;
       atomicSub(&g.refs[old], 1);
     }
   }
@@ -213,7 +223,7 @@ __global__ void __launch_bounds__(kAssignThreads) extend_assign_kernel(PoolGeom 
   const int s = s0 + warp;
   if (s >= t.S) return;
   for (int i = s0; i < s; ++i) before += need_of(w, i);
-  extend_stream(g, t, s, w.need[s], before, none, nfree, add, add_all, start);
+  extend_stream(g, t, s, w.need[s], before, none, nfree, add, add_all, start, status);
 }
 
 // Counted down; a page whose last reference goes is marked.
@@ -539,7 +549,7 @@ __global__ void __cluster_dims__(kOneCtas, 1, 1) __launch_bounds__(kOneThreads)
       *g.nfree = nfree - total;
   }
   const int s = warp * kOneCtas + cl.block_rank();  // neighbours on different SMs
-  if (s < t.S) extend_stream(g, t, s, sm_need[s], sm_before[s], none, nfree, add, add_all, start);
+  if (s < t.S) extend_stream(g, t, s, sm_need[s], sm_before[s], none, nfree, add, add_all, start, status);
 }
 
 bool one_fits(const PoolGeom& g, const PageTab& t, const PageTab& o) {

@@ -469,7 +469,7 @@ KVC_API int kvc_page_init(const kvc_pool* pool, const kvc_pages* pages, void* st
  * first (when all its sharers grow in this call, the lowest sequence keeps it). The copied page comes
  * before the fresh ones. start[l,b,h] (device, out, may be NULL) receives the old length, -1 for a
  * stream that was left alone because of an error: add[b] < 0 (KVC_STATUS_BAD_INDEX), more than maxp
- * pages (KVC_STATUS_TABLE_FULL), a bad length or last page (KVC_STATUS_BAD_PAGE). With too few free
+ * pages (KVC_STATUS_TABLE_FULL), a bad length, last or free page (KVC_STATUS_BAD_PAGE). With too few free
  * pages for the whole call nothing changes and every start is -1 (KVC_STATUS_NO_PAGES).
  */
 KVC_API int kvc_page_extend(const kvc_pool* pool, const kvc_pages* pages, const int32_t* add, int32_t add_all,

@@ -296,6 +296,34 @@ def test_compaction_with_a_damaged_free_list(Hkv, at, bad):
     x.check("compaction")
 
 
+@pytest.mark.parametrize("bad", [-1, 13000, 1 << 30])
+@pytest.mark.parametrize("Hkv", [1, 140])  # the one-launch form, and the wide one
+@pytest.mark.parametrize("at,copies", [(0, False), (39, False), (0, True), (33, True)])
+def test_extension_with_a_damaged_free_list(Hkv, at, copies, bad):
+    """A number out of range where a stream would take its page (the copy of a shared one, a fresh one): it
+    stays as it was, the others take theirs."""
+    x = Both(13000, 64, 16, 1, 2, Hkv, 42, seed=at)
+    if copies:
+        x.extend([20, 0])
+        x.fork([0, 0])
+    add = [630, 0 if copies else 630]  # 40 pages a stream; the first sequence's last page is copied where it is shared
+    x.pool.free_list[x.p.nfree - 1 - at] = bad
+    start = torch.full(x.t.shape, -9, dtype=torch.int32, device=DEV)
+    x.kvc.kvc_page_extend(x.pool, x.pages, add=up(np.array(add, np.int32)), start=start, status=x.status)
+    # the model: the first stream's pages are off the list, its own state is as before
+    n0, row0, data0, s0 = int(x.t.len[0, 0, 0]), x.t.table[0, 0, 0].copy(), x.p.data.copy(), (0, 0, 0)
+    want = R.extend(x.p, x.t, add)
+    taken = np.setdiff1d(x.t.table[s0], row0)
+    assert x.p.status == 0 and len(taken) == 40
+    if copies:
+        x.p.refs[row0[1]] += 1
+    x.p.refs[taken], x.p.data[taken] = 0, data0[taken]
+    x.t.len[s0], x.t.table[s0], want[s0] = n0, row0, -1
+    x.p.status = R.BAD_PAGE
+    np.testing.assert_array_equal(start.cpu().numpy(), want)
+    x.check("extension")
+
+
 # ---- attention -----------------------------------------------------------------------------------
 def make_attend(dt, D, B, Hkv, G, T, page, lens, seed=0, k_scale=1.0, v_scale=1.0):
     lens = np.asarray(lens, np.int32).reshape(1, B, Hkv)
