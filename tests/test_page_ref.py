@@ -32,6 +32,47 @@ def test_quantise_is_nearest():
     assert (np.abs(v - x) <= step + 6 * 0.5 * 2.0 ** -10).all()
 
 
+def e2m1_of(y):
+    """The magnitude code of |y| (fp32 or exact), ties to the even code, saturating."""
+    a = np.abs(y)
+    return sum(((a > b) if k % 2 == 0 else (a >= b)).astype(np.int64)
+               for k, b in enumerate((0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0)))
+
+
+def test_rounded_reciprocals_decide_as_exact_quotients_do():
+    """The store's short way for bf16 rows and tensor scales that are powers of two (page_store.cu), in fp32 as the
+    kernel computes it, over every bf16 significand: every scale, with its reciprocal an ulp off either way, and every
+    code under every scale, likewise. A power of two as tensor scale shifts exponents only: 1 stands for all."""
+    f, one = np.float32, np.float32(1)
+    bits = lambda x: np.asarray(x, f).view(np.uint32)
+    ulps = lambda x: [np.asarray(bits(x).astype(np.int64) + d, np.int64).astype(np.uint32).view(f) for d in (-1, 0, 1)]
+    sig = np.arange(128, 256, dtype=np.float64)
+    # scales: quotients from a quarter of the smallest scale to four times the largest
+    amax = (sig[:, None] * np.exp2(np.arange(-18, 12))[None]).ravel()
+    want = R.quantise(np.repeat(amax[:, None], 64, 1), 1.0)[1][:, 0]
+    assert amax.min() / 6 < 2.0 ** -11 and amax.max() / 6 > 4 * 448 and want.min() == 1 and want.max() == 126
+    for inv6 in ulps(one / f(6)):
+        q = np.clip(amax.astype(f) * inv6, f(2.0 ** -9), f(448))
+        q = ((bits(q) + np.uint32(0x400)) & np.uint32(0xfffff800)).view(f).astype(np.float64)
+        pos = R.E4M3[:127]
+        hi = np.clip(np.searchsorted(pos, q), 1, 126)
+        dl, dh = q - pos[hi - 1], pos[hi] - q
+        np.testing.assert_array_equal(np.where((dl < dh) | ((dl == dh) & (hi % 2 == 1)), hi - 1, hi), want)
+    # codes
+    for sb in range(1, 127):
+        step = R.E4M3[sb]
+        e = np.arange(-5, 6) + np.floor(np.log2(step)) - 7
+        x = (sig[:, None] * np.exp2(e)[None]).ravel()
+        assert x.min() / step < 0.125 and x.max() / step > 16
+        borders = np.array((0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0)) * step  # exact: at most seven bits
+        want = sum(((x > b) if k % 2 == 0 else (x >= b)).astype(np.int64) for k, b in enumerate(borders))
+        for r in ulps(one / f(step)):
+            for sign in (1, -1):
+                # the product has at most 32 bits and its sum with 1536 at most 53: one rounding, as fma's
+                y = (sign * x * np.float64(r) + 1536).astype(f) - f(1536)
+                np.testing.assert_array_equal(e2m1_of(y), want, err_msg=str((sb, r, sign)))
+
+
 def test_reference_extend_copies_on_write():
     p = R.RefPool(8, 64, 16)
     t = R.RefPages(1, 2, 1, 4)
