@@ -164,6 +164,51 @@ def test_store_special_values_and_refusals():
     assert int(x.status.item()) == R.BAD_PAGE
 
 
+@pytest.mark.parametrize("scales", [(1.0, 1.0), (2.0 ** -9, 2.0 ** 9), (2.0 ** 66, 2.0 ** -66), (0.7, 3.0)])
+def test_store_every_bf16_value(scales):
+    """All 65536 patterns, NaNs of either sign, infinities, zeros, subnormals and the largest among them, in groups of
+    neighbours and in groups that mix magnitudes, with tensor scales of the short way and of the general one."""
+    D, page, T = 64, 256, 1024
+    x = Both(9, D, page, 1, 2, 1, 4, *scales)
+    start = x.extend([T, T])
+    every = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    near = every.view(1, T, 1, D)
+    far = every.view(D, T).T.reshape(1, T, 1, D)  # a row's patterns lie 1024 apart
+    # rows with one value of all binades around each NaN, infinity and zero
+    g = torch.Generator().manual_seed(8)
+    rows = (torch.randn((1, T, 1, D), generator=g) * torch.exp2(torch.randint(-20, 20, (1, T, 1, 1), generator=g))).bfloat16()
+    odd = torch.tensor([float("nan"), -float("nan"), float("inf"), -float("inf"), 0.0, -0.0, 2.0 ** -133, -2.0 ** -126]).bfloat16()
+    at = torch.randint(0, D, (T,), generator=g)
+    rows[0, torch.arange(T), 0, at] = odd[torch.arange(T) % 8]
+    k, v = torch.cat((near, rows)), torch.cat((far, rows.flip(3)))
+    x.store(k.to(DEV), v.to(DEV), start)
+    R.store(x.p, x.t, k.double().numpy(), v.double().numpy(), start.cpu().numpy())
+    x.check("every value")
+
+
+def test_store_rows_past_32_bits():
+    """2^31 rows of K and V in one call (all of them the same row in memory, most without a page): the last ones
+    land where they belong."""
+    from decoding_kv_cache_gb300 import kvc
+    D, page, T = 64, 256, 1 << 29
+    maxp = T // page
+    pool, pages = kvc.Pool.empty(8, D, page, device=DEV), kvc.Pages.empty(1, 1, 2, maxp, device=DEV)
+    pages.len.fill_(T)
+    pool.refs.fill_(1)
+    pages.table[0, 0, 0, 0], pages.table[0, 0, 0, -1] = 3, 1
+    pages.table[0, 0, 1, 5], pages.table[0, 0, 1, -1] = 6, 4
+    k, v = rand_rows((1, 1, 2, D), "bf16", 5).to(DEV), rand_rows((1, 1, 2, D), "bf16", 6).to(DEV)
+    start = torch.zeros((1, 1, 2), dtype=torch.int32, device=DEV)
+    kvc.kvc_page_store(pool, pages, k.expand(1, T, 2, D), v.expand(1, T, 2, D), start)
+    small = Both(2, D, page, 1, 1, 2, 1)
+    s2 = small.extend([page])
+    kvc.kvc_page_store(small.pool, small.pages, k.expand(1, page, 2, D), v.expand(1, page, 2, D), s2)
+    for h, ids in ((0, (3, 1)), (1, (6, 4))):
+        for p in ids:
+            assert torch.equal(pool.data[p], small.pool.data[int(small.pages.table[0, 0, h, 0])])
+    assert not pool.data[[0, 2, 5, 7]].any()
+
+
 # ---- the page operators --------------------------------------------------------------------------
 def random_lists(rng, t, shrink):
     lists = {}
@@ -219,6 +264,39 @@ def test_random_sequences_of_page_operators(seed, D, page, L, B, Hkv, maxp, npag
                                     (list(range(n)) + [n], n + 1), ([-1, 1, 2], 3)][int(rng.integers(0, 6))]
             x.compact(lists, maxp * page + 1)
         x.check(what)
+
+
+@pytest.mark.parametrize("npages,L,B,Hkv,maxp,keep", [
+    (20000, 2, 24, 8, 48, 700),    # several CTAs give pages back, each behind the marks of those before it
+    (300000, 2, 4, 4, 500, 200),   # one launch whose CTAs take their words in two rounds
+])
+def test_pages_of_large_pools_given_back(npages, L, B, Hkv, maxp, keep):
+    """Pages in use and given back lie all over the pool: counts, tables and the free list equal the model's."""
+    from decoding_kv_cache_gb300 import kvc
+    rng = np.random.default_rng(npages)
+    x = Both.__new__(Both)
+    x.kvc, x.p, x.t = kvc, R.RefPool(npages, 64, 16), R.RefPages(L, B, Hkv, maxp)
+    x.p.data[:] = np.frombuffer(rng.bytes(x.p.data.size), np.uint8).reshape(x.p.data.shape)
+    x.p.free = rng.permutation(npages).astype(np.int32)
+    x.pool, x.pages = kvc.Pool.empty(npages, 64, 16, device=DEV), kvc.Pages.empty(L, B, Hkv, maxp, device=DEV)
+    x.pool.data.copy_(up(x.p.data.reshape(npages, -1)))
+    x.pool.free_list.copy_(up(x.p.free))
+    x.status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    x.extend(rng.integers(1, 16 * maxp + 1, B).tolist())
+    x.free(rng.integers(0, 8 * maxp, B).tolist())
+    x.check("free")
+    x.fork(rng.integers(0, B, B).tolist())
+    x.check("fork")
+    x.extend([int(min(a, 16 * maxp - n)) for a, n in zip(rng.integers(0, 50, B), x.t.len.max((0, 2)))])
+    lists = {}
+    for s in x.t.streams():
+        n = int(x.t.len[s])
+        lists[s] = np.sort(rng.choice(n, int(rng.integers(0, min(n, keep) + 1)), replace=False))
+    x.compact(lists, keep)
+    x.check("compact")
+    x.free([1 << 30] * B)
+    assert x.p.nfree == npages
+    x.check("all given back")
 
 
 def test_lists_per_sequence_and_exhausted_pool():
