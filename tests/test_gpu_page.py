@@ -558,6 +558,21 @@ def test_attend_strided_ragged_scaled(dt, T):
     check_attend(x, q0, dt, run=run)
 
 
+@pytest.mark.parametrize("dt,D,G,T,page,lens", [
+    ("bf16", 128, 4, 4, 64, [700, 3, 0, 1, 2000, 64]),   # split streams
+    ("f32", 64, 3, 5, 16, [900, 4, 5, 0, 33, 16]),
+    ("bf16", 64, 2, 8, 32, [200, 7, 0, 8, 9, 100]),      # whole streams
+    ("bf16", 128, 4, 300, 64, [700, 299, 300, 1, 0, 301]),  # ten row blocks
+])
+def test_attend_fewer_queries_than_rows(dt, D, G, T, page, lens):
+    """n_q on each kernel: sequences with none, one, some and all of their queries, some of them before any token."""
+    x, q = make_attend(dt, D, 3, 2, G, T, page, lens, seed=T)
+    for n_q in ([0, 1, T], [T - 1, 2, 0], [T + 5, -1, T // 2]):
+        run = lambda out, lse: x.kvc.kvc_page_attend(x.pool, x.pages, q.to(DEV), out, lse=lse, status=x.status,
+                                                     n_q=up(np.array(n_q, np.int32)))
+        check_attend(x, q, dt, n_q=n_q, run=run)
+
+
 @pytest.mark.parametrize("dt,T", [("bf16", 2), ("bf16", 20), ("f32", 2)])
 def test_attend_extreme_logits(dt, T):
     """Large and negative scales, one dominant key, zero queries: the running maximum has to follow."""
@@ -750,6 +765,59 @@ def test_captured_and_replayed_with_new_lengths():
         tol, ltol = R.tolerances("bf16", n, 128, ref)
         assert (np.abs(out[1, 0, 4:].double().cpu().numpy() - ref["out"]) <= tol).all()
         assert (np.abs(lse[1, 0, 4:].double().cpu().numpy() - ref["lse"]) <= ltol).all()
+
+
+@pytest.mark.parametrize("L,B,Hkv,maxp,npages", [(1, 3, 2, 8, 120), (2, 24, 8, 48, 9000)])  # one launch each, and the wide forms
+def test_page_operators_captured_and_replayed(L, B, Hkv, maxp, npages):
+    """Room, eviction, fork and rollback captured once; each replay with new numbers equals the model's, eager calls
+    between the replays use the same workspace."""
+    from decoding_kv_cache_gb300 import kvc
+    rng = np.random.default_rng(B)
+    x = Both(npages, 64, 16, L, B, Hkv, maxp, seed=B)
+    S, other = x.t.shape, kvc.Pages.empty(L, B, Hkv, maxp, device=DEV)
+    ws = torch.empty(kvc.kvc_page_workspace_size(x.pool, x.pages), dtype=torch.uint8, device=DEV)
+    add, drop, parent = (torch.zeros(B, dtype=torch.int32, device=DEV) for _ in range(3))
+    kept, klen = torch.zeros(S + (64,), dtype=torch.int32, device=DEV), torch.zeros(S, dtype=torch.int32, device=DEV)
+    a, b = x.pages, other
+
+    def step():
+        kvc.kvc_page_extend(x.pool, a, add=add, status=x.status, workspace=ws)
+        kvc.kvc_page_compact(x.pool, a, kept, klen, status=x.status, workspace=ws)
+        kvc.kvc_page_fork(x.pool, a, parent, b, status=x.status, workspace=ws)
+        kvc.kvc_page_free(x.pool, b, drop=drop, status=x.status, workspace=ws)
+        kvc.kvc_page_fork(x.pool, b, parent, a, status=x.status, workspace=ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()  # nothing to do yet: no tokens, empty lists
+    torch.cuda.current_stream().wait_stream(side)
+    R.fork(x.p, x.t, [0] * B)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    x.check("captured")
+    for i in range(6):
+        ad, dr = rng.integers(0, 40, B), rng.integers(0, 30, B)
+        pa = rng.integers(0, B, B)
+        lists, idx, ln = {}, np.zeros(S + (64,), np.int32), np.zeros(S, np.int32)
+        for s in x.t.streams():
+            n = int(x.t.len[s]) + int(ad[s[1]])
+            m = int(rng.integers(min(n, 20), min(n, 50) + 1))
+            lists[s] = np.sort(rng.choice(n, m, replace=False))
+            idx[s][:m], ln[s] = lists[s], m
+        for t, v in ((add, ad), (drop, dr), (parent, pa), (kept, idx), (klen, ln)):
+            t.copy_(up(np.ascontiguousarray(v, np.int32)))
+        graph.replay()
+        R.extend(x.p, x.t, ad.tolist())
+        R.compact(x.p, x.t, lists)
+        x.t = R.fork(x.p, x.t, pa.tolist())
+        R.free(x.p, x.t, dr.tolist())
+        x.t = R.fork(x.p, x.t, pa.tolist())
+        x.check(f"replay {i}")
+        kvc.kvc_page_free(x.pool, a, drop_all=1, status=x.status, workspace=ws)
+        R.free(x.p, x.t, [1] * B)
+        x.check(f"between {i}")
 
 
 def test_streams_with_their_own_workspaces():
