@@ -353,6 +353,23 @@ def test_bad_pages_are_reported_not_followed():
         x.pool.free_list.copy_(up(x.p.free))
 
 
+@pytest.mark.parametrize("Hkv,maxp", [(1, 4), (40, 300)])  # one launch each, and the wide forms
+def test_what_free_and_fork_make_of_a_bad_page(Hkv, maxp):
+    x = Both(1000, 64, 16, 1, 2, Hkv, maxp)
+    x.extend([60, 20])
+    good = int(x.t.table[0, 0, 0, 2])
+    x.pages.table[0, 0, 0, 2] = 1000
+    x.fork([0, 0])  # sequence 1's pages go, sequence 0's are shared but for the bad one, which both children hold
+    assert int(x.status.item()) == R.BAD_PAGE
+    assert x.pages.table[0, :, 0, 2].tolist() == [1000, 1000] and int(x.pool.refs[good]) == 1
+    x.status.zero_()
+    x.kvc.kvc_page_free(x.pool, x.pages, drop=up(np.array([40, 0], np.int32)), status=x.status)
+    assert int(x.status.item()) == R.BAD_PAGE
+    assert x.pages.len[0, :, 0].tolist() == [20, 60] and x.pages.table[0, 0, 0, :5].tolist()[2:4] == [-1, -1]
+    assert (x.pages.table[0, 0, :, 2:4] == -1).all() and int(x.pages.table[0, 1, 0, 2]) == 1000
+    assert int(x.pool.nfree) == 1000 - 4 * Hkv  # the four pages of each of sequence 0's streams, the bad entry's lost one too
+
+
 @pytest.mark.parametrize("bad", [-1, 400, 1 << 30])
 @pytest.mark.parametrize("Hkv,at", [(1, 0), (1, 1), (40, 0), (40, 1)])  # one finishing launch, and two
 def test_compaction_with_a_damaged_free_list(Hkv, at, bad):
