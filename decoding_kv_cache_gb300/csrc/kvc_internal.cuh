@@ -39,13 +39,19 @@ __device__ __forceinline__ void status_or(int32_t* status, unsigned bits) {
 // A kernel launched with programmatic stream serialisation may start while the previous
 // kernel in the stream is still running; griddep_wait() returns once that kernel has
 // completed and its memory operations are visible (immediately when launched normally).
-// No kernel here signals early completion: dependents are released when their predecessor
-// exits (an early signal let waiting CTAs sit beside the scoring kernel and slowed it), so
-// the overlap is the launch's own latency and the waiting roles' prologue.
+// The eviction step's kernels (scoring, selection, compaction, EPIKV) signal nothing early:
+// dependents are released when their predecessor exits (an early signal let waiting CTAs sit
+// beside the scoring kernel and slowed it), so the overlap is the launch's own latency and the
+// waiting roles' prologue. The page operators and the attention's second kernels do signal,
+// with griddep_launch(). So a kernel launched this way may begin while its predecessor, and those
+// before it, still run, and touches what they read or write only behind griddep_wait(). The
+// scoring kernels that load keys before it follow the observation kernel, a plain launch, which
+// begins when everything before it is done and writes no keys.
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 
-// For kernels of a few CTAs (the page operators), whose successors' waiting CTAs cost nothing: lets
-// the next kernel of the stream come up and wait in griddep_wait().
+// Lets the next kernel of the stream come up and wait in griddep_wait() while this one's last CTAs run. In
+// kernels that are short or whose CTAs leave room beside them (the page operators, store and read, the merging
+// kernels); not in the attention kernels, whose wave the waiting CTAs disturb (8 x 32768 tokens: 69 and 74 us).
 __device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 
 // Launch with programmatic stream serialisation (and cooperatively if asked); when the

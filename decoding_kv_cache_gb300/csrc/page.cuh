@@ -71,13 +71,7 @@ __device__ __forceinline__ uint8_t* block_of(const PoolGeom& g, int page_id, int
 __device__ __forceinline__ bool page_ok(const PoolGeom& g, int id) { return (unsigned)id < (unsigned)g.npages; }
 __host__ __device__ __forceinline__ int pages_of(int n, int lp) { return (int)(((long long)n + (1 << lp) - 1) >> lp); }
 
-// two e2m1 codes (a byte) to fp16, the low nibble in the low half
-__device__ __forceinline__ uint32_t e2m1x2_f16x2(uint32_t byte) {
-  uint32_t r;
-  asm("{\n .reg .b8 b, x;\n .reg .b16 h;\n cvt.u16.u32 h, %1;\n mov.b16 {b, x}, h;\n cvt.rn.f16x2.e2m1x2 %0, b;\n}\n" : "=r"(r) : "r"(byte));
-  return r;
-}
-// the four bytes of a word (eight codes) to four fp16 pairs
+// the four bytes of a word (eight e2m1 codes) to four fp16 pairs, a byte's low nibble in the low half
 __device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t (&r)[4]) {
   asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n cvt.rn.f16x2.e2m1x2 %0, b0;\n"
       " cvt.rn.f16x2.e2m1x2 %1, b1;\n cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}\n"

@@ -158,8 +158,9 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
     for (int i = 0; i < kStages && i < mine && alive; ++i) issue(i, (n + i) % kStages);
 
     // the query rows as B fragments: k step i, k = 2t,2t+1 -> channels CPL t + 4 i + 0,1 and
-    // k = 2t+8,2t+9 -> + 2,3. Each row is brought to [256, 512) by a power of two, which makes bf16
-    // values exact in fp16 (fp32 ones split in two terms).
+    // k = 2t+8,2t+9 -> + 2,3. Each row is brought to [256, 512) by a power of two. bf16 values are then exact in
+    // fp16 from 2^-25 of the row's largest on, smaller ones off by at most 2^-33 of it (fp16's smallest step is
+    // 2^-24); fp32 values are split in two terms, 22 bits of 24.
     uint32_t qf[NT][PARTS][KS][2];
     float f[NT][2];  // rows 2t, 2t+1: scale * log2 e over that power
     int lim[NT][2];
@@ -346,7 +347,9 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
             }
           }
       }
-      // P^T fragments
+      // P^T fragments. A probability is rounded to fp16, once, for bf16 outputs: 2^-11 relative at most, token by
+      // token, against the output's own 2^-8; two terms would double the products. For fp32 outputs a second term
+      // holds what the first cut off. The sum adds the unrounded ones.
       uint32_t pf[2][NT][PARTS][2];
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk)

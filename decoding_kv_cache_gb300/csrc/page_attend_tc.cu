@@ -3,8 +3,9 @@
 //
 // A CTA takes 128 query rows of a KV head and a run of its 128-token units. Per unit: 4 * 128 * 128 * D
 // operations, S = Q K^T and O += P V, both kind::f16 with M = 128 rows on the tensor-memory lanes.
-// The cache's codes become fp16 exactly (page.cuh), so decoding costs no precision; queries are brought
-// to fp16 by a power of two per row (bf16 values exact).
+// The cache's codes become fp16 exactly (page.cuh), so decoding costs no precision; queries are brought to
+// fp16 by a power of two per row (bf16 values exact from 2^-25 of the row's largest on, below that off by at
+// most 2^-33 of it); a probability is rounded to fp16 once, 2^-11 relative against the bf16 output's 2^-8.
 //
 //   producer  (warp 16)     a unit's blocks by bulk copies into a three-stage ring of raw bytes
 //   decoders  (warps 8-15)  four warps K, four V: a thread a token, codes and scales to fp16 rows in the
@@ -336,8 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
     parts([&](const Stream& x, int vs, int ua, int ub, int U, int base) {
       const int m = ub - ua;
       {
-        // the query rows, each brought to [256, 512) by a power of two (bf16 values exact in fp16), with the
-        // scale's sign, so that maxima of dot products are maxima of logits. A warp takes 16 rows, D/8 lanes
+        // the query rows, each brought to [256, 512) by a power of two, with the scale's sign, so that maxima of dot products are maxima of logits. A warp takes 16 rows, D/8 lanes
         // a row, all of its reads in flight at once.
         constexpr int kLanes = D / 8, kAt = 32 / kLanes, kBatch = 16 / kAt;  // lanes of a row, rows at a time, reads in flight
         const int i = lane % kLanes;

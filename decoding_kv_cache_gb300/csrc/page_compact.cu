@@ -129,7 +129,8 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(PoolGeom g, PageTab 
   const int s = blockIdx.x >> 1, kv = blockIdx.x & 1;
   const int4 plan = w.plan[s];
   const int nfree = w.head[0];
-  // pages the streams before this one take, and all: nearly always none, in one batch of reads
+  // pages the streams before this one take, and all (nearly always none): every CTA sums all streams' needs, two
+  // or three reads a thread for some hundred streams; the sums of all CTAs grow with the square of the streams
   int before = 0, total = 0;
   for (int i = threadIdx.x; i < t.S; i += kMoveThreads) {
     const int v = w.need[i];

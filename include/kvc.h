@@ -511,7 +511,8 @@ KVC_API int kvc_page_read(const kvc_pool* pool, const kvc_pages* pages, int32_t 
  * Sequences of `pages` that no child names give up their pages; `pages` itself is not valid
  * afterwards (out takes its place). out->B may differ; L, Hkv and maxp are the same, and out's arrays
  * do not overlap those of pages. parent[c] = -1 makes an empty sequence, another value out of [0, B)
- * too (KVC_STATUS_BAD_INDEX).
+ * too (KVC_STATUS_BAD_INDEX). A bad page number goes to the children like any other entry, reported
+ * (KVC_STATUS_BAD_PAGE) where its count would change; a stream of bad length makes empty ones.
  */
 KVC_API int kvc_page_fork(const kvc_pool* pool, const kvc_pages* pages, const int32_t* parent, const kvc_pages* out,
                           int32_t* status, void* workspace, size_t ws_bytes, void* stream);
@@ -519,7 +520,9 @@ KVC_API int kvc_page_fork(const kvc_pool* pool, const kvc_pages* pages, const in
 /*
  * kvc_page_free -- the last drop[b] tokens of every stream of sequence b go (drop_all when drop is NULL;
  * all its tokens where it has fewer): a finished sequence, or drafts that were not accepted. Pages
- * left without a token are given up. drop[b] < 0 leaves the sequence alone (KVC_STATUS_BAD_INDEX).
+ * left without a token are given up. drop[b] < 0 leaves the sequence alone (KVC_STATUS_BAD_INDEX), a bad
+ * length its stream; a bad page number among those given up is reported (KVC_STATUS_BAD_PAGE) and its entry
+ * cleared like the others'.
  */
 KVC_API int kvc_page_free(const kvc_pool* pool, const kvc_pages* pages, const int32_t* drop, int32_t drop_all,
                           int32_t* status, void* workspace, size_t ws_bytes, void* stream);
@@ -554,7 +557,7 @@ KVC_API int kvc_page_compact(const kvc_pool* pool, const kvc_pages* pages, const
  *   dtype      kvc_dtype of q and out
  *   q          [B][T][Hq][D] rows (device, 16-byte aligned), strides as kvc_page_store's
  *   scale      finite, and so its product with k_scale; 1/sqrt(D) is usual
- *   out, lse   [B,T,Hq,D] and [B,T,Hq] fp32 (device); lse may be NULL
+ *   out, lse   [B,T,Hq,D] and [B,T,Hq] fp32 (device), overlapping none of the inputs; lse may be NULL
  *   workspace  at least kvc_page_attend_workspace_size() bytes, 256-byte aligned
  */
 KVC_API size_t kvc_page_attend_workspace_size(const kvc_pool* pool, const kvc_pages* pages, int32_t Hq, int32_t T);
