@@ -118,8 +118,10 @@ __device__ __forceinline__ uint4 load_row(const uint4* p) {
   return r;
 }
 
+// Five CTAs an SM, as the registers allow anyway: told so, the compiler orders the sweep's reads better (28 x 8 x 4
+// heads that keep a quarter: 104.4 us a cycle without, 102.0 with).
 template <int D>
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(PoolGeom g, PageTab t, const int32_t* kept_idx, int stride,
+__global__ void __launch_bounds__(kMoveThreads, 5) move_kernel(PoolGeom g, PageTab t, const int32_t* kept_idx, int stride,
                                                            int per_seq, int32_t* status, PageWs w) {
   __shared__ int sm[2 * kMoveThreads / 32];
   griddep_launch();

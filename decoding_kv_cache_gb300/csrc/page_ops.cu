@@ -171,9 +171,14 @@ __device__ __forceinline__ void extend_stream(const PoolGeom& g, const PageTab& 
   const int k = need & ~kCopyFlag, copy = need & kCopyFlag ? 1 : 0;
   const int at = nfree - 1 - before;  // free-list slot of the stream's first page
   int32_t* row = t.table + (size_t)s * t.maxp;
-  const int mine = lane < k ? g.free_list[at - lane] : 0;  // its first 32 pages
-  bool lost = !page_ok(g, mine);
-  for (int j = lane + 32; j < k; j += 32) lost |= !page_ok(g, g.free_list[at - j]);
+  constexpr int kHeld = 4;
+  int mine[kHeld];  // its first 128 pages, in one round of reads
+  bool lost = false;
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u) mine[u] = lane + 32 * u < k ? g.free_list[at - lane - 32 * u] : 0;
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u) lost |= !page_ok(g, mine[u]);
+  for (int j = lane + 32 * kHeld; j < k; j += 32) lost |= !page_ok(g, g.free_list[at - j]);
   if (__any_sync(kFull, lost)) {  // no page's number in the free list
     if (lane == 0) {
       status_or(status, KVC_STATUS_BAD_PAGE);
@@ -182,13 +187,16 @@ __device__ __forceinline__ void extend_stream(const PoolGeom& g, const PageTab& 
     return;
   }
   const int first = pages_of(n, g.lp) - copy;
-  for (int j = lane; j < k; j += 32) {
-    const int p = j < 32 ? mine : g.free_list[at - j];
+  auto take = [&](int j, int p) {
     if (j >= copy) row[first + j] = p;
     g.refs[p] = 1;
-  }
+  };
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u)
+    if (lane + 32 * u < k) take(lane + 32 * u, mine[u]);
+  for (int j = lane + 32 * kHeld; j < k; j += 32) take(j, g.free_list[at - j]);
   if (copy) {
-    const int old = row[n >> g.lp], p = __shfl_sync(kFull, mine, 0);
+    const int old = row[n >> g.lp], p = __shfl_sync(kFull, mine[0], 0);
     copy_page(g, p, old, lane);
     __syncwarp();
     if (lane == 0) {

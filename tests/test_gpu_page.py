@@ -419,6 +419,21 @@ def test_extension_with_a_damaged_free_list(Hkv, at, copies, bad):
     x.check("extension")
 
 
+@pytest.mark.parametrize("at,lost", [(31, 0), (32, 0), (128, 0), (299, 0), (300, 1), (430, 1)])
+def test_long_extension_with_a_damaged_free_list(at, lost):
+    """300 pages a stream: which of its reads of the free list meets the bad number makes no difference."""
+    x = Both(700, 64, 16, 1, 2, 1, 300)
+    x.pool.free_list[x.p.nfree - 1 - at] = 700
+    start = torch.full(x.t.shape, -9, dtype=torch.int32, device=DEV)
+    x.kvc.kvc_page_extend(x.pool, x.pages, add_all=4800, start=start, status=x.status)
+    want = R.extend(x.p, x.t, [4800, 4800])
+    x.p.refs[x.t.table[0, lost, 0]] = 0
+    x.t.len[0, lost, 0], x.t.table[0, lost, 0], want[0, lost, 0] = 0, -1, -1
+    x.p.status = R.BAD_PAGE
+    np.testing.assert_array_equal(start.cpu().numpy(), want)
+    x.check("extension")
+
+
 # ---- attention -----------------------------------------------------------------------------------
 def make_attend(dt, D, B, Hkv, G, T, page, lens, seed=0, k_scale=1.0, v_scale=1.0):
     lens = np.asarray(lens, np.int32).reshape(1, B, Hkv)
