@@ -103,6 +103,14 @@ int launch_page_fork(const PoolGeom& g, const PageTab& t, const int32_t* parent,
                      const PageWs& w, cudaStream_t s);
 int launch_page_compact(const PoolGeom& g, const PageTab& t, const int32_t* kept_idx, const int32_t* kept_len,
                         int stride, int per_seq, int32_t* status, const PageWs& w, cudaStream_t s);
+int launch_page_slide(const PoolGeom& g, const PageTab& t, int window, int sinks, int32_t* gone, int32_t* status,
+                      const PageWs& w, cudaStream_t s);
+int launch_page_accept(const PoolGeom& g, const PageTab& t, int T, const int32_t* path, const int32_t* n_path,
+                       const int32_t* n_q, int32_t* status, const PageWs& w, cudaStream_t s);
+int launch_tree_mask(int B, int T, const int32_t* parent, const int32_t* n_q, int window, uint32_t* mask, int32_t* depth,
+                     int32_t* status, cudaStream_t s);
+int launch_tree_verify(int B, int T, const int32_t* parent, const int32_t* draft, const int32_t* target,
+                       const int32_t* n_q, int32_t* path, int32_t* n_path, int32_t* next, int32_t* status, cudaStream_t s);
 
 struct RowStrides {  // in elements
   long long b, t, h;
@@ -146,8 +154,18 @@ struct AttendArgs {
   void* ws;
   int fault;  // kvc_debug_fault 2 (0 in normal use)
 };
+// What a query of kvc_page_attend_masked sees; all but sinks, window <= kSeenAll (longer than any stream).
+constexpr int kSeenAll = 1 << 30;
+struct SeenArgs {
+  int window, sinks;     // kSeenAll: no window
+  const uint32_t* mask;  // [B][T][words] or null
+  const int32_t* depth;  // [B][T] or null
+  int words;
+};
 bool attend_fits(const AttendArgs& a);
 size_t attend_ws_bytes(const PoolGeom& g, const PageTab& t, int Hq, int T);
 int launch_page_attend(const AttendArgs& a, int dtype, cudaStream_t s);
+size_t attend_masked_ws_bytes(const PoolGeom& g, const PageTab& t, int Hq, int T, const SeenArgs& m);
+int launch_page_attend_masked(const AttendArgs& a, const SeenArgs& m, int dtype, cudaStream_t s);
 
 }  // namespace kvc

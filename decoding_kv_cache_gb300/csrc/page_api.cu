@@ -96,6 +96,47 @@ int check_rows(const void* x, const int64_t* st, int es, RowStrides* out) {
 
 int elem_size(int dtype) { return dtype == KVC_BF16 ? 2 : dtype == KVC_F32 ? 4 : 0; }
 
+// kvc_page_attend's and kvc_page_attend_masked's checks but for the workspace
+int check_attend(const kvc_pool* pool, const kvc_pages* pages, int32_t dtype, int32_t Hq, int32_t T, const void* q,
+                 const int64_t* q_strides, const int32_t* n_q, float scale, void* out, float* lse, int32_t* status,
+                 AttendArgs* a) {
+  int rc = check_pool(pool, &a->g);
+  if (rc || (rc = check_pages(pages, a->g.lp, &a->t))) return rc;
+  const int es = elem_size(dtype);
+  if (!es) return KVC_ERR_UNSUPPORTED_DTYPE;
+  if (a->t.L != 1 || Hq < 1 || T < 1 || !out || !isfinite(scale * a->g.ts[0])) return KVC_ERR_INVALID_ARG;
+  if (Hq % a->t.Hkv) return KVC_ERR_NOT_DIVISIBLE;
+  if ((long long)a->t.B * Hq > (1LL << 30) || (long long)a->t.B * Hq * T > (1LL << 30)) return KVC_ERR_TOO_LARGE;
+  a->Hq = Hq;
+  a->T = T;
+  if (!attend_fits(*a)) return KVC_ERR_TOO_LARGE;
+  if ((rc = check_rows(q, q_strides, es, &a->qs))) return rc;
+  if (!at16(out) || !at4(lse)) return KVC_ERR_ALIGNMENT;
+  a->q = q;
+  a->out = out;
+  a->lse = lse;
+  a->n_q = n_q;
+  a->scale = scale * a->g.ts[0];
+  a->status = status;
+  a->fault = debug_fault_mode() == 2;
+  return KVC_OK;
+}
+bool ws_fits(const void* ws, size_t bytes, size_t need) {
+  return ws && bytes >= need && (reinterpret_cast<uintptr_t>(ws) & 255u) == 0;
+}
+
+SeenArgs seen_args(int32_t window, int32_t sinks, const uint32_t* mask, const int32_t* depth, int32_t T) {
+  // no stream is longer than kSeenAll: beyond it both mean everything
+  return SeenArgs{window > 0 && window < kSeenAll ? window : kSeenAll, sinks < kSeenAll ? sinks : kSeenAll, mask, depth,
+                  (T + 31) / 32};
+}
+
+int check_tree(int32_t B, int32_t T, const int32_t* parent) {
+  if (B < 1 || T < 1 || !parent) return KVC_ERR_INVALID_ARG;
+  if (T > KVC_TREE_MAX || B > (1 << 20)) return KVC_ERR_TOO_LARGE;
+  return at4(parent) ? KVC_OK : KVC_ERR_ALIGNMENT;
+}
+
 }  // namespace
 }  // namespace kvc
 
@@ -232,30 +273,84 @@ int kvc_page_attend(const kvc_pool* pool, const kvc_pages* pages, int32_t dtype,
                     const int64_t* q_strides, const int32_t* n_q, float scale, void* out, float* lse, int32_t* status,
                     void* workspace, size_t ws_bytes, void* stream) {
   AttendArgs a = {};
-  int rc = check_pool(pool, &a.g);
-  if (rc || (rc = check_pages(pages, a.g.lp, &a.t))) return rc;
-  const int es = elem_size(dtype);
-  if (!es) return KVC_ERR_UNSUPPORTED_DTYPE;
-  if (a.t.L != 1 || Hq < 1 || T < 1 || !out || !isfinite(scale * a.g.ts[0])) return KVC_ERR_INVALID_ARG;
-  if (Hq % a.t.Hkv) return KVC_ERR_NOT_DIVISIBLE;
-  if ((long long)a.t.B * Hq > (1LL << 30) || (long long)a.t.B * Hq * T > (1LL << 30)) return KVC_ERR_TOO_LARGE;
-  a.Hq = Hq;
-  a.T = T;
-  if (!attend_fits(a)) return KVC_ERR_TOO_LARGE;
-  if ((rc = check_rows(q, q_strides, es, &a.qs))) return rc;
-  if (!at16(out) || !at4(lse)) return KVC_ERR_ALIGNMENT;
-  if (!workspace || ws_bytes < attend_ws_bytes(a.g, a.t, Hq, T) ||
-      (reinterpret_cast<uintptr_t>(workspace) & 255u))
-    return KVC_ERR_WORKSPACE;
-  a.q = q;
-  a.out = out;
-  a.lse = lse;
-  a.n_q = n_q;
-  a.scale = scale * a.g.ts[0];
-  a.status = status;
+  const int rc = check_attend(pool, pages, dtype, Hq, T, q, q_strides, n_q, scale, out, lse, status, &a);
+  if (rc) return rc;
+  if (!ws_fits(workspace, ws_bytes, attend_ws_bytes(a.g, a.t, Hq, T))) return KVC_ERR_WORKSPACE;
   a.ws = workspace;
-  a.fault = debug_fault_mode() == 2;
   return launch_page_attend(a, dtype, static_cast<cudaStream_t>(stream));
+}
+
+size_t kvc_page_attend_masked_workspace_size(const kvc_pool* pool, const kvc_pages* pages, int32_t Hq, int32_t T,
+                                             int32_t window, int32_t sinks) {
+  PoolGeom g;
+  PageTab t;
+  if (check_pool(pool, &g) || check_pages(pages, g.lp, &t) || Hq < 1 || Hq % t.Hkv || T < 1 || window < 0 || sinks < 0 ||
+      (long long)t.B * Hq * T > (1LL << 30))
+    return 0;
+  return attend_masked_ws_bytes(g, t, Hq, T, seen_args(window, sinks, nullptr, nullptr, T));
+}
+
+int kvc_page_attend_masked(const kvc_pool* pool, const kvc_pages* pages, int32_t dtype, int32_t Hq, int32_t T,
+                           const void* q, const int64_t* q_strides, const int32_t* n_q, int32_t window, int32_t sinks,
+                           const uint32_t* mask, const int32_t* depth, float scale, void* out, float* lse,
+                           int32_t* status, void* workspace, size_t ws_bytes, void* stream) {
+  AttendArgs a = {};
+  const int rc = check_attend(pool, pages, dtype, Hq, T, q, q_strides, n_q, scale, out, lse, status, &a);
+  if (rc) return rc;
+  if (window < 0 || sinks < 0 || (depth && !mask)) return KVC_ERR_INVALID_ARG;
+  if (mask && T > KVC_TREE_MAX) return KVC_ERR_TOO_LARGE;
+  if (!at4(mask) || !at4(depth)) return KVC_ERR_ALIGNMENT;
+  const SeenArgs m = seen_args(window, sinks, mask, depth, T);
+  if (!ws_fits(workspace, ws_bytes, attend_masked_ws_bytes(a.g, a.t, Hq, T, m))) return KVC_ERR_WORKSPACE;
+  a.ws = workspace;
+  return launch_page_attend_masked(a, m, dtype, static_cast<cudaStream_t>(stream));
+}
+
+int kvc_page_slide(const kvc_pool* pool, const kvc_pages* pages, int32_t window, int32_t sinks, int32_t* gone,
+                   int32_t* status, void* workspace, size_t ws_bytes, void* stream) {
+  PoolGeom g;
+  PageTab t;
+  PageWs w;
+  int rc = check_pool(pool, &g);
+  if (rc || (rc = check_pages(pages, g.lp, &t))) return rc;
+  if (window < 1 || sinks < 0) return KVC_ERR_INVALID_ARG;
+  if (!at4(gone)) return KVC_ERR_ALIGNMENT;
+  if ((rc = check_ws(g, t, workspace, ws_bytes, &w))) return rc;
+  return launch_page_slide(g, t, window, sinks < kSeenAll ? sinks : kSeenAll, gone, status, w,
+                           static_cast<cudaStream_t>(stream));
+}
+
+int kvc_page_accept(const kvc_pool* pool, const kvc_pages* pages, int32_t T, const int32_t* path, const int32_t* n_path,
+                    const int32_t* n_q, int32_t* status, void* workspace, size_t ws_bytes, void* stream) {
+  PoolGeom g;
+  PageTab t;
+  PageWs w;
+  int rc = check_pool(pool, &g);
+  if (rc || (rc = check_pages(pages, g.lp, &t))) return rc;
+  if (T < 1 || !path || !n_path) return KVC_ERR_INVALID_ARG;
+  if (T > KVC_TREE_MAX) return KVC_ERR_TOO_LARGE;
+  if (!at4(path) || !at4(n_path) || !at4(n_q)) return KVC_ERR_ALIGNMENT;
+  if ((rc = check_ws(g, t, workspace, ws_bytes, &w))) return rc;
+  return launch_page_accept(g, t, T, path, n_path, n_q, status, w, static_cast<cudaStream_t>(stream));
+}
+
+int kvc_tree_mask(int32_t B, int32_t T, const int32_t* parent, const int32_t* n_q, int32_t window, uint32_t* mask,
+                  int32_t* depth, int32_t* status, void* stream) {
+  const int rc = check_tree(B, T, parent);
+  if (rc) return rc;
+  if (window < 0 || !mask) return KVC_ERR_INVALID_ARG;
+  if (!at4(n_q) || !at4(mask) || !at4(depth)) return KVC_ERR_ALIGNMENT;
+  return launch_tree_mask(B, T, parent, n_q, window, mask, depth, status, static_cast<cudaStream_t>(stream));
+}
+
+int kvc_tree_verify(int32_t B, int32_t T, const int32_t* parent, const int32_t* draft, const int32_t* target,
+                    const int32_t* n_q, int32_t* path, int32_t* n_path, int32_t* next, int32_t* status, void* stream) {
+  const int rc = check_tree(B, T, parent);
+  if (rc) return rc;
+  if (!draft || !target || !path || !n_path) return KVC_ERR_INVALID_ARG;
+  if (!at4(draft) || !at4(target) || !at4(n_q) || !at4(path) || !at4(n_path) || !at4(next)) return KVC_ERR_ALIGNMENT;
+  return launch_tree_verify(B, T, parent, draft, target, n_q, path, n_path, next, status,
+                            static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

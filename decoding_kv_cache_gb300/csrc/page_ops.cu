@@ -273,6 +273,53 @@ __global__ void __launch_bounds__(256) free_kernel(PoolGeom g, PageTab t, const 
   if (lane == 0) t.len[s] = left;
 }
 
+// The entries that a slide takes out of a stream of n tokens: [first, last).
+struct SlideSpan {
+  int first, last;
+};
+__device__ __forceinline__ SlideSpan slide_span(const PoolGeom& g, int n, int window, int sinks) {
+  const int first = pages_of(sinks, g.lp);
+  return SlideSpan{first, max(first, n < window ? 0 : (n - window + 1) >> g.lp)};
+}
+
+// A warp slides stream s: the pages of [first, last) are counted down, the entries behind them move up 32 at a time (a
+// chunk's places lie before every later chunk's).
+__device__ __forceinline__ void slide_stream(const PoolGeom& g, const PageTab& t, const PageWs& w, int s, int window,
+                                             int sinks, int32_t* gone, int32_t* status) {
+  const int lane = threadIdx.x & 31, n = t.len[s];
+  if (n < 0 || n > ((long long)t.maxp << g.lp)) {
+    if (lane == 0) {
+      status_or(status, KVC_STATUS_BAD_PAGE);
+      if (gone) gone[s] = -1;
+    }
+    return;
+  }
+  const SlideSpan x = slide_span(g, n, window, sinks);
+  const int m = x.last - x.first, e = pages_of(n, g.lp);
+  if (lane == 0 && gone) gone[s] = m << g.lp;
+  if (m == 0) return;
+  int32_t* row = t.table + (size_t)s * t.maxp;
+  for (int i = x.first + lane; i < x.last; i += 32) drop_page(g, w, row[i], status);
+  __syncwarp();
+  for (int i0 = x.first; i0 < e; i0 += 32) {
+    const int i = i0 + lane;
+    const int p = i + m < e ? row[i + m] : -1;
+    __syncwarp();
+    if (i < e) row[i] = p;
+    __syncwarp();
+  }
+  if (lane == 0) t.len[s] = n - (m << g.lp);
+}
+
+__global__ void __launch_bounds__(256) slide_kernel(PoolGeom g, PageTab t, int window, int sinks, int32_t* gone,
+                                                   int32_t* status, PageWs w) {
+  griddep_launch();
+  griddep_wait();
+  const int s = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  if (s == 0 && threadIdx.x == 0) w.head[0] = *g.nfree;
+  if (s < t.S) slide_stream(g, t, w, s, window, sinks, gone, status);
+}
+
 // Warps of the first t.S streams count their pages' new references (children - 1 each: old references
 // plus every partial sum stay above zero unless all of a page's holders go, so the one that reaches
 // zero is the last whatever the order); the others write the children's rows.
@@ -671,6 +718,15 @@ int launch_page_free(const PoolGeom& g, const PageTab& t, const int32_t* drop, i
                : KVC_ERR_LAUNCH;
   if (cudaMemsetAsync(w.head, 0, w.zero_bytes, s) != cudaSuccess) return KVC_ERR_LAUNCH;
   if (launch_pdl(free_kernel, dim3((t.S + 7) / 8), dim3(256), 0, s, false, g, t, drop, drop_all, status, w) !=
+      cudaSuccess)
+    return KVC_ERR_LAUNCH;
+  return page_push(g, w, s);
+}
+
+int launch_page_slide(const PoolGeom& g, const PageTab& t, int window, int sinks, int32_t* gone, int32_t* status,
+                      const PageWs& w, cudaStream_t s) {
+  if (cudaMemsetAsync(w.head, 0, w.zero_bytes, s) != cudaSuccess) return KVC_ERR_LAUNCH;
+  if (launch_pdl(slide_kernel, dim3((t.S + 7) / 8), dim3(256), 0, s, false, g, t, window, sinks, gone, status, w) !=
       cudaSuccess)
     return KVC_ERR_LAUNCH;
   return page_push(g, w, s);

@@ -20,13 +20,15 @@ KVC_BF16, KVC_F32 = 0, 1
 KVC_STATUS_BUDGET_RANGE, KVC_STATUS_COUNT_RANGE, KVC_STATUS_BAD_INDEX, KVC_STATUS_TIMEOUT = 0x1, 0x2, 0x4, 0x8
 KVC_STATUS_NO_PAGES, KVC_STATUS_BAD_PAGE, KVC_STATUS_TABLE_FULL = 0x10, 0x20, 0x40
 KVC_MAX_LAYERS = 128
+KVC_TREE_MAX = 1024
 
 EXPORTED = ("kvc_fps_update", "kvc_score_workspace_size", "kvc_score", "kvc_select", "kvc_compact",
             "kvc_evict_workspace_size", "kvc_evict", "kvc_evict_launch_count", "kvc_strerror", "kvc_abi_version",
             "kvc_score_static", "kvc_debug_fault", "kvc_head_budget", "kvc_append", "kvc_epikv_workspace_size",
             "kvc_epikv_score", "kvc_epikv_evict", "kvc_page_bytes", "kvc_page_workspace_size", "kvc_page_init",
             "kvc_page_extend", "kvc_page_store", "kvc_page_read", "kvc_page_fork", "kvc_page_free",
-            "kvc_page_compact", "kvc_page_attend_workspace_size", "kvc_page_attend")
+            "kvc_page_compact", "kvc_page_attend_workspace_size", "kvc_page_attend", "kvc_tree_mask", "kvc_tree_verify",
+            "kvc_page_attend_masked_workspace_size", "kvc_page_attend_masked", "kvc_page_slide", "kvc_page_accept")
 KVC_ABI_VERSION = 5
 KVC_AGG_MAX, KVC_AGG_MEAN, KVC_AGG_SUM = 0, 1, 2
 KVC_BUDGET_GIVEN, KVC_BUDGET_ENTROPY = 0, 1
@@ -109,6 +111,13 @@ def lib():
         "kvc_page_compact": (C.c_int, [pl, pg, vp, vp, i32, i32, vp, vp, sz, vp]),
         "kvc_page_attend_workspace_size": (sz, [pl, pg, i32, i32]),
         "kvc_page_attend": (C.c_int, [pl, pg, i32, i32, i32, vp, ps, vp, C.c_float, vp, vp, vp, vp, sz, vp]),
+        "kvc_tree_mask": (C.c_int, [i32, i32, vp, vp, i32, vp, vp, vp, vp]),
+        "kvc_tree_verify": (C.c_int, [i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
+        "kvc_page_attend_masked_workspace_size": (sz, [pl, pg, i32, i32, i32, i32]),
+        "kvc_page_attend_masked": (C.c_int, [pl, pg, i32, i32, i32, vp, ps, vp, i32, i32, vp, vp, C.c_float, vp, vp, vp,
+                                             vp, sz, vp]),
+        "kvc_page_slide": (C.c_int, [pl, pg, i32, i32, vp, vp, vp, sz, vp]),
+        "kvc_page_accept": (C.c_int, [pl, pg, i32, vp, vp, vp, vp, vp, sz, vp]),
         "kvc_strerror": (C.c_char_p, [C.c_int]),
         "kvc_abi_version": (C.c_int, []),
         "kvc_debug_fault": (C.c_int, [i32]),
@@ -558,3 +567,104 @@ def kvc_page_attend(pool: Pool, pages: Pages, q: torch.Tensor, out: torch.Tensor
                (_dtype_code(q), Hq, T, qp, qs, _ints(n_q, (B,), pool.device, "n_q"),
                 float(D ** -0.5 if scale is None else scale), _ints(out, shape, pool.device, "out", q.dtype),
                 _ints(lse, (B, T, Hq), pool.device, "lse", torch.float32), _word(status, pool), wp, wb))
+
+
+# ---------------------------------------------------------------------------------------------
+# windows and drafted trees over the paged cache
+# ---------------------------------------------------------------------------------------------
+def _tree_call(name: str, parent: torch.Tensor, stream, args):
+    """One tree entry point on the device of ``parent`` [B, T]; the stream comes last."""
+    dev = parent.device
+    stream = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream(stream)
+    f = getattr(_lib or lib(), name)
+    if dev.index == torch._C._cuda_getDevice():
+        rc = f(*parent.shape, parent.data_ptr(), *args, stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = f(*parent.shape, parent.data_ptr(), *args, stream)
+    if rc:
+        _check(rc)
+
+
+def _tree(parent: torch.Tensor):
+    """(B, T, device) of a tree's parents."""
+    if not parent.is_cuda:
+        raise ValueError("libkvc takes CUDA tensors")
+    if parent.dim() != 2 or parent.dtype is not torch.int32 or not parent.is_contiguous():
+        raise ValueError("parent must be a contiguous int32 tensor [B, T]")
+    return (*parent.shape, parent.device)
+
+
+def kvc_tree_mask(parent: torch.Tensor, mask: torch.Tensor, depth: Optional[torch.Tensor] = None,
+                  n_q: Optional[torch.Tensor] = None, window: int = 0, status: Optional[torch.Tensor] = None,
+                  stream=None):
+    """Which drafts each one sees: ``parent`` [B, T] to the bits ``mask`` [B, T, ceil(T/32)] (int32 words) of itself and
+    its ancestors (the nearest ``window`` of them, 0: all) and its ``depth`` [B, T]; once a step, for all layers."""
+    B, T, dev = _tree(parent)
+    _tree_call("kvc_tree_mask", parent, stream,
+               (_ints(n_q, (B,), dev, "n_q"), int(window), _ints(mask, (B, T, (T + 31) // 32), dev, "mask"),
+                _ints(depth, (B, T), dev, "depth"), _ints(status, (1,), dev, "status")))
+
+
+def kvc_tree_verify(parent: torch.Tensor, draft: torch.Tensor, target: torch.Tensor, path: torch.Tensor,
+                    n_path: torch.Tensor, next: Optional[torch.Tensor] = None, n_q: Optional[torch.Tensor] = None,
+                    status: Optional[torch.Tensor] = None, stream=None):
+    """The drafts that the model's picks confirm: token numbers ``draft`` [B, T] and, behind each draft, the model's
+    ``target`` [B, T] to ``path`` [B, T] (ascending, -1 behind), ``n_path`` [B] and the pick behind it, ``next`` [B]."""
+    B, T, dev = _tree(parent)
+    _tree_call("kvc_tree_verify", parent, stream,
+               (_ints(draft, (B, T), dev, "draft"), _ints(target, (B, T), dev, "target"), _ints(n_q, (B,), dev, "n_q"),
+                _ints(path, (B, T), dev, "path"), _ints(n_path, (B,), dev, "n_path"), _ints(next, (B,), dev, "next"),
+                _ints(status, (1,), dev, "status")))
+
+
+def kvc_page_attend_masked_workspace_size(pool: Pool, pages: Pages, Hq: int, T: int, window: int = 0,
+                                          sinks: int = 0) -> int:
+    return int(lib().kvc_page_attend_masked_workspace_size(pool.ref, pages.ref, Hq, T, window, sinks))
+
+
+def kvc_page_attend_masked(pool: Pool, pages: Pages, q: torch.Tensor, out: torch.Tensor, window: int = 0, sinks: int = 0,
+                           mask: Optional[torch.Tensor] = None, depth: Optional[torch.Tensor] = None,
+                           lse: Optional[torch.Tensor] = None, n_q: Optional[torch.Tensor] = None,
+                           scale: Optional[float] = None, status: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None, stream=None):
+    """kvc_page_attend where a query sees the first ``sinks`` tokens and those less than ``window`` positions back (0:
+    all) and, with ``mask`` [B, T, ceil(T/32)] and ``depth`` [B, T] of kvc_tree_mask, of the queries' own tokens its
+    ancestors."""
+    B = pages.shape[1]
+    shape = q.shape
+    if len(shape) != 4:
+        raise ValueError("q must be a [B, T, Hq, D] tensor")
+    _, T, Hq, D = shape
+    dev = pool.device
+    qp, qs = _rows(q, (B, T, Hq, pool.D), pool, "q")
+    wp, wb, ws = _page_ws(lambda: kvc_page_attend_masked_workspace_size(pool, pages, Hq, T, window, sinks), pool,
+                          workspace, stream)
+    _page_call("kvc_page_attend_masked", pool, pages, stream,
+               (_dtype_code(q), Hq, T, qp, qs, _ints(n_q, (B,), dev, "n_q"), int(window), int(sinks),
+                _ints(mask, (B, T, (T + 31) // 32), dev, "mask"), _ints(depth, (B, T), dev, "depth"),
+                float(D ** -0.5 if scale is None else scale), _ints(out, shape, dev, "out", q.dtype),
+                _ints(lse, (B, T, Hq), dev, "lse", torch.float32), _word(status, pool), wp, wb))
+
+
+def kvc_page_slide(pool: Pool, pages: Pages, window: int, sinks: int = 0, gone: Optional[torch.Tensor] = None,
+                   status: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Every stream's whole pages between the first ``sinks`` tokens and the last ``window`` are given up; ``gone``
+    [L, B, Hkv] receives the tokens that went."""
+    wp, wb, ws = _page_ws(lambda: kvc_page_workspace_size(pool, pages), pool, workspace, stream)
+    _page_call("kvc_page_slide", pool, pages, stream,
+               (int(window), int(sinks), _ints(gone, pages.shape, pool.device, "gone"), _word(status, pool), wp, wb))
+
+
+def kvc_page_accept(pool: Pool, pages: Pages, path: torch.Tensor, n_path: torch.Tensor,
+                    n_q: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, stream=None):
+    """Of every stream's newest T (or ``n_q`` [B]) tokens those at ``path`` [B, T] stay, ``n_path`` [B] of them; the
+    others go."""
+    B, dev = pages.shape[1], pool.device
+    if path.dim() != 2:
+        raise ValueError("path must be a [B, T] tensor")
+    wp, wb, ws = _page_ws(lambda: kvc_page_workspace_size(pool, pages), pool, workspace, stream)
+    _page_call("kvc_page_accept", pool, pages, stream,
+               (path.shape[1], _ints(path, (B, path.shape[1]), dev, "path"), _ints(n_path, (B,), dev, "n_path"),
+                _ints(n_q, (B,), dev, "n_q"), _word(status, pool), wp, wb))

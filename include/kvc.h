@@ -453,7 +453,7 @@ typedef struct {
 /* Bytes of a page; 0 for an unsupported D or page. */
 KVC_API size_t kvc_page_bytes(int32_t D, int32_t page);
 
-/* Device scratch of kvc_page_extend, _free, _fork and _compact (256-byte aligned; contents on entry do
+/* Device scratch of kvc_page_extend, _free, _fork, _compact, _slide and _accept (256-byte aligned; contents on entry do
  * not matter; two calls that may overlap need two). 0 for bad arguments. */
 KVC_API size_t kvc_page_workspace_size(const kvc_pool* pool, const kvc_pages* pages);
 
@@ -564,6 +564,92 @@ KVC_API size_t kvc_page_attend_workspace_size(const kvc_pool* pool, const kvc_pa
 KVC_API int kvc_page_attend(const kvc_pool* pool, const kvc_pages* pages, int32_t dtype, int32_t Hq, int32_t T,
                             const void* q, const int64_t* q_strides, const int32_t* n_q, float scale, void* out,
                             float* lse, int32_t* status, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Windows and drafted trees over the paged cache
+ * ----------------------------------------------
+ * The eviction policy's prefix and recent windows without its scores ("prefix token 和最近一小段 token 始终保留",
+ * BeaconKV write-up, end of "打分时的 RoPE 对齐"): kvc_page_attend_masked reads only them, and kvc_page_slide
+ * gives up the pages between. And speculative decoding with trees: a step's drafts are stored as the newest n_q
+ * tokens (kvc_page_extend, kvc_page_store), each with its parent among them; kvc_tree_mask says which drafts each
+ * one sees, kvc_tree_verify which path the model's picks confirm, kvc_page_accept keeps that path's rows. The pages
+ * describe neither: this library's own.
+ *
+ * A tree: parent[b,i] is in [-1, i) for every draft i < n_q[b] (all T when n_q is NULL; clamped to [0, T]); -1 marks
+ * a root. T <= KVC_TREE_MAX.
+ */
+#define KVC_TREE_MAX 1024
+
+/*
+ * kvc_tree_mask -- who sees whom: bit j % 32 of mask[b,i,j/32] is set where j is i or one of its ancestors and, with
+ * window > 0, fewer than `window` steps above it; depth[b,i] is the number of i's ancestors. Rows i >= n_q[b] are
+ * zero. A sequence with a malformed parent gets zeros (KVC_STATUS_BAD_INDEX). Once a step: all layers use the result.
+ *
+ *   parent     [B,T] int32 (device);  n_q [B] (device) or NULL
+ *   mask       [B,T,ceil(T/32)] (device, out);  depth [B,T] int32 (device, out) or NULL
+ */
+KVC_API int kvc_tree_mask(int32_t B, int32_t T, const int32_t* parent, const int32_t* n_q, int32_t window,
+                          uint32_t* mask, int32_t* depth, int32_t* status, void* stream);
+
+/*
+ * kvc_tree_verify -- the path that the model's picks confirm, greedily: draft 0, the tree's root, is the token that the
+ * step before chose and is always kept; behind a kept draft i comes the lowest child c with draft[b,c] ==
+ * target[b,i], the model's pick after i. path[b] receives the kept drafts (ascending, -1 behind them), n_path[b] their
+ * number, next[b] the pick behind the last one: the next step's root. A sequence without drafts, or with a malformed
+ * parent (KVC_STATUS_BAD_INDEX), gets an empty path and next = -1. Programs that accept otherwise (by sampling) fill
+ * path and n_path themselves.
+ *
+ *   parent, draft, target  [B,T] int32 (device);  n_q [B] (device) or NULL
+ *   path [B,T], n_path [B], next [B] or NULL (device, out)
+ */
+KVC_API int kvc_tree_verify(int32_t B, int32_t T, const int32_t* parent, const int32_t* draft, const int32_t* target,
+                            const int32_t* n_q, int32_t* path, int32_t* n_path, int32_t* next, int32_t* status,
+                            void* stream);
+
+/*
+ * kvc_page_attend_masked -- kvc_page_attend where a query sees part of the tokens. Arguments, results and their
+ * precision, refusals and workspace as there, and:
+ *
+ *   base = len - n_q[b] tokens came before the queries' own; query i < n_q stands at pos = base + depth[b,i] (depth
+ *   NULL: base + i; values out of [0, n_q) count as the nearer end).
+ *   window, sinks  with window > 0, of the base tokens it sees j < sinks and j > pos - window; 0: all of them
+ *   mask           NULL: the queries' own tokens up to itself, under the same window and sinks;
+ *                  else the own token base + u exactly where bit u of mask[b,i] is set, as kvc_tree_mask wrote it or
+ *                  otherwise (T <= KVC_TREE_MAX; bits at or past n_q do not count)
+ *   depth          [B,T] (device) or NULL; only with a mask
+ * Tokens are counted in storage order, so after an eviction a window is one of kept tokens.
+ */
+KVC_API size_t kvc_page_attend_masked_workspace_size(const kvc_pool* pool, const kvc_pages* pages, int32_t Hq, int32_t T,
+                                                     int32_t window, int32_t sinks);
+KVC_API int kvc_page_attend_masked(const kvc_pool* pool, const kvc_pages* pages, int32_t dtype, int32_t Hq, int32_t T,
+                                   const void* q, const int64_t* q_strides, const int32_t* n_q, int32_t window,
+                                   int32_t sinks, const uint32_t* mask, const int32_t* depth, float scale, void* out,
+                                   float* lse, int32_t* status, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * kvc_page_slide -- the pages that no later query's window reaches. Of every stream the pages from ceil(sinks / page) on
+ * that lie wholly before token len + 1 - window (the first one that a query at position len sees) are given up and
+ * the entries behind them move up; no row moves, shared pages stay with their other holders. The stream's tokens are
+ * then those left, in order: a windowed attention with no more sinks and no longer window returns the same as before.
+ * (With drafts in the cache that may be dropped again, slide first or take a window longer by their number.)
+ * gone[l,b,h] (device, out, may be NULL) receives the tokens given up, -1 for a stream of bad length (KVC_STATUS_BAD_PAGE,
+ * left alone); a bad page number among those given up is reported like kvc_page_free's. window >= 1, sinks >= 0.
+ */
+KVC_API int kvc_page_slide(const kvc_pool* pool, const kvc_pages* pages, int32_t window, int32_t sinks, int32_t* gone,
+                           int32_t* status, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * kvc_page_accept -- of every stream's newest n_q[b] tokens (all T when n_q is NULL; clamped to [0, T]) those at
+ * path[b,0..n_path[b]) stay, moved to the front of the n_q, and the others go, with the pages that then hold no token: as
+ * kvc_page_compact with the list 0 .. base-1, base + path[b,.] (what it says of shared, fresh and bad pages holds
+ * here). A path that is not strictly increasing in [0, n_q), or longer than n_q, or a stream shorter than n_q sets
+ * KVC_STATUS_BAD_INDEX: that stream is left alone.
+ *
+ *   path       [B,T] int32 (device), n_path [B] (device), as kvc_tree_verify wrote them or otherwise
+ */
+KVC_API int kvc_page_accept(const kvc_pool* pool, const kvc_pages* pages, int32_t T, const int32_t* path,
+                            const int32_t* n_path, const int32_t* n_q, int32_t* status, void* workspace, size_t ws_bytes,
+                            void* stream);
 
 /* Number of kernels one kvc_evict call with these arguments and default options
  * launches (host only; for accounting, e.g. counting launches inside a timed region;
