@@ -54,8 +54,8 @@ struct Smem {
 
 // Rows per thread in the accumulators: of tile nt, rows 2t and 2t+1 (t = lane % 4); channels
 // CPV*g + 2 mt (+1), g = lane / 4.
-template <typename T, int D, int NT, int PARTS, int MINB>
-__global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a, AttendPlan p) {
+template <typename T, int D, int NT, int PARTS, int MINB, typename M>
+__global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a, AttendPlan p, M m) {
   using SM = Smem<D, NT>;
   constexpr int KS = D / 16;   // k steps of Q K^T and m tiles of V^T
   constexpr int CPL = D / 4;   // channels of a lane in K
@@ -80,14 +80,14 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
   if (!p.whole) {
     const int per = (p.nvs + 32 * kWarps - 1) / (32 * kWarps);
     int W;
-    int before = scan_units<32 * kWarps>(a, p, sm_scan, per, &W);
+    int before = scan_units<32 * kWarps>(a, p, m, sm_scan, per, &W);
     split = Split(W, p.grid);
     const int w0 = split.first(blockIdx.x), w1 = split.first(blockIdx.x + 1);
     if (w0 >= w1) return;
     for (int i = 0; i < per; ++i) {
       const int v = threadIdx.x * per + i;
       if (v >= p.nvs) break;
-      const int u = cost_of(p, stream_of(a, p, v, false));
+      const int u = cost_of(p, stream_of(a, p, m, v, false));
       if (before <= w0 && w0 < before + u) {
         sm_first[0] = v;
         sm_first[1] = before;
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
     ca = w0 - base;
     left = w1 - w0;
   } else {
-    const Stream x = stream_of(a, p, vs, threadIdx.x == 0);
+    const Stream x = stream_of(a, p, m, vs, threadIdx.x == 0);
     left = units_of(p, x);
     if (left == 0)  // rows that see nothing
       for (int e = threadIdx.x; e < x.rows * D; e += 32 * kWarps) {
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
   bool alive = true;
 
   for (int C; left > 0; ++vs, ca = 0, base += C) {
-    const Stream x = stream_of(a, p, vs, true);
+    const Stream x = stream_of(a, p, m, vs, true);
     C = cost_of(p, x);
     if (C == 0) continue;
     const int cb = min(C, ca + left), ua = max(ca - p.lead, 0), ub = max(cb - p.lead, 0), U = C - p.lead;
@@ -130,6 +130,16 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
     const uint8_t* src[2];
     auto locate = [&](int i) {
       const int tok = (c0 + kWarps * (i + lane)) * kChunk32;
+      if constexpr (kPart<M>) {  // the blocks left out may end anywhere in a page
+        const bool want = i + lane < mine, want1 = want && tok + 16 < x.vis;
+        const int r0 = x.real(tok), r1 = x.real(tok + 16);
+        const int id0 = want ? row[r0 >> a.g.lp] : 0, id1 = want1 ? row[r1 >> a.g.lp] : 0;
+        const int pmask = (1 << a.g.lp) - 1;
+        src[0] = page_ok(a.g, id0) ? block_of(a.g, id0, (r0 & pmask) >> 4) : nullptr;
+        src[1] = want1 && page_ok(a.g, id1) ? block_of(a.g, id1, (r1 & pmask) >> 4) : nullptr;
+        if (want && (!src[0] || (want1 && !src[1]))) status_or(a.status, KVC_STATUS_BAD_PAGE);
+        return;
+      }
       const int q0 = tok >> a.g.lp, q1 = (tok + 16) >> a.g.lp;
       const bool want = i + lane < mine, want1 = want && tok + 16 < x.vis;
       const int id0 = want ? row[q0] : 0;
@@ -164,6 +174,7 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
     uint32_t qf[NT][PARTS][KS][2];
     float f[NT][2];  // rows 2t, 2t+1: scale * log2 e over that power
     int lim[NT][2];
+    int lo[NT][2];  // under SeenArgs
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = x.r0 + nt * 8 + g;
@@ -208,9 +219,22 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
         f[nt][e] = __shfl_sync(kFull, inv, 8 * t + 4 * e);
         const int rr = nt * 8 + 2 * t + e;
         lim[nt][e] = rr < x.rows ? seen_by(p, x, x.r0 + rr) : x.vis;
+        if constexpr (kPart<M>) {
+          lo[nt][e] = 0;
+          if (rr < x.rows) {
+            const RowSeen w = row_seen(a, p, m, x, x.r0 + rr);
+            lo[nt][e] = w.lo;
+            lim[nt][e] = w.hi;
+          }
+        }
       }
     }
-    const int minlim = seen_by(p, x, x.r0);
+    int minlim = seen_by(p, x, x.r0), maxlo = 0;
+    if constexpr (kPart<M>) {
+      const RowSeen w = all_see(p, m, x);
+      maxlo = w.lo;
+      minlim = w.hi;
+    }
 
     float o[NT][KS][4];
     float ref[NT][2], l[NT][2];  // reference minus kOff (0 until a token is seen), this lane's part of the sum
@@ -290,7 +314,8 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
       }
 
       // logits in base 2 over the reference; what a row does not see is -inf
-      const bool masked = tok0 + kChunk32 > minlim || ok != 3;
+      bool masked = tok0 + kChunk32 > minlim || ok != 3;
+      if constexpr (kPart<M>) masked |= tok0 < maxlo && tok0 + kChunk32 > x.sinks;
       float2 y[2][NT][2];  // rows 2t, 2t+1 of token g (first) and g + 8
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk)
@@ -300,7 +325,28 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
           for (int h = 0; h < 2; ++h)
             y[blk][nt][h] = fma2(make_float2(sc[blk][nt][2 * h], sc[blk][nt][2 * h + 1]), make_float2(f[nt][0], f[nt][1]),
                                  make_float2(-ref[nt][0], -ref[nt][1]));
-      if (masked) {
+      if (kPart<M> && masked) {
+        if constexpr (kPart<M>) {
+          const int base = x.len - x.nq;
+          const bool own = m.mask && tok0 + kChunk32 > base;  // the same for the whole warp
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int rr = nt * 8 + 2 * t + e;
+              const uint32_t* words = own && rr < x.rows ? mask_words(a, p, m, x, x.r0 + rr) : nullptr;
+#pragma unroll
+              for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const int tok = tok0 + 16 * blk + g + 8 * h, u = tok - base;
+                  bool see = tok < lim[nt][e] && (tok < x.sinks || tok >= lo[nt][e]);
+                  if (words && u >= 0 && tok < x.vis) see = words[u >> 5] >> (u & 31) & 1;
+                  if (!see || !(ok >> blk & 1)) (e ? y[blk][nt][h].y : y[blk][nt][h].x) = -INFINITY;
+                }
+            }
+        }
+      } else if (masked) {
 #pragma unroll
         for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
@@ -388,12 +434,16 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
             s[e] = sb[tk * 4 + (g >> 1)];
           }
         }
-        if (masked) {  // behind the last visible token lies anything: a zero scale keeps it out of 0 * NaN
+        if (!kPart<M> && masked) {  // behind the last visible token lies anything: a zero scale keeps it out of 0 * NaN
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             if (tok0 + 16 * blk + 2 * t + (e & 1) + (e >= 2 ? 8 : 0) >= x.vis || !(ok >> blk & 1)) s[e] = 0;
         }
-        const uint32_t s01 = e4m3x2_f16x2(__byte_perm(s[0], s[1], 0x3340)), s23 = e4m3x2_f16x2(__byte_perm(s[2], s[3], 0x3340));
+        uint32_t s01 = e4m3x2_f16x2(__byte_perm(s[0], s[1], 0x3340)), s23 = e4m3x2_f16x2(__byte_perm(s[2], s[3], 0x3340));
+        if constexpr (kPart<M>) {
+          s01 = no_nan2(s01);
+          s23 = no_nan2(s23);
+        }
 #pragma unroll
         for (int j = 0; j < CPV / 8; ++j) {
           uint32_t e01[4], o01[4], e23[4], o23[4];
@@ -524,8 +574,8 @@ struct Merged {
 // Rows whose stream several CTAs shared, and rows of streams without tokens: a CTA per row, its warps taking
 // every fourth part, four at a time.
 constexpr int kCombThreads = 128, kCombWarps = kCombThreads / 32;
-template <typename T, int D>
-__global__ void __launch_bounds__(kCombThreads) combine_kernel(AttendArgs a, AttendPlan p) {
+template <typename T, int D, typename M>
+__global__ void __launch_bounds__(kCombThreads) combine_kernel(AttendArgs a, AttendPlan p, M seen) {
   __shared__ float sm_o[kCombWarps][D];
   __shared__ float2 sm_ml[kCombWarps];
   griddep_launch();
@@ -533,7 +583,7 @@ __global__ void __launch_bounds__(kCombThreads) combine_kernel(AttendArgs a, Att
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int vs = blockIdx.x >> p.lrb, rr = blockIdx.x & (p.rb - 1);
   const int2 span = p.span[vs];  // read beside the length; undefined for a stream without units
-  const Stream x = stream_of(a, p, vs, threadIdx.x == 0 && rr == 0);
+  const Stream x = stream_of(a, p, seen, vs, threadIdx.x == 0 && rr == 0);
   if (rr >= x.rows) return;
   const size_t at = out_row(a, p, x, x.r0 + rr);
   T* op = static_cast<T*>(a.out) + at * D;
@@ -584,14 +634,14 @@ __global__ void __launch_bounds__(kCombThreads) combine_kernel(AttendArgs a, Att
 }
 
 // The tcgen05 kernel's parts lie with the rows contiguous: a thread a row, 16 channels a CTA.
-template <typename T, int D>
-__global__ void __launch_bounds__(kTcRows) combine_tc_kernel(AttendArgs a, AttendPlan p) {
+template <typename T, int D, typename M>
+__global__ void __launch_bounds__(kTcRows) combine_tc_kernel(AttendArgs a, AttendPlan p, M seen) {
   griddep_launch();
   griddep_wait();
   constexpr int C = 16, kPer = D / C;
   const int vs = blockIdx.x / kPer, c0 = blockIdx.x % kPer * C, rr = threadIdx.x;
   const int2 span = p.span[vs];
-  const Stream x = stream_of(a, p, vs, rr == 0);
+  const Stream x = stream_of(a, p, seen, vs, rr == 0);
   const bool given_up = x.vis && span.x < 0;
   if (rr >= x.rows || (x.vis && span.x == span.y && !given_up)) return;
   float o[C], l = 0.f, m = -INFINITY;
@@ -649,7 +699,15 @@ constexpr int kWholeCap = 512, kWholeCapMany = 2048;
 constexpr int tiles_for(int R) { return R <= 8 ? 1 : 2; }
 constexpr int min_blocks(int nt, int parts) { return nt * parts == 1 ? 4 : nt * parts == 2 ? 3 : 2; }
 
-AttendPlan make_plan(const AttendArgs& a, int parts, int sms, size_t* bytes) {
+// The most tokens that a block of rows sees, of a stream of `cap` and `ntok` queries.
+long long most_seen(const Causal&, long long cap, long long) { return cap; }
+long long most_seen(const SeenArgs& m, long long cap, long long ntok) {
+  const long long n = (long long)m.window + m.sinks + ntok + 3 * kBlkTok;  // rounded to blocks
+  return n < cap ? n : cap;
+}
+
+template <typename M>
+AttendPlan make_plan(const AttendArgs& a, const M& m, int parts, int sms, size_t* bytes) {
   AttendPlan p = {};
   p.G = a.Hq / a.t.Hkv;
   const int R = p.G * a.T, nt = tiles_for(R);
@@ -665,7 +723,7 @@ AttendPlan make_plan(const AttendArgs& a, int parts, int sms, size_t* bytes) {
   while ((1 << p.lrb) < p.rb) ++p.lrb;
   sms = sms < kMaxGridSMs ? sms : kMaxGridSMs;
   p.grid = sms * (tc ? 1 : min_blocks(nt, parts));
-  const long long cap = (long long)a.t.maxp << a.g.lp;
+  const long long cap = most_seen(m, (long long)a.t.maxp << a.g.lp, a.T);
   const long long cost = (long long)p.nvs * ((cap + p.unit - 1) / p.unit + p.lead);  // if every stream is full
   if (cost < p.grid) p.grid = (int)cost;
   if (!tc && cap <= (p.nvs >= 2 * sms ? kWholeCapMany : kWholeCap)) {
@@ -685,38 +743,67 @@ AttendPlan make_plan(const AttendArgs& a, int parts, int sms, size_t* bytes) {
   return p;
 }
 
-template <typename T, int D, int NT, int PARTS>
-int go(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
-  auto k = attend_kernel<T, D, NT, PARTS, min_blocks(NT, PARTS)>;
+template <typename T, int D, int NT, int PARTS, typename M>
+int go(const AttendArgs& a, const AttendPlan& p, const M& m, cudaStream_t s) {
+  auto k = attend_kernel<T, D, NT, PARTS, min_blocks(NT, PARTS), M>;
   constexpr int smem = Smem<D, NT>::bytes;
   if (smem > 47 * 1024 &&  // beyond the default, beside the kernel's static part
       cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return KVC_ERR_LAUNCH;
-  return launch_pdl(k, dim3(p.grid), dim3(32 * kWarps), smem, s, false, a, p) == cudaSuccess ? KVC_OK : KVC_ERR_LAUNCH;
+  return launch_pdl(k, dim3(p.grid), dim3(32 * kWarps), smem, s, false, a, p, m) == cudaSuccess ? KVC_OK
+                                                                                                : KVC_ERR_LAUNCH;
 }
 
-template <typename T, int D, int PARTS>
-int run(const AttendArgs& a, int sms, cudaStream_t s) {
-  const AttendPlan p = make_plan(a, PARTS, sms, nullptr);
+template <typename T, int D, int PARTS, typename M>
+int run(const AttendArgs& a, const M& m, int sms, cudaStream_t s) {
+  const AttendPlan p = make_plan(a, m, PARTS, sms, nullptr);
   int rc = KVC_ERR_INVALID_ARG;
   switch (p.rb / 8) {
-    case 1: rc = go<T, D, 1, PARTS>(a, p, s); break;
-    case 2: rc = go<T, D, 2, PARTS>(a, p, s); break;
+    case 1: rc = go<T, D, 1, PARTS>(a, p, m, s); break;
+    case 2: rc = go<T, D, 2, PARTS>(a, p, m, s); break;
     case kTcRows / 8:
-      if constexpr (PARTS == 1) rc = launch_attend_tc(a, p, s);
+      if constexpr (PARTS == 1) rc = launch_attend_tc(a, p, m, s);
       break;
   }
   if (rc || p.whole) return rc;
   const long long rows = (long long)p.nvs * p.rb;
   if constexpr (PARTS == 1)
     if (p.rb == kTcRows)
-      return launch_pdl(combine_tc_kernel<T, D>, dim3((unsigned)(p.nvs * (D / 16))), dim3(kTcRows), 0, s, false, a, p) ==
-                     cudaSuccess
+      return launch_pdl(combine_tc_kernel<T, D, M>, dim3((unsigned)(p.nvs * (D / 16))), dim3(kTcRows), 0, s, false, a, p,
+                        m) == cudaSuccess
                  ? KVC_OK
                  : KVC_ERR_LAUNCH;
-  return launch_pdl(combine_kernel<T, D>, dim3((unsigned)rows), dim3(kCombThreads), 0, s, false, a, p) == cudaSuccess
+  return launch_pdl(combine_kernel<T, D, M>, dim3((unsigned)rows), dim3(kCombThreads), 0, s, false, a, p, m) == cudaSuccess
              ? KVC_OK
              : KVC_ERR_LAUNCH;
+}
+
+template <typename M>
+size_t ws_bytes(const PoolGeom& g, const PageTab& t, int Hq, int T, const M& m) {
+  AttendArgs a = {};
+  a.g = g;
+  a.t = t;
+  a.Hq = Hq;
+  a.T = T;
+  if (!attend_fits(a)) return 0;
+  size_t most = 0;
+  for (int parts = 1; parts <= 2; ++parts) {
+    size_t n;
+    make_plan(a, m, parts, kMaxGridSMs, &n);
+    most = n > most ? n : most;
+  }
+  return most;
+}
+
+template <typename M>
+int launch(const AttendArgs& a, const M& m, int dtype, cudaStream_t s) {
+  int dev, sms;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return KVC_ERR_LAUNCH;
+  if (dtype == KVC_BF16)
+    return a.g.D == 128 ? run<__nv_bfloat16, 128, 1>(a, m, sms, s) : run<__nv_bfloat16, 64, 1>(a, m, sms, s);
+  return a.g.D == 128 ? run<float, 128, 2>(a, m, sms, s) : run<float, 64, 2>(a, m, sms, s);
 }
 
 }  // namespace
@@ -727,29 +814,14 @@ bool attend_fits(const AttendArgs& a) {  // work units and rows are counted in 3
   return nvs * rb <= 0x7fffffffLL && nvs * ((((long long)a.t.maxp << a.g.lp) + kUnit - 1) / kUnit + kTcLead) <= 0x7fffffffLL;
 }
 
-size_t attend_ws_bytes(const PoolGeom& g, const PageTab& t, int Hq, int T) {
-  AttendArgs a = {};
-  a.g = g;
-  a.t = t;
-  a.Hq = Hq;
-  a.T = T;
-  if (!attend_fits(a)) return 0;
-  size_t most = 0;
-  for (int parts = 1; parts <= 2; ++parts) {
-    size_t n;
-    make_plan(a, parts, kMaxGridSMs, &n);
-    most = n > most ? n : most;
-  }
-  return most;
-}
+size_t attend_ws_bytes(const PoolGeom& g, const PageTab& t, int Hq, int T) { return ws_bytes(g, t, Hq, T, Causal{}); }
+int launch_page_attend(const AttendArgs& a, int dtype, cudaStream_t s) { return launch(a, Causal{}, dtype, s); }
 
-int launch_page_attend(const AttendArgs& a, int dtype, cudaStream_t s) {
-  int dev, sms;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return KVC_ERR_LAUNCH;
-  if (dtype == KVC_BF16) return a.g.D == 128 ? run<__nv_bfloat16, 128, 1>(a, sms, s) : run<__nv_bfloat16, 64, 1>(a, sms, s);
-  return a.g.D == 128 ? run<float, 128, 2>(a, sms, s) : run<float, 64, 2>(a, sms, s);
+size_t attend_masked_ws_bytes(const PoolGeom& g, const PageTab& t, int Hq, int T, const SeenArgs& m) {
+  return ws_bytes(g, t, Hq, T, m);
+}
+int launch_page_attend_masked(const AttendArgs& a, const SeenArgs& m, int dtype, cudaStream_t s) {
+  return launch(a, m, dtype, s);
 }
 
 }  // namespace kvc

@@ -2,6 +2,8 @@
 // over the CTAs, partial results, and small helpers.
 #pragma once
 
+#include <type_traits>
+
 #include "page.cuh"
 #include "tc_ptx.cuh"
 
@@ -27,9 +29,19 @@ struct AttendPlan {
 
 struct Stream {  // what a (stream, row block) has to see
   int s, b, h, len, nq, r0, rows, vis;
+  // Under SeenArgs the tokens that no row of the block sees, between the sinks and the windows, are left out in
+  // whole 16-token blocks: len, vis and every token number count without them, and token v lies in the cache at
+  // real(v). With skip > 0 the sinks end at or before `at` and every row's window begins at or behind it.
+  int at, skip, sinks;
+  __device__ __forceinline__ int real(int v) const { return v < at ? v : v + skip; }
 };
 
-__device__ __forceinline__ Stream stream_of(const AttendArgs& a, const AttendPlan& p, int vs, bool report) {
+struct Causal {};  // what the rows of kvc_page_attend see: SeenArgs' place there
+template <typename M>
+constexpr bool kPart = !std::is_same<M, Causal>::value;
+
+template <typename M>
+__device__ __forceinline__ Stream stream_of(const AttendArgs& a, const AttendPlan& p, const M& m, int vs, bool report) {
   Stream x;
   x.s = p.by_nrb.div(vs);
   x.r0 = (vs - x.s * p.nrb) * p.rb;
@@ -44,6 +56,18 @@ __device__ __forceinline__ Stream stream_of(const AttendArgs& a, const AttendPla
   x.rows = max(0, min(p.rb, x.nq * p.G - x.r0));
   const int tmax = min(p.by_G.div(x.r0 + p.rb - 1), x.nq - 1);
   x.vis = x.rows ? max(0, x.len - x.nq + tmax + 1) : 0;
+  if constexpr (kPart<M>) {
+    const int base = x.len - x.nq;
+    if (m.mask && x.rows) x.vis = x.len;
+    int lo = max(0, base + (m.depth ? 0 : p.by_G.div(x.r0)) - m.window + 1);  // no row's window begins before it
+    if (m.mask) lo = min(lo, max(base, 0));  // of the own tokens any may be seen
+    const int sinks = min(m.sinks, lo);
+    x.at = (sinks + kBlkTok - 1) & -kBlkTok;
+    x.skip = x.vis ? max(0, (lo & -kBlkTok) - x.at) : 0;
+    x.sinks = x.skip ? sinks : m.sinks;
+    x.len -= x.skip;
+    x.vis -= x.skip;
+  }
   return x;
 }
 // Row r of a stream's block: its query token and, with it, offsets in q and out.
@@ -59,16 +83,37 @@ __device__ __forceinline__ size_t out_row(const AttendArgs& a, const AttendPlan&
 __device__ __forceinline__ int seen_by(const AttendPlan& p, const Stream& x, int r) {
   return min(max(x.len - x.nq + p.by_G.div(r) + 1, 0), x.vis);
 }
+// Under SeenArgs row r sees the tokens below x.sinks and those from lo on, up to hi, and under a mask the own tokens,
+// from `base` on, whose bits its words have set.
+struct RowSeen {
+  int lo, hi;
+};
+__device__ __forceinline__ RowSeen row_seen(const AttendArgs& a, const AttendPlan& p, const SeenArgs& m, const Stream& x,
+                                            int r) {
+  const int base = x.len - x.nq, i = p.by_G.div(r);
+  const int d = m.depth ? min(max(m.depth[(size_t)x.b * a.T + i], 0), x.nq - 1) : i;
+  return RowSeen{max(0, base + d - m.window + 1), m.mask ? max(base, 0) : seen_by(p, x, r)};
+}
+// Every row of the block sees all tokens of [lo, hi).
+__device__ __forceinline__ RowSeen all_see(const AttendPlan& p, const SeenArgs& m, const Stream& x) {
+  const int base = x.len - x.nq, last = m.depth ? x.nq - 1 : min(p.by_G.div(x.r0 + p.rb - 1), x.nq - 1);
+  return RowSeen{max(0, base + last - m.window + 1), m.mask ? max(base, 0) : seen_by(p, x, x.r0)};
+}
+__device__ __forceinline__ const uint32_t* mask_words(const AttendArgs& a, const AttendPlan& p, const SeenArgs& m,
+                                                      const Stream& x, int r) {
+  return m.mask + ((size_t)x.b * a.T + p.by_G.div(r)) * m.words;
+}
 __device__ __forceinline__ int units_of(const AttendPlan& p, const Stream& x) { return (x.vis + p.unit - 1) / p.unit; }
 __device__ __forceinline__ int cost_of(const AttendPlan& p, const Stream& x) { return x.vis ? units_of(p, x) + p.lead : 0; }
 
 // Cost, in units, before each thread's run of streams and in all (block of kThr threads; every thread calls).
-template <int kThr>
-__device__ __forceinline__ int scan_units(const AttendArgs& a, const AttendPlan& p, int* sm, int per, int* total) {
+template <int kThr, typename M>
+__device__ __forceinline__ int scan_units(const AttendArgs& a, const AttendPlan& p, const M& m, int* sm, int per,
+                                          int* total) {
   int mine = 0;
   for (int i = 0; i < per; ++i) {
     const int vs = threadIdx.x * per + i;
-    if (vs < p.nvs) mine += cost_of(p, stream_of(a, p, vs, false));
+    if (vs < p.nvs) mine += cost_of(p, stream_of(a, p, m, vs, false));
   }
   int incl = mine;
 #pragma unroll
@@ -109,6 +154,12 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t x, uint32_t y) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// Under SeenArgs a row's probability of a token that it does not see is 0, whatever the token's bytes: a V scale that the
+// store does not write (NaN, below zero) counts as zero.
+__device__ __forceinline__ uint32_t no_nan2(uint32_t x) {
+  const __half2 r = __hmax2(*reinterpret_cast<const __half2*>(&x), __half2half2(__ushort_as_half(0)));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -176,6 +227,7 @@ __device__ __noinline__ static bool mbar_wait_far(uint64_t* bar, uint32_t parity
 
 // The kernel for many query rows (tcgen05, 128 rows a block).
 constexpr int kTcRows = 128, kTcUnit = 128;
-int launch_attend_tc(const AttendArgs& a, const AttendPlan& p, cudaStream_t s);
+template <typename M>
+int launch_attend_tc(const AttendArgs& a, const AttendPlan& p, const M& m, cudaStream_t s);
 
 }  // namespace kvc
