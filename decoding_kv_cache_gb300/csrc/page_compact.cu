@@ -24,43 +24,19 @@ constexpr int kPlanThreads = 256;
 constexpr int kMoveThreads = 128;
 constexpr int kTile = 64;  // tokens moved at a time (36 layers x 8 heads: 36 us a cycle; 32 tokens 42, 128 tokens 41)
 
-// A stream's kept tokens: base of them stay where they are, token base + idx[k] becomes token base + k.
-struct Kept {
-  const int32_t* idx;
-  int base, m, n;  // m kept of n tokens
-  bool ok;
-  __device__ __forceinline__ int at(int k) const { return k < base ? k : base + idx[k - base]; }
-};
-struct KeptLists {  // kvc_page_compact
-  const int32_t *idx, *len;
-  int stride, per_seq;
-  __device__ __forceinline__ Kept of(const PageTab& t, int s) const {
-    const int lst = per_seq ? s / t.Hkv % t.B : s, m = len[lst], n = t.len[s];
-    return Kept{idx + (size_t)lst * stride, 0, m, n, m >= 0 && m <= n && m <= stride};
-  }
-};
-struct KeptPaths {  // kvc_page_accept
-  const int32_t *path, *n_path, *n_q;
-  int T;
-  __device__ __forceinline__ Kept of(const PageTab& t, int s) const {
-    const int b = s / t.Hkv % t.B, n = t.len[s], nq = n_q ? min(max(n_q[b], 0), T) : T, k = n_path[b];
-    return Kept{path + (size_t)b * T, n - nq, n - nq + k, n, n >= nq && k >= 0 && k <= nq};
-  }
-};
-
-template <typename Lists>
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(PoolGeom g, PageTab t, Lists lists, int32_t* status,
-                                                           PageWs w) {
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(PoolGeom g, PageTab t, const int32_t* kept_idx,
+                                                           const int32_t* kept_len, int stride, int per_seq,
+                                                           int32_t* status, PageWs w) {
   __shared__ int sm_bad, sm_k0, sm_need;
   griddep_launch();
   griddep_wait();
-  const int s = blockIdx.x;
-  const Kept x = lists.of(t, s);
-  const int m = x.m, n = x.n;
+  const int s = blockIdx.x, lst = per_seq ? s / t.Hkv % t.B : s;
+  const int32_t* idx = kept_idx + (size_t)lst * stride;
+  const int m = kept_len[lst], n = t.len[s];
   if (threadIdx.x == 0) {
     const bool badlen = n < 0 || n > ((long long)t.maxp << g.lp);
     if (badlen) status_or(status, KVC_STATUS_BAD_PAGE);
-    sm_bad = badlen || !x.ok;
+    sm_bad = badlen || m < 0 || m > n || m > stride;
     sm_k0 = m;
     sm_need = 0;
     if (s == 0) {
@@ -74,8 +50,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PoolGeom g, PageTab 
   int k0 = m;
   if (!bad) {
 #pragma unroll 4
-    for (int k = x.base + threadIdx.x; k < m; k += kPlanThreads) {  // four reads in flight
-      const int v = x.at(k), next = k + 1 < m ? x.at(k + 1) : n;
+    for (int k = threadIdx.x; k < m; k += kPlanThreads) {  // four reads in flight
+      const int v = idx[k], next = k + 1 < m ? idx[k + 1] : n;
       if (v < k || v >= next) bad = true;
       if (v != k && k < k0) k0 = k;
     }
@@ -144,9 +120,9 @@ __device__ __forceinline__ uint4 load_row(const uint4* p) {
 
 // Five CTAs an SM, as the registers allow anyway: told so, the compiler orders the sweep's reads better (28 x 8 x 4
 // heads that keep a quarter: 104.4 us a cycle without, 102.0 with).
-template <int D, typename Lists>
-__global__ void __launch_bounds__(kMoveThreads, 5) move_kernel(PoolGeom g, PageTab t, Lists lists, int32_t* status,
-                                                           PageWs w) {
+template <int D>
+__global__ void __launch_bounds__(kMoveThreads, 5) move_kernel(PoolGeom g, PageTab t, const int32_t* kept_idx, int stride,
+                                                           int per_seq, int32_t* status, PageWs w) {
   __shared__ int sm[2 * kMoveThreads / 32];
   griddep_launch();
   griddep_wait();
@@ -213,7 +189,7 @@ __global__ void __launch_bounds__(kMoveThreads, 5) move_kernel(PoolGeom g, PageT
   }
   if (!(plan.w & kCompactMoves)) return;
 
-  const Kept kept = lists.of(t, s);
+  const int32_t* idx = kept_idx + (size_t)(per_seq ? s / t.Hkv % t.B : s) * stride;
   const int lmask = (1 << g.lp) - 1;
   const int codes = kv ? piece_off(D, 2) : 0, scales = kv ? piece_off(D, 3) : piece_off(D, 1);
   const bool has_sc = threadIdx.x < kTile;
@@ -227,10 +203,10 @@ __global__ void __launch_bounds__(kMoveThreads, 5) move_kernel(PoolGeom g, PageT
 #pragma unroll
     for (int u = 0; u < M::U; ++u) {
       const int k = t0 + k_of + u * kStep;
-      x.tok[u] = k < m ? kept.at(k) : -1;
+      x.tok[u] = k < m ? idx[k] : -1;
     }
     const int k = t0 + (int)threadIdx.x;
-    x.tok[M::U] = has_sc && k < m ? kept.at(k) : -1;
+    x.tok[M::U] = has_sc && k < m ? idx[k] : -1;
   };
   auto read_pages = [&](Ahead& x) {
 #pragma unroll
@@ -299,26 +275,17 @@ __global__ void __launch_bounds__(kMoveThreads, 5) move_kernel(PoolGeom g, PageT
     }
 }
 
-template <typename Lists>
-int compact(const PoolGeom& g, const PageTab& t, const Lists& lists, int32_t* status, const PageWs& w, cudaStream_t s) {
-  if (launch_pdl(plan_kernel<Lists>, dim3(t.S), dim3(kPlanThreads), 0, s, false, g, t, lists, status, w) != cudaSuccess)
-    return KVC_ERR_LAUNCH;
-  if (launch_pdl(g.D == 128 ? move_kernel<128, Lists> : move_kernel<64, Lists>, dim3(2 * t.S), dim3(kMoveThreads), 0, s,
-                 false, g, t, lists, status, w) != cudaSuccess)
-    return KVC_ERR_LAUNCH;
-  return page_finish_compact(g, t, w, s);
-}
-
 }  // namespace
 
 int launch_page_compact(const PoolGeom& g, const PageTab& t, const int32_t* kept_idx, const int32_t* kept_len,
                         int stride, int per_seq, int32_t* status, const PageWs& w, cudaStream_t s) {
-  return compact(g, t, KeptLists{kept_idx, kept_len, stride, per_seq}, status, w, s);
-}
-
-int launch_page_accept(const PoolGeom& g, const PageTab& t, int T, const int32_t* path, const int32_t* n_path,
-                       const int32_t* n_q, int32_t* status, const PageWs& w, cudaStream_t s) {
-  return compact(g, t, KeptPaths{path, n_path, n_q, T}, status, w, s);
+  if (launch_pdl(plan_kernel, dim3(t.S), dim3(kPlanThreads), 0, s, false, g, t, kept_idx, kept_len, stride, per_seq,
+                 status, w) != cudaSuccess)
+    return KVC_ERR_LAUNCH;
+  if (launch_pdl(g.D == 128 ? move_kernel<128> : move_kernel<64>, dim3(2 * t.S), dim3(kMoveThreads), 0, s, false, g, t,
+                 kept_idx, stride, per_seq, status, w) != cudaSuccess)
+    return KVC_ERR_LAUNCH;
+  return page_finish_compact(g, t, w, s);
 }
 
 }  // namespace kvc

@@ -273,53 +273,6 @@ __global__ void __launch_bounds__(256) free_kernel(PoolGeom g, PageTab t, const 
   if (lane == 0) t.len[s] = left;
 }
 
-// The entries that a slide takes out of a stream of n tokens: [first, last).
-struct SlideSpan {
-  int first, last;
-};
-__device__ __forceinline__ SlideSpan slide_span(const PoolGeom& g, int n, int window, int sinks) {
-  const int first = pages_of(sinks, g.lp);
-  return SlideSpan{first, max(first, n < window ? 0 : (n - window + 1) >> g.lp)};
-}
-
-// A warp slides stream s: the pages of [first, last) are counted down, the entries behind them move up 32 at a time (a
-// chunk's places lie before every later chunk's).
-__device__ __forceinline__ void slide_stream(const PoolGeom& g, const PageTab& t, const PageWs& w, int s, int window,
-                                             int sinks, int32_t* gone, int32_t* status) {
-  const int lane = threadIdx.x & 31, n = t.len[s];
-  if (n < 0 || n > ((long long)t.maxp << g.lp)) {
-    if (lane == 0) {
-      status_or(status, KVC_STATUS_BAD_PAGE);
-      if (gone) gone[s] = -1;
-    }
-    return;
-  }
-  const SlideSpan x = slide_span(g, n, window, sinks);
-  const int m = x.last - x.first, e = pages_of(n, g.lp);
-  if (lane == 0 && gone) gone[s] = m << g.lp;
-  if (m == 0) return;
-  int32_t* row = t.table + (size_t)s * t.maxp;
-  for (int i = x.first + lane; i < x.last; i += 32) drop_page(g, w, row[i], status);
-  __syncwarp();
-  for (int i0 = x.first; i0 < e; i0 += 32) {
-    const int i = i0 + lane;
-    const int p = i + m < e ? row[i + m] : -1;
-    __syncwarp();
-    if (i < e) row[i] = p;
-    __syncwarp();
-  }
-  if (lane == 0) t.len[s] = n - (m << g.lp);
-}
-
-__global__ void __launch_bounds__(256) slide_kernel(PoolGeom g, PageTab t, int window, int sinks, int32_t* gone,
-                                                   int32_t* status, PageWs w) {
-  griddep_launch();
-  griddep_wait();
-  const int s = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  if (s == 0 && threadIdx.x == 0) w.head[0] = *g.nfree;
-  if (s < t.S) slide_stream(g, t, w, s, window, sinks, gone, status);
-}
-
 // Warps of the first t.S streams count their pages' new references (children - 1 each: old references
 // plus every partial sum stay above zero unless all of a page's holders go, so the one that reaches
 // zero is the last whatever the order); the others write the children's rows.
@@ -607,6 +560,332 @@ __global__ void __cluster_dims__(kOneCtas, 1, 1) __launch_bounds__(kOneThreads)
   if (s < t.S) extend_stream(g, t, s, sm_need[s], sm_before[s], none, nfree, add, add_all, start, status);
 }
 
+// ---- slides ---------------------------------------------------------------------------------------
+// The entries that a slide takes out of a stream of n tokens: m from `first` on.
+__device__ __forceinline__ int slide_count(const PoolGeom& g, int n, int window, int first) {
+  return n < window ? 0 : max(0, ((n - window + 1) >> g.lp) - first);
+}
+
+// A warp slides stream s: the pages that go are counted down, the entries behind them move up, 256 read before
+// they are written (their places lie before every later entry's).
+__device__ __forceinline__ void slide_stream(const PoolGeom& g, const PageTab& t, const PageWs& w, int s, int n, int first,
+                                             int m, int32_t* status) {
+  const int lane = threadIdx.x & 31, e = pages_of(n, g.lp);
+  int32_t* row = t.table + (size_t)s * t.maxp;
+  for (int i = first + lane; i < first + m; i += 32) drop_page(g, w, row[i], status);
+  __syncwarp();
+  constexpr int kDeep = 8;
+  for (int i0 = first; i0 < e; i0 += 32 * kDeep) {
+    int p[kDeep];
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) {
+      const int i = i0 + 32 * u + lane + m;
+      p[u] = i < e ? row[i] : -1;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) {
+      const int i = i0 + 32 * u + lane;
+      if (i < e) row[i] = p[u];
+    }
+    __syncwarp();
+  }
+  if (lane == 0) t.len[s] = n - (m << g.lp);
+}
+
+// Lane i of a warp looks at stream s0 + i * step; those that lose pages are slid one after another by the whole warp
+// (in a decode step one in `page`).
+__device__ __forceinline__ void slide_streams(const PoolGeom& g, const PageTab& t, const PageWs& w, int s0, int step,
+                                              int window, int first, int32_t* gone, int32_t* status) {
+  const int lane = threadIdx.x & 31;
+  for (; s0 < t.S; s0 += 32 * step) {
+    const long long s = s0 + (long long)lane * step;
+    int n = 0, m = 0;
+    if (s < t.S) {
+      n = t.len[s];
+      const bool bad = n < 0 || n > ((long long)t.maxp << g.lp);
+      if (bad) status_or(status, KVC_STATUS_BAD_PAGE);
+      m = bad ? 0 : slide_count(g, n, window, first);
+      if (gone) gone[s] = bad ? -1 : m << g.lp;
+    }
+    for (unsigned any = __ballot_sync(kFull, m > 0); any; any &= any - 1) {
+      const int j = __ffs(any) - 1;
+      slide_stream(g, t, w, s0 + j * step, __shfl_sync(kFull, n, j), first, __shfl_sync(kFull, m, j), status);
+    }
+  }
+}
+
+constexpr int kSlideStreams = 4, kSlideOne = 256;  // a warp's in the wide form, a call's in the one-launch form
+__global__ void __launch_bounds__(256) slide_kernel(PoolGeom g, PageTab t, int window, int first, int32_t* gone,
+                                                   int32_t* status, PageWs w) {
+  griddep_launch();
+  griddep_wait();
+  const int warps = gridDim.x * (blockDim.x >> 5), wi = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (wi == 0 && threadIdx.x == 0) w.head[0] = *g.nfree;
+  slide_streams(g, t, w, wi, warps, window, first, gone, status);
+}
+
+__global__ void __cluster_dims__(kOneCtas, 1, 1) __launch_bounds__(kOneThreads)
+    slide_one_kernel(PoolGeom g, PageTab t, int window, int first, int32_t* gone, int32_t* status, PageWs w) {
+  griddep_launch();
+  griddep_wait();
+  cg::cluster_group cl = cg::this_cluster();
+  const int nfree = *g.nfree;
+  cluster_zero(g, w, cl.block_rank() * kOneThreads + threadIdx.x);
+  cl.sync();
+  slide_streams(g, t, w, (threadIdx.x >> 5) * kOneCtas + cl.block_rank(), kOneCtas * kOneThreads / 32, window, first, gone,
+                status);
+  cl.sync();
+  cluster_push(cl, g, w, nfree);
+}
+
+// ---- accepted drafts ------------------------------------------------------------------------------
+// kvc_page_compact's steps for lists that name a few tokens behind `base` unmoved ones, a warp a stream: few rows move
+// and few entries are looked at, so the plan, the move and the new tables are a chain of some six reads, and two
+// launches (or one cluster, barriers between) do instead of four.
+//   plan  the path checked, the first row that moves, the destination pages that are shared (refs are read only here)
+//   move  fresh pages numbered in stream order, rows moved, entries, counts and lengths set
+struct Paths {
+  const int32_t *path, *n_path, *n_q;
+  int T;
+  __device__ __forceinline__ int drafts(int b) const { return n_q ? min(max(n_q[b], 0), T) : T; }
+};
+
+__device__ __forceinline__ void accept_plan(const PoolGeom& g, const PageTab& t, const Paths& x, const PageWs& w, int s,
+                                            int32_t* status) {
+  const int lane = threadIdx.x & 31, b = s / t.Hkv % t.B;
+  const int n = t.len[s], nq = x.drafts(b), np = x.n_path[b], base = n - nq, m = base + np;
+  const int32_t* path = x.path + (size_t)b * x.T;
+  const int32_t* row = t.table + (size_t)s * t.maxp;
+  int32_t* to = w.newtab + (size_t)s * t.maxp;
+  const bool badlen = n < 0 || n > ((long long)t.maxp << g.lp);
+  bool bad = badlen || base < 0 || np < 0 || np > nq;
+  int k0 = np;  // the first draft that moves
+  if (!bad) {
+    for (int k = lane; k < np; k += 32) {
+      const int v = path[k], next = k + 1 < np ? path[k + 1] : nq;
+      bad |= v < k || v >= next;
+      if (v != k && k < k0) k0 = k;
+    }
+    k0 = __reduce_min_sync(kFull, k0);
+    bad = __any_sync(kFull, bad);
+  }
+  if (bad && lane == 0) status_or(status, badlen ? KVC_STATUS_BAD_PAGE : KVC_STATUS_BAD_INDEX);
+  int need = 0, first = base + k0;
+  if (!bad) {
+    bool missing = false, shared0 = false;
+    const int e = pages_of(n, g.lp), pe = k0 < np ? pages_of(m, g.lp) : 0, p0 = first >> g.lp;
+    for (int i = p0 + lane; i < e; i += 32) {
+      const int p = row[i];
+      const bool ok = page_ok(g, p);
+      missing |= !ok;
+      if (i < pe) {
+        const bool shared = ok && g.refs[p] > 1;
+        to[i] = shared ? -1 : p;
+        need += shared;
+        shared0 |= shared && i == p0;
+      }
+    }
+    need = warp_sum_i(need);
+    if (__any_sync(kFull, shared0)) first = p0 << g.lp;  // with its page replaced, the unmoved rows go along
+    bad = __any_sync(kFull, missing);
+    if (bad && lane == 0) status_or(status, KVC_STATUS_BAD_PAGE);
+  }
+  if (lane == 0) {
+    w.need[s] = bad ? 0 : need;
+    w.plan[s] = make_int4(first, m, n, bad ? kCompactBad : k0 < np ? kCompactMoves : 0);
+  }
+}
+
+// Rows [first, m) of a stream by a warp, 16 tokens at a time: a lane holds four of their code vectors (16 bytes) and a
+// token's K or V scales. A batch is read before it is written, and lies before every later batch's sources.
+template <int D>
+__device__ __forceinline__ void accept_rows(const PoolGeom& g, const int32_t* row, const int32_t* to, const int32_t* path,
+                                            int base, int first, int m) {
+  constexpr int kVec = D / 16, kAt = 32 / kVec, kTok = 16, U = kTok / kAt;  // vectors of a token (K, then V)
+  const int lane = threadIdx.x & 31, lmask = (1 << g.lp) - 1, v = lane % kVec, kv = v / (kVec / 2);
+  auto code = [&](int page, int tok) {
+    return reinterpret_cast<uint4*>(block_of(g, page, (tok & lmask) >> 4) + piece_off(D, 2 * kv) + (tok & 15) * (D / 2)) +
+           v % (kVec / 2);
+  };
+  auto scale = [&](int page, int tok) {
+    return block_of(g, page, (tok & lmask) >> 4) + piece_off(D, 1 + 2 * (lane >> 4)) + (tok & 15) * (D / 16);
+  };
+  for (int k0 = first; k0 < m; k0 += kTok) {
+    const int mine = k0 + (lane & 15);
+    const int src = mine >= m ? -1 : mine < base ? mine : base + path[mine - base];
+    const int ps = src >= 0 ? row[src >> g.lp] : 0, pd = src >= 0 ? to[mine >> g.lp] : 0;
+    uint4 c[U];
+    uint64_t sc = 0;
+    if (src >= 0) {
+      if constexpr (D == 128)
+        sc = *reinterpret_cast<const uint64_t*>(scale(ps, src));
+      else
+        sc = *reinterpret_cast<const uint32_t*>(scale(ps, src));
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = u * kAt + lane / kVec;
+      const int sj = __shfl_sync(kFull, src, j), pj = __shfl_sync(kFull, ps, j);
+      if (sj >= 0) c[u] = *code(pj, sj);
+    }
+    __syncwarp();
+    if (src >= 0) {
+      if constexpr (D == 128)
+        *reinterpret_cast<uint64_t*>(scale(pd, mine)) = sc;
+      else
+        *reinterpret_cast<uint32_t*>(scale(pd, mine)) = (uint32_t)sc;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = u * kAt + lane / kVec;
+      const int pj = __shfl_sync(kFull, pd, j);
+      if (k0 + j < m) *code(pj, k0 + j) = c[u];
+    }
+    __syncwarp();
+  }
+}
+
+// before: the pages that the streams before this one take
+template <int D>
+__device__ __forceinline__ void accept_move(const PoolGeom& g, const PageTab& t, const Paths& x, const PageWs& w, int s,
+                                            int4 plan, int need, int before, int nfree, int32_t* status) {
+  if (plan.w & kCompactBad) return;
+  const int lane = threadIdx.x & 31, b = s / t.Hkv % t.B, first = plan.x, m = plan.y, n = plan.z;
+  int32_t* row = t.table + (size_t)s * t.maxp;
+  int32_t* to = w.newtab + (size_t)s * t.maxp;
+  const int pe = pages_of(m, g.lp);
+  if (need) {
+    int at = nfree - 1 - before;
+    bool lost = false;
+    for (int i0 = first >> g.lp; i0 < pe; i0 += 32) {
+      const int i = i0 + lane;
+      const bool want = i < pe && to[i] < 0;
+      const unsigned mask = __ballot_sync(kFull, want);
+      if (want) {
+        const int p = g.free_list[at - __popc(mask & ((1u << lane) - 1))];
+        if (page_ok(g, p))
+          to[i] = p;
+        else
+          lost = true;
+      }
+      at -= __popc(mask);
+    }
+    if (__any_sync(kFull, lost)) {  // a damaged free list: the stream is left alone
+      if (lane == 0) status_or(status, KVC_STATUS_BAD_PAGE);
+      return;
+    }
+    __syncwarp();
+  }
+  if (plan.w & kCompactMoves) {
+    accept_rows<D>(g, row, to, x.path + (size_t)b * x.T, n - x.drafts(b), first, m);
+    if (need)
+      for (int i = (first >> g.lp) + lane; i < pe; i += 32) {
+        const int old = row[i], p = to[i];
+        if (p != old) {
+          row[i] = p;
+          g.refs[p] = 1;
+          drop_page(g, w, old, nullptr);
+        }
+      }
+  }
+  for (int i = pe + lane; i < pages_of(n, g.lp); i += 32) {
+    drop_page(g, w, row[i], nullptr);
+    row[i] = -1;
+  }
+  if (lane == 0) t.len[s] = m;
+}
+
+constexpr int kAcceptWarps = 8;
+__global__ void __launch_bounds__(32 * kAcceptWarps) accept_plan_kernel(PoolGeom g, PageTab t, Paths x, int32_t* status,
+                                                                       PageWs w) {
+  griddep_launch();
+  griddep_wait();
+  const int s = blockIdx.x * kAcceptWarps + (threadIdx.x >> 5);
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    w.head[0] = *g.nfree;
+    w.head[1] = 0;
+  }
+  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < (g.npages + 31) / 32; i += gridDim.x * blockDim.x) w.gone[i] = 0u;
+  if (s < t.S) accept_plan(g, t, x, w, s, status);
+}
+
+// The pages that the streams before s take, and all: by 32 * kAcceptWarps threads.
+__device__ __forceinline__ void accept_needs(const PageWs& w, int S, int s0, int* sm, int* before, int* total) {
+  int b = 0, all = 0;
+  for (int i = threadIdx.x; i < S; i += 32 * kAcceptWarps) {
+    const int v = w.need[i];
+    all += v;
+    if (i < s0) b += v;
+  }
+  *before = *total = 0;
+  if (!__syncthreads_or(all)) return;  // nearly always
+  *total = block_sum(all, sm);
+  *before = block_sum(b, sm);
+}
+
+template <int D>
+__global__ void __launch_bounds__(32 * kAcceptWarps) accept_move_kernel(PoolGeom g, PageTab t, Paths x, int32_t* status,
+                                                                       PageWs w) {
+  __shared__ int sm[8];
+  griddep_launch();
+  griddep_wait();
+  const int s0 = blockIdx.x * kAcceptWarps, s = s0 + (threadIdx.x >> 5), nfree = w.head[0];
+  const int4 plan = s < t.S ? w.plan[s] : make_int4(0, 0, 0, kCompactBad);
+  int before, total;
+  accept_needs(w, t.S, s0, sm, &before, &total);
+  const bool none = total > 0 && (total > nfree || nfree > g.npages);
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    if (none) status_or(status, KVC_STATUS_NO_PAGES);
+    w.head[1] = none ? 0 : total;
+  }
+  if (none || s >= t.S) return;
+  if (total)
+    for (int i = s0; i < s; ++i) before += w.need[i];
+  accept_move<D>(g, t, x, w, s, plan, w.need[s], before, nfree, status);
+}
+
+// Up to kAcceptOne streams: a warp of the cluster has one.
+constexpr int kAcceptOne = kOneCtas * kOneThreads / 32;
+template <int D>
+__global__ void __cluster_dims__(kOneCtas, 1, 1) __launch_bounds__(kOneThreads)
+    accept_one_kernel(PoolGeom g, PageTab t, Paths x, int32_t* status, PageWs w) {
+  __shared__ int sm[kOneThreads / 32];
+  griddep_launch();
+  griddep_wait();
+  cg::cluster_group cl = cg::this_cluster();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, s = warp * kOneCtas + cl.block_rank(), nfree = *g.nfree;
+  cluster_zero(g, w, cl.block_rank() * kOneThreads + threadIdx.x);
+  if (s < t.S) accept_plan(g, t, x, w, s, status);
+  cl.sync();
+  // every stream's need, a thread each
+  const int v = (int)threadIdx.x < t.S ? __ldcg(&w.need[threadIdx.x]) : 0;
+  int before = 0, total = 0;
+  if (__syncthreads_or(v)) {  // hardly ever
+    int incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) sm[warp] = incl;
+    __syncthreads();
+    total = warp_sum_i(sm[lane]);
+    for (int i = 0; i < kOneThreads / 32; ++i)
+      if (i < (s >> 5)) before += sm[i];
+    if (s < t.S) {  // the streams before s in its group of 32
+      const int y = (s & ~31) + lane < s ? __ldcg(&w.need[(s & ~31) + lane]) : 0;
+      before += warp_sum_i(y);
+    }
+  }
+  const bool none = total > 0 && (total > nfree || nfree > g.npages);
+  if (cl.block_rank() == 0 && threadIdx.x == 0 && none) status_or(status, KVC_STATUS_NO_PAGES);
+  if (none) return;  // every CTA of the cluster alike
+  if (s < t.S) accept_move<D>(g, t, x, w, s, w.plan[s], w.need[s], before, nfree, status);
+  cl.sync();
+  cluster_push(cl, g, w, nfree - total);
+}
+
 bool one_fits(const PoolGeom& g, const PageTab& t, const PageTab& o) {
   return g.npages <= kOnePages && (long long)t.S * t.maxp <= kOneEntries && (long long)o.S * o.maxp <= kOneEntries &&
          t.B <= kOneSeqs && o.B <= kOneSeqs;
@@ -725,9 +1004,32 @@ int launch_page_free(const PoolGeom& g, const PageTab& t, const int32_t* drop, i
 
 int launch_page_slide(const PoolGeom& g, const PageTab& t, int window, int sinks, int32_t* gone, int32_t* status,
                       const PageWs& w, cudaStream_t s) {
+  const int first = (int)(((long long)sinks + (1 << g.lp) - 1) >> g.lp);
+  if (t.S <= kSlideOne && g.npages <= kOnePages)
+    return launch_pdl(slide_one_kernel, dim3(kOneCtas), dim3(kOneThreads), 0, s, false, g, t, window, first, gone, status,
+                      w) == cudaSuccess
+               ? KVC_OK
+               : KVC_ERR_LAUNCH;
   if (cudaMemsetAsync(w.head, 0, w.zero_bytes, s) != cudaSuccess) return KVC_ERR_LAUNCH;
-  if (launch_pdl(slide_kernel, dim3((t.S + 7) / 8), dim3(256), 0, s, false, g, t, window, sinks, gone, status, w) !=
+  const int per = 8 * kSlideStreams;
+  if (launch_pdl(slide_kernel, dim3((t.S + per - 1) / per), dim3(256), 0, s, false, g, t, window, first, gone, status, w) !=
       cudaSuccess)
+    return KVC_ERR_LAUNCH;
+  return page_push(g, w, s);
+}
+
+int launch_page_accept(const PoolGeom& g, const PageTab& t, int T, const int32_t* path, const int32_t* n_path,
+                       const int32_t* n_q, int32_t* status, const PageWs& w, cudaStream_t s) {
+  const Paths x{path, n_path, n_q, T};
+  if (t.S <= kAcceptOne && g.npages <= kOnePages)
+    return launch_pdl(g.D == 128 ? accept_one_kernel<128> : accept_one_kernel<64>, dim3(kOneCtas), dim3(kOneThreads), 0, s,
+                      false, g, t, x, status, w) == cudaSuccess
+               ? KVC_OK
+               : KVC_ERR_LAUNCH;
+  const dim3 grid((t.S + kAcceptWarps - 1) / kAcceptWarps), block(32 * kAcceptWarps);
+  if (launch_pdl(accept_plan_kernel, grid, block, 0, s, false, g, t, x, status, w) != cudaSuccess) return KVC_ERR_LAUNCH;
+  if (launch_pdl(g.D == 128 ? accept_move_kernel<128> : accept_move_kernel<64>, grid, block, 0, s, false, g, t, x, status,
+                 w) != cudaSuccess)
     return KVC_ERR_LAUNCH;
   return page_push(g, w, s);
 }
