@@ -634,8 +634,8 @@ __global__ void __launch_bounds__(kCombThreads) combine_kernel(AttendArgs a, Att
 }
 
 // The tcgen05 kernel's parts lie with the rows contiguous: a thread a row, 16 channels a CTA.
-template <typename T, int D, typename M>
-__global__ void __launch_bounds__(kTcRows) combine_tc_kernel(AttendArgs a, AttendPlan p, M seen) {
+template <typename T, int D, int ROWS, typename M>
+__global__ void __launch_bounds__(ROWS) combine_tc_kernel(AttendArgs a, AttendPlan p, M seen) {
   griddep_launch();
   griddep_wait();
   constexpr int C = 16, kPer = D / C;
@@ -656,10 +656,10 @@ __global__ void __launch_bounds__(kTcRows) combine_tc_kernel(AttendArgs a, Atten
       for (int i = 0; i < N; ++i) {
         const int c = min(c1 + i, span.y);
         const size_t slot = (size_t)c * 2 + (c == span.x ? 1 : 0);
-        ml[i] = p.ml[slot * kTcRows + rr];
-        const float* src = p.part + (slot * D + c0) * kTcRows + rr;
+        ml[i] = p.ml[slot * ROWS + rr];
+        const float* src = p.part + (slot * D + c0) * ROWS + rr;
 #pragma unroll
-        for (int e = 0; e < C; ++e) y[i][e] = src[e * kTcRows];
+        for (int e = 0; e < C; ++e) y[i][e] = src[e * ROWS];
       }
 #pragma unroll
       for (int i = 0; i < N; ++i) {
@@ -714,7 +714,7 @@ AttendPlan make_plan(const AttendArgs& a, const M& m, int parts, int sms, size_t
   const bool tc = parts == 1 && R >= kTcMin;
   p.unit = tc ? kTcUnit : kUnit;
   p.lead = tc ? kTcLead : kLead;
-  p.rb = tc ? kTcRows : 8 * nt;
+  p.rb = !tc ? 8 * nt : kPart<M> && R > kTcRows ? 2 * kTcRows : kTcRows;
   p.nrb = (R + p.rb - 1) / p.rb;
   p.nvs = a.t.S * p.nrb;
   p.by_nrb = FastDiv::make(p.nrb);
@@ -761,18 +761,25 @@ int run(const AttendArgs& a, const M& m, int sms, cudaStream_t s) {
   switch (p.rb / 8) {
     case 1: rc = go<T, D, 1, PARTS>(a, p, m, s); break;
     case 2: rc = go<T, D, 2, PARTS>(a, p, m, s); break;
-    case kTcRows / 8:
-      if constexpr (PARTS == 1) rc = launch_attend_tc(a, p, m, s);
-      break;
+    default:
+      if constexpr (PARTS == 1) {
+        if constexpr (kPart<M>)
+          rc = launch_attend_rows(a, p, m, s);
+        else
+          rc = launch_attend_tc(a, p, s);
+      }
   }
   if (rc || p.whole) return rc;
   const long long rows = (long long)p.nvs * p.rb;
   if constexpr (PARTS == 1)
-    if (p.rb == kTcRows)
-      return launch_pdl(combine_tc_kernel<T, D, M>, dim3((unsigned)(p.nvs * (D / 16))), dim3(kTcRows), 0, s, false, a, p,
-                        m) == cudaSuccess
+    if (p.rb >= kTcRows) {
+      auto k = combine_tc_kernel<T, D, kTcRows, M>;
+      if constexpr (kPart<M>)
+        if (p.rb > kTcRows) k = combine_tc_kernel<T, D, 2 * kTcRows, M>;
+      return launch_pdl(k, dim3((unsigned)(p.nvs * (D / 16))), dim3(p.rb), 0, s, false, a, p, m) == cudaSuccess
                  ? KVC_OK
                  : KVC_ERR_LAUNCH;
+    }
   return launch_pdl(combine_kernel<T, D, M>, dim3((unsigned)rows), dim3(kCombThreads), 0, s, false, a, p, m) == cudaSuccess
              ? KVC_OK
              : KVC_ERR_LAUNCH;

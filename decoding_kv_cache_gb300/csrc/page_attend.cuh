@@ -225,9 +225,9 @@ __device__ __noinline__ static bool mbar_wait_far(uint64_t* bar, uint32_t parity
   return mbar_wait_until(bar, parity, [] { return false; });
 }
 
-// The kernel for many query rows (tcgen05, 128 rows a block).
+// The kernels for many query rows (tcgen05): 128 rows a block, under SeenArgs 128 or 256.
 constexpr int kTcRows = 128, kTcUnit = 128;
-template <typename M>
-int launch_attend_tc(const AttendArgs& a, const AttendPlan& p, const M& m, cudaStream_t s);
+int launch_attend_tc(const AttendArgs& a, const AttendPlan& p, cudaStream_t s);
+int launch_attend_rows(const AttendArgs& a, const AttendPlan& p, const SeenArgs& m, cudaStream_t s);
 
 }  // namespace kvc

@@ -21,6 +21,7 @@
 // At a part's end the groups' O are merged and written (whole streams) or left for the combine kernel.
 // All waits are bounded; a role that gives up raises KVC_STATUS_TIMEOUT and the others follow.
 #include "page_attend.cuh"
+#include "page_attend_tc.cuh"
 #include "score_tc.cuh"
 
 namespace kvc {
@@ -47,71 +48,12 @@ struct Bars {
   uint64_t s_full[2], p_full[2][2], pv_done[2], q_full, merge, drain;  // p_full: S buffer, group (a group may be a unit ahead)
 };
 
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(tc::smem_u32(bar)) : "memory");
-}
-// The first poll in line, the waiting out of it (the roles' loops stay short: five warps of different roles
-// share an SM quarter's instruction cache). Gives up as soon as another role has.
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
-  if (mbar_wait_until(bar, parity, [&] { return *abort_flag != 0; })) return true;
-  if (!*abort_flag) status_or(status, KVC_STATUS_TIMEOUT);
-  *abort_flag = 1;
-  return false;
-}
-__device__ __forceinline__ bool elect_one() {
-  uint32_t e;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
-  return e;
-}
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
-
-// fp16 A and B, fp32 accumulator; b_mn: B lies with its N dimension contiguous
-__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
-  return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-// B operand with channels contiguous: 128-byte rows of 64 channels, a row per token, 8-token groups 1024
-// bytes apart (stride offset), the next 64 channels `next64` bytes on (leading offset)
-__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t next64) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(next64 >> 4) << 16;
-  d |= (uint64_t)(1024u >> 4) << 32;
-  d |= (uint64_t)1u << 46;
-  d |= (uint64_t)2u << 61;
-  return d;
-}
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  tc::umma_bf16(d, a, b, idesc, acc);  // kind::f16; the descriptor names the types
-}
-// A from tensor memory: lane = row, a 32-bit column two reduction elements
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc));
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
-
-// 16 columns of this thread's lane, without waiting
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
 // A token's codes and scales to a row of fp16 in the swizzled tile; zero: the row stands for nothing.
 // Lanes hold neighbouring tokens, whose 16-byte code vectors lie D/2 bytes apart: each lane begins at another
 // vector of its row, so that eight lanes' reads fall on eight different bank groups (with all lanes at the
 // same vector, four of them met on one: the shared memory, which the first product reads too, is what
 // bounds this kernel). Their stores, of different chunks, still differ in every chunk's low bits.
-template <int D, bool kNoNaN>
+template <int D>
 __device__ __forceinline__ void decode_row(const uint8_t* codes, const uint8_t* scales, uint8_t* tile, int j, bool zero) {
   constexpr int V = D / 32;  // code vectors of a row
   // the tile is 1024-byte aligned: 16-byte chunk c of row j lies at (row + (j & 7) 16) ^ c 16
@@ -121,8 +63,7 @@ __device__ __forceinline__ void decode_row(const uint8_t* codes, const uint8_t* 
     const int c = (q + (D == 128 ? j >> 1 : j >> 2)) & (V - 1);  // 32 channels: two scale groups, four chunks
     const uint4 w4 = reinterpret_cast<const uint4*>(codes)[c];
     const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-    uint32_t two = zero ? 0u : e4m3x2_f16x2(reinterpret_cast<const uint16_t*>(scales)[c]);
-    if constexpr (kNoNaN) two = no_nan2(two);
+    const uint32_t two = zero ? 0u : e4m3x2_f16x2(reinterpret_cast<const uint16_t*>(scales)[c]);
     const uint32_t s2[2] = {__byte_perm(two, two, 0x1010), __byte_perm(two, two, 0x3232)};
     const uint32_t at = (row ^ ((c & 1) << 6)) + (c >> 1) * Lay<D>::kHalf;
 #pragma unroll
@@ -136,29 +77,8 @@ __device__ __forceinline__ void decode_row(const uint8_t* codes, const uint8_t* 
   }
 }
 
-// Which of the 64 tokens from tok0 on row rr sees, `ok` telling the 16-token blocks that are there.
-__device__ __forceinline__ uint64_t below(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; }
-__device__ __noinline__ void row_bits(const AttendArgs& a, const AttendPlan& p, const SeenArgs& m, const Stream& x, int rr,
-                                      int lo, int hi, int tok0, uint32_t ok, uint32_t (&out)[2]) {
-  uint64_t v = (below(x.sinks - tok0) | ~below(lo - tok0)) & below(hi - tok0);
-  const int base = x.len - x.nq, u = tok0 - base;
-  if (m.mask && rr < x.rows && u > -64) {
-    const uint32_t* w = mask_words(a, p, m, x, x.r0 + rr);
-    auto word = [&](int i) { return i >= 0 && i < m.words ? (uint64_t)w[i] : 0ull; };
-    const int i = u >> 5, sh = u & 31;  // 64 bits from bit u on; bits before the first are the base's
-    uint64_t own = (word(i) | word(i + 1) << 32) >> sh;
-    if (sh) own |= word(i + 2) << (64 - sh);
-    v |= own & below(x.vis - tok0);
-  }
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t blocks = (ok >> 2 * h & 1 ? 0xffffu : 0u) | (ok >> (2 * h + 1) & 1 ? 0xffff0000u : 0u);
-    out[h] = (uint32_t)(v >> 32 * h) & blocks;
-  }
-}
-
-template <typename T, int D, typename M>
-__global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, AttendPlan p, M seen) {
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, AttendPlan p) {
   using L = Lay<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
@@ -196,14 +116,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
   griddep_wait();
   const int per = (p.nvs + kThreads - 1) / kThreads;
   int W;
-  int before = scan_units<kThreads>(a, p, seen, sm_scan, per, &W);
+  int before = scan_units<kThreads>(a, p, Causal{}, sm_scan, per, &W);
   const Split split(W, p.grid);
   const int w0 = split.first(blockIdx.x), w1 = split.first(blockIdx.x + 1);
   if (w0 >= w1) return;
   for (int i = 0; i < per; ++i) {
     const int vs = threadIdx.x * per + i;
     if (vs >= p.nvs) break;
-    const int u = cost_of(p, stream_of(a, p, seen, vs, false));
+    const int u = cost_of(p, stream_of(a, p, Causal{}, vs, false));
     if (before <= w0 && w0 < before + u) {
       sm_first[0] = vs;
       sm_first[1] = before;
@@ -224,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
   auto parts = [&](auto&& f) {
     int vs = sm_first[0], base = sm_first[1], left = w1 - w0, ca = w0 - base;
     for (int C; left > 0; ++vs, ca = 0, base += C) {
-      const Stream x = stream_of(a, p, seen, vs, false);
+      const Stream x = stream_of(a, p, Causal{}, vs, false);
       C = cost_of(p, x);
       if (C == 0) continue;
       const int cb = min(C, ca + left), ua = max(ca - p.lead, 0), ub = max(cb - p.lead, 0);
@@ -241,27 +161,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
       const int run = a.g.lp >= 7 ? 8 : 1 << (a.g.lp - 4);  // blocks that lie side by side
       auto id_of = [&](int u) {
         const int tok = u * kTcUnit + (lane & 7) * 16;
-        if constexpr (kPart<M>) return lane < 8 && u < ub && tok < x.vis ? row[x.real(tok) >> a.g.lp] : -1;
         return lane < 8 && lane % run == 0 && u < ub && tok < x.vis ? row[tok >> a.g.lp] : -1;
       };
       int id = id_of(ua);
       for (int u = ua; u < ub; ++u, ++n) {
         const int s = n % kRaw, tok = u * kTcUnit;
         const int nblk = min(8, (x.vis - tok + 15) >> 4);
-        bool lead = lane < nblk && lane % run == 0;
-        int cnt = lead ? min(run, nblk - lane) : 0;
-        int at = tok;  // of the lane's block in the stream's pages
-        if constexpr (kPart<M>) {  // a run ends with its page, and where tokens are left out
-          at = x.real(tok + (lane & 7) * 16);
-          lead = lane < nblk && (lane == 0 || (at & ((1 << a.g.lp) - 1)) == 0 || tok + lane * 16 == x.at);
-          const uint32_t heads = __ballot_sync(kFull, lead) | 1u << nblk;
-          cnt = lead ? __ffs(heads >> (lane + 1)) : 0;
-        }
+        const bool lead = lane < nblk && lane % run == 0;
+        const int cnt = lead ? min(run, nblk - lane) : 0;
         const bool ok = lead && page_ok(a.g, id);
         if (lead && !ok) status_or(a.status, KVC_STATUS_BAD_PAGE);
         const uint32_t bytes = __reduce_add_sync(kFull, ok ? cnt * blk_bytes(D) : 0);
         const uint32_t mask = __reduce_or_sync(kFull, ok ? ((1u << cnt) - 1) << lane : 0u);
-        const uint8_t* src = ok ? block_of(a.g, id, ((at & ((1 << a.g.lp) - 1)) >> 4)) : nullptr;
+        const uint8_t* src = ok ? block_of(a.g, id, ((tok & ((1 << a.g.lp) - 1)) >> 4)) : nullptr;
         id = id_of(u + 1);
         if (!wait(&bars.raw_empty[s], ((n / kRaw) & 1) ^ 1)) return false;
         if (lane == 0) {
@@ -343,9 +255,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
         const uint8_t* blk = smem + L::oRaw + s * L::kRawBytes + (j >> 4) * blk_bytes(D);
         // behind the last visible token lies anything: V rows of zero keep it out of 0 * NaN
         const bool zero = u * kTcUnit + j >= x.vis || !(ok >> (j >> 4) & 1);
-        decode_row<D, kPart<M>>(blk + (kv ? piece_off(D, 2) : 0) + (j & 15) * (D / 2),
-                                blk + (kv ? piece_off(D, 3) : piece_off(D, 1)) + (j & 15) * (D / 16),
-                                smem + (kv ? L::oV : L::oK) + t * L::kTile, j, zero);
+        decode_row<D>(blk + (kv ? piece_off(D, 2) : 0) + (j & 15) * (D / 2),
+                      blk + (kv ? piece_off(D, 3) : piece_off(D, 1)) + (j & 15) * (D / 16),
+                      smem + (kv ? L::oV : L::oK) + t * L::kTile, j, zero);
         if (kv == 0 && j == 0) unit_ok[n & 3] = ok;
         fence_async();
         __syncwarp();
@@ -402,18 +314,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.q_full);
       }
-      int lim = rr < x.rows ? seen_by(p, x, x.r0 + rr) : x.vis;
-      int minlim = seen_by(p, x, x.r0), lo = 0, maxlo = 0;
-      if constexpr (kPart<M>) {
-        if (rr < x.rows) {
-          const RowSeen y = row_seen(a, p, seen, x, x.r0 + rr);
-          lo = y.lo;
-          lim = y.hi;
-        }
-        const RowSeen y = all_see(p, seen, x);
-        maxlo = y.lo;
-        minlim = y.hi;
-      }
+      const int lim = rr < x.rows ? seen_by(p, x, x.r0 + rr) : x.vis;
+      const int minlim = seen_by(p, x, x.r0);
       float ref = 0.f, l = 0.f;
       bool none = true;
       // the query rows' factors were written before q_full, which precedes every s_full
@@ -425,12 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
         f = *reinterpret_cast<volatile float*>(&row_f[rr]);
         const int tok0 = (ua + i) * kTcUnit + w * kHalfTok;
         const uint32_t ok = *reinterpret_cast<volatile uint32_t*>(&unit_ok[n & 3]) >> (4 * w) & 0xf;
-        bool masked = tok0 + kHalfTok > minlim || ok != 0xf;
-        uint32_t vm[2];  // under SeenArgs, where masked: which of the tokens the row sees
-        if constexpr (kPart<M>) {
-          masked |= tok0 < maxlo && tok0 + kHalfTok > x.sinks;
-          if (masked) row_bits(a, p, seen, x, rr, lo, lim, tok0, ok, vm);
-        }
+        const bool masked = tok0 + kHalfTok > minlim || ok != 0xf;
         float mx = -INFINITY;
         {
           uint32_t r[2][32];
@@ -444,11 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
             float v[32];
 #pragma unroll
             for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[h][k]);
-            if (kPart<M> && masked) {
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (!(vm[h] >> k & 1)) v[k] = -INFINITY;
-            } else if (masked) {
+            if (masked) {
 #pragma unroll
               for (int k = 0; k < 32; ++k)
                 if (tok0 + 32 * h + k >= lim || !(ok >> (2 * h + (k >> 4)) & 1)) v[k] = -INFINITY;
@@ -493,16 +386,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
         uint32_t s0[16], s1[16];
         auto probabilities = [&](uint32_t (&v)[16], int c, auto with_mask) {
           uint32_t o[8];
-          const uint32_t see = kPart<M> && decltype(with_mask)::value ? vm[c >> 1] >> 16 * (c & 1) : 0u;
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             float2 y = fma2(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), f2, ref2);
             y.x = ex2(y.x);
             y.y = ex2(y.y);
-            if constexpr (kPart<M> && decltype(with_mask)::value) {
-              if (!(see >> 2 * k & 1)) y.x = 0.f;
-              if (!(see >> (2 * k + 1) & 1)) y.y = 0.f;
-            } else if constexpr (decltype(with_mask)::value) {
+            if constexpr (decltype(with_mask)::value) {
               const bool blk = ok >> c & 1;
               if (tok0 + 16 * c + 2 * k >= lim || !blk) y.x = 0.f;
               if (tok0 + 16 * c + 2 * k + 1 >= lim || !blk) y.y = 0.f;
@@ -632,22 +521,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
   if (warp == 17) tc::tmem_dealloc(tmem, kTmemCols);
 }
 
-template <typename T, int D, typename M>
-int go(const AttendArgs& a, const AttendPlan& p, const M& m, cudaStream_t s) {
-  auto k = attend_tc_kernel<T, D, M>;
+template <typename T, int D>
+int go(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
+  auto k = attend_tc_kernel<T, D>;
   if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::bytes) != cudaSuccess)
     return KVC_ERR_LAUNCH;
-  return launch_pdl(k, dim3(p.grid), dim3(kThreads), Lay<D>::bytes, s, false, a, p, m) == cudaSuccess ? KVC_OK
-                                                                                                      : KVC_ERR_LAUNCH;
+  return launch_pdl(k, dim3(p.grid), dim3(kThreads), Lay<D>::bytes, s, false, a, p) == cudaSuccess ? KVC_OK
+                                                                                                   : KVC_ERR_LAUNCH;
 }
 
 }  // namespace
 
-template <typename M>
-int launch_attend_tc(const AttendArgs& a, const AttendPlan& p, const M& m, cudaStream_t s) {
-  return a.g.D == 128 ? go<__nv_bfloat16, 128>(a, p, m, s) : go<__nv_bfloat16, 64>(a, p, m, s);
+int launch_attend_tc(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
+  return a.g.D == 128 ? go<__nv_bfloat16, 128>(a, p, s) : go<__nv_bfloat16, 64>(a, p, s);
 }
-template int launch_attend_tc<Causal>(const AttendArgs&, const AttendPlan&, const Causal&, cudaStream_t);
-template int launch_attend_tc<SeenArgs>(const AttendArgs&, const AttendPlan&, const SeenArgs&, cudaStream_t);
 
 }  // namespace kvc
