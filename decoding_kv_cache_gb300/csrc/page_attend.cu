@@ -648,7 +648,9 @@ __global__ void __launch_bounds__(ROWS) combine_tc_kernel(AttendArgs a, AttendPl
 #pragma unroll
   for (int e = 0; e < C; ++e) o[e] = 0.f;
   if (x.vis && !given_up) {
-    constexpr int N = 4;  // parts whose reads are in flight at once
+    // parts whose reads are in flight at once; blocks of 256 rows come in numbers, in few parts each, and more of their
+    // CTAs fit an SM with fewer registers
+    constexpr int N = ROWS > kTcRows ? 2 : 4;
     for (int c1 = span.x; c1 <= span.y; c1 += N) {
       float2 ml[N];
       float y[N][C];

@@ -7,10 +7,10 @@
 // of it); a probability is rounded to fp16 once, 2^-11 relative against the bf16 output's 2^-8.
 //
 //   decoders               a part's query rows to fp16; then half of the warps K, half V: codes and scales from global memory
-//                          straight to registers, two units ahead, four lanes a token, and as fp16 into the
+//                          straight to registers ahead of time, four lanes a token, and as fp16 into the
 //                          128-byte-swizzled tiles (two stages each). V's tile [token][channel] is the second
 //                          product's B operand as it lies (MN-major).
-//   issuer   (one warp)     the products
+//   issuers                 the products
 //   softmax  (warps 0-7)   two groups, a thread a row. RT = 2: a row tile each. While one group's tile is in its
 //                          softmax the tensor cores work on the other's: P V of a unit, then Q K of the next into the
 //                          same columns. RT = 1: a unit's first and last 64 tokens each, with their own O, reference and
@@ -42,11 +42,11 @@ struct Roles<1> {  // 896 threads with 72 registers (64512): 2 x 128 x 120 + 4 x
   static constexpr int kSoft = 8, kDec = 16, kSoftRegs = 120, kDecRegs = 56, kIssueRegs = 32;
 };
 template <>
-struct Roles<2> {  // 640 threads with 96 registers (61440): 2 x 128 x 128 + 2 x 128 x 88 + 128 x 40 = 60416
-  static constexpr int kSoft = 8, kDec = 8, kSoftRegs = 128, kDecRegs = 88, kIssueRegs = 40;
+struct Roles<2> {  // 640 threads with 96 registers (61440): 2 x 128 x 144 + 2 x 128 x 72 + 128 x 48 = 61440
+  static constexpr int kSoft = 8, kDec = 8, kSoftRegs = 144, kDecRegs = 72, kIssueRegs = 48;
 };
 template <int RT>
-constexpr int kThreadsOf = 32 * (Roles<RT>::kSoft + Roles<RT>::kDec + 4);  // the issuer's warpgroup has three idle warps
+constexpr int kThreadsOf = 32 * (Roles<RT>::kSoft + Roles<RT>::kDec + 4);  // the issuers' warpgroup is not filled
 template <int kRegs>
 __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegs));
@@ -69,10 +69,12 @@ struct Lay {
 };
 
 struct Bars {
-  uint64_t k_full[kTiles], k_empty[kTiles], v_full[kTiles], v_empty[kTiles];
-  uint64_t s_full[2];     // RT = 1: by S buffer; 2: by row tile
-  uint64_t p_full[2][2];  // RT = 1: by S buffer and group (a group may be a unit ahead); 2: [0][row tile]
-  uint64_t pv_done[2], q_full, q_empty, merge, drain;
+  uint64_t k_full[kTiles], v_full[kTiles], v_empty[kTiles];
+  // RT = 1: by S buffer, which is the tile's stage; 2: of the first row tile, and of the second by the stage. The last one
+  // over K's tile says that it is free.
+  uint64_t s_full[3], p_full[2];
+  uint64_t pv_done[2];  // RT = 2: a part's last P V, by row tile
+  uint64_t q_full, q_empty, merge, drain;
 };
 
 // A decoder lane's share of a unit: V vectors of 16 bytes of codes and their two scales each.
@@ -117,7 +119,8 @@ template <typename T, int D, int RT>
 __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendArgs a, AttendPlan p, SeenArgs seen) {
   using L = Lay<D, RT>;
   constexpr int kRows = RT * 128, kThreads = kThreadsOf<RT>;
-  constexpr int kSoftWarps = Roles<RT>::kSoft, kDecWarps = Roles<RT>::kDec, kIssuer = kSoftWarps + kDecWarps;
+  constexpr int kSoftWarps = Roles<RT>::kSoft, kDecWarps = Roles<RT>::kDec;
+  constexpr int kIssuer = kSoftWarps + kDecWarps, kIssuers = RT == 1 ? 2 : 1;  // first warp, warps
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   __shared__ Bars bars;
@@ -134,18 +137,17 @@ __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendAr
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&bars.k_full[i], kDecWarps / 2);
       tc::mbar_init(&bars.v_full[i], kDecWarps / 2);
-      tc::mbar_init(&bars.k_empty[i], 1);
       tc::mbar_init(&bars.v_empty[i], 1);
       // test-only fault (kvc_debug_fault 2): a wait of the first CTA is for an arrival that nothing makes
       tc::mbar_init(&bars.s_full[i], a.fault && blockIdx.x == 0 && i == 1 ? 2 : 1);
+      tc::mbar_init(&bars.s_full[2], 1);
       tc::mbar_init(&bars.pv_done[i], 1);
-      tc::mbar_init(&bars.p_full[i][0], 4);
-      tc::mbar_init(&bars.p_full[i][1], 4);
+      tc::mbar_init(&bars.p_full[i], kSoftWarps / RT);
     }
     tc::mbar_init(&bars.q_full, kDecWarps);
     tc::mbar_init(&bars.q_empty, 1);
     tc::mbar_init(&bars.merge, kSoftWarps);
-    tc::mbar_init(&bars.drain, 1);
+    tc::mbar_init(&bars.drain, kIssuers);
     tc::mbar_fence_init();
   }
   griddep_wait();
@@ -201,13 +203,18 @@ __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendAr
 
   if (warp >= kIssuer) {
     regs_down<Roles<RT>::kIssueRegs>();
-    if (warp == kIssuer) {
-    // ---- issuer --------------------------------------------------------------------------------
-    // the whole warp walks the loop, so that addresses stay in uniform registers; one lane issues
+    if (warp < kIssuer + kIssuers) {
+    // ---- issuers -------------------------------------------------------------------------------
+    // A product costs some 50 cycles to issue and a wait or commit 100 to 300, so there are as few of those as can be. A
+    // warp's products run in the order of their issue, which is all that keeps Q K from overwriting a P. RT = 1: two
+    // warps share the work; one issues Q K, into a buffer of S once P V has read the last P in it, the other P V (one warp
+    // for both: 134 us and not 131 for 16 x 5 rows over 8 x 8 x 32768 tokens). RT = 2: one (a warp a row tile: 112 us and not 96 for a
+    // prompt's 1024 tokens). The whole warp walks the loop, so that addresses stay in uniform registers; one lane issues.
     constexpr uint32_t id_qk = idesc_f16(128, kTcUnit, false), id_pv = idesc_f16(128, D, true);
     const uint64_t dq = tc::desc_k_sw128(tc::smem_u32(smem)), dk = tc::desc_k_sw128(tc::smem_u32(smem + L::oK)),
                    dv = desc_mn_sw128(tc::smem_u32(smem + L::oV), L::kHalf);
     const bool leader = elect_one();
+    const int iw = warp - kIssuer;
     uint32_t nk = 0, nv = 0, seg = 0;
     auto qk = [&](uint32_t cols, int tile, int t) {  // S of row tile `tile` with the keys of stage t
       const uint64_t q = dq + (uint64_t)(tile * (L::kTile >> 4)), d = dk + (uint64_t)(t * (L::kTile >> 4));
@@ -232,63 +239,49 @@ __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendAr
           if (i > 0 && !wait(&bars.v_full[tv], (nv >> 1) & 1)) return false;
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
-            if (i > 0) {
-              if (!wait(&bars.p_full[0][w], nv & 1)) return false;
-              tc::fence_after_sync();
-              if (leader) {
+            if (i > 0 && !wait(&bars.p_full[w], nv & 1)) return false;
+            if (w == 0 && i < m && !wait(&bars.k_full[tk], (nk >> 1) & 1)) return false;
+            tc::fence_after_sync();
+            if (leader) {
+              if (i > 0) {
                 pv(kColO + w * 128, w * 128, 0, kTcUnit, tv, i > 1);
-                tc::umma_commit(&bars.pv_done[w]);
                 if (w == 1) tc::umma_commit(&bars.v_empty[tv]);
+                if (i == m) tc::umma_commit(&bars.pv_done[w]);
               }
-              __syncwarp();
-            }
-            if (i < m) {
-              if (w == 0 && !wait(&bars.k_full[tk], (nk >> 1) & 1)) return false;
-              tc::fence_after_sync();
-              if (leader) {
+              if (i < m) {
                 qk(w * 128, w, tk);
-                tc::umma_commit(&bars.s_full[w]);
-                if (w == 1) tc::umma_commit(&bars.k_empty[tk]);
+                tc::umma_commit(w == 0 ? &bars.s_full[0] : &bars.s_full[1 + tk]);
                 if (w == 1 && i == m - 1) tc::umma_commit(&bars.q_empty);
               }
-              __syncwarp();
             }
+            __syncwarp();
           }
           if (i > 0) ++nv;
           if (i < m) ++nk;
         }
+      } else if (iw == 0) {
+        for (int i = 0; i < m; ++i, ++nk) {
+          const int t = nk & 1;
+          if (!wait(&bars.k_full[t], (nk >> 1) & 1) || !wait(&bars.v_empty[t], ((nk >> 1) & 1) ^ 1)) return false;
+          tc::fence_after_sync();
+          if (leader) {
+            qk(t * 128, 0, t);
+            tc::umma_commit(&bars.s_full[t]);
+            if (i == m - 1) tc::umma_commit(&bars.q_empty);
+          }
+          __syncwarp();
+        }
       } else {
-        for (int i = 0; i <= m; ++i) {
-          if (i < m) {
-            const int t = nk & 1;
-            if (!wait(&bars.k_full[t], (nk >> 1) & 1)) return false;
-            tc::fence_after_sync();
-            if (leader) {
-              qk(t * 128, 0, t);
-              tc::umma_commit(&bars.k_empty[t]);
-              tc::umma_commit(&bars.s_full[t]);
-              if (i == m - 1) tc::umma_commit(&bars.q_empty);
-            }
-            __syncwarp();
-            ++nk;
-          }
-          if (i > 0) {
-            const int t = nv & 1;
-            if (!wait(&bars.v_full[t], (nv >> 1) & 1)) return false;
+        for (int i = 0; i < m; ++i, ++nv) {
+          const int t = nv & 1;
+          if (!wait(&bars.v_full[t], (nv >> 1) & 1) || !wait(&bars.p_full[t], (nv >> 1) & 1)) return false;
+          tc::fence_after_sync();
+          if (leader) {
 #pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              if (!wait(&bars.p_full[t][w], (nv >> 1) & 1)) return false;
-              tc::fence_after_sync();
-              if (leader) {
-                pv(kColO + w * 128, t * 128 + w * kStep, w * kStep, kStep, t, i > 1);
-                tc::umma_commit(&bars.pv_done[w]);
-              }
-              __syncwarp();
-            }
-            if (leader) tc::umma_commit(&bars.v_empty[t]);
-            __syncwarp();
-            ++nv;
+            for (int w = 0; w < 2; ++w) pv(kColO + w * 128, t * 128 + w * kStep, w * kStep, kStep, t, i > 0);
+            tc::umma_commit(&bars.v_empty[t]);
           }
+          __syncwarp();
         }
       }
       return true;
@@ -301,7 +294,7 @@ __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendAr
     using Sh = Share<D, kTokens>;
     const int dw = warp - kSoftWarps, kv = dw / kPer, wd = dw % kPer;  // K or V; tokens of the unit
     uint64_t* full = kv ? bars.v_full : bars.k_full;
-    uint64_t* empty = kv ? bars.v_empty : bars.k_empty;
+    uint64_t* empty = kv ? bars.v_empty : &bars.s_full[RT - 1];
     // Lane l has 32 channels, chunk c of a row, of tokens r + kTok * i: a warp's loads are contiguous. Its four 16-byte
     // stores of a vector go chunk by chunk; with c & 2 in another order, so that eight lanes' stores fall on different
     // banks (their rows' chunks c and c + 2 lie a multiple of 128 bytes apart).
@@ -385,10 +378,11 @@ __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendAr
         ++n;
         return true;
       };
+      // rows two units ahead of their decoding, one for RT = 2, whose units take twice as long
       Sh v0, v1;
       uint32_t ok0 = 0, ok1 = 0;
       load(v0, ok0, ua);
-      load(v1, ok1, ua + 1);
+      if (RT == 1) load(v1, ok1, ua + 1);
       {
         // the query rows, each brought to [256, 512) by a power of two, with the scale's sign, so that maxima of dot
         // products are maxima of logits. D/8 lanes take a row.
@@ -432,10 +426,10 @@ __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendAr
         if (lane == 0) mbar_arrive(&bars.q_full);
       }
       ++seg;
-      for (int u = ua; u < ub; u += 2) {
+      for (int u = ua; u < ub; u += RT == 1 ? 2 : 1) {
         if (!decode(v0, ok0)) return false;
-        load(v0, ok0, u + 2);
-        if (u + 1 < ub) {
+        load(v0, ok0, u + (RT == 1 ? 2 : 1));
+        if (RT == 1 && u + 1 < ub) {
           if (!decode(v1, ok1)) return false;
           load(v1, ok1, u + 3);
         }
@@ -462,7 +456,7 @@ __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendAr
       bool none = true, fresh = true;  // the row has seen no token; one of the warp's rows has not
       for (int i = 0; i < m; ++i, ++n) {
         const uint32_t tS = tmem + lanes + (RT == 2 ? w * 128 : (n & 1) * 128 + w * kStep);
-        if (!wait(&bars.s_full[RT == 2 ? w : n & 1], RT == 2 ? n & 1 : (n >> 1) & 1)) return false;
+        if (!(RT == 2 && w == 0 ? wait(&bars.s_full[0], n & 1) : wait(&bars.s_full[RT - 1 + (n & 1)], (n >> 1) & 1))) return false;
         tc::fence_after_sync();
         // the factors were written before q_full, which precedes every s_full
         if (i == 0) f = *reinterpret_cast<volatile float*>(&row_f[seg & 1][rr]);
@@ -474,58 +468,61 @@ __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendAr
           const uint32_t by = *reinterpret_cast<volatile uint32_t*>(&unit_ok[n & 3]);  // two a byte
           blocks = by * 0x01041040u >> 24;
         }
-#pragma unroll 1
+        // every row sees every token, and nearly always the reference holds: one straight run, the next chunk's logits on
+        // their way
+        uint32_t s[2][32];
+        tc::tmem_ld32_async(tS, s[0]);
+        if (RT == 1) tc::tmem_ld32_async(tS + kChunk, s[1]);
+#pragma unroll
         for (int h = 0; h < RT; ++h) {
           const int part = RT == 2 ? h : w, tok0 = (ua + i) * kTcUnit + part * kStep;
           const uint32_t ok = blocks >> 4 * part & 15;
           bool slow = fresh || ok != 15 || tok0 + kStep > all.hi || (tok0 < all.lo && tok0 + kStep > x.sinks);
+          const float2 f2 = make_float2(f, f), ref2 = make_float2(-ref, -ref);
+          uint32_t o[2][16];
+          float l2[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            if (RT == 2 || e == 0) tc::tmem_wait();
+            tc::tmem_regs_ready(s[e]);
+            if (RT == 2 && 2 * h + e < 3) tc::tmem_ld32_async(tS + (2 * h + e + 1) * kChunk, s[e ^ 1]);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              float2 y = fma2(make_float2(__uint_as_float(s[e][2 * k]), __uint_as_float(s[e][2 * k + 1])), f2, ref2);
+              y.x = ex2(y.x);
+              y.y = ex2(y.y);
+              sum[k & 1] = add2(sum[k & 1], y);
+              o[e][k] = pack2(y.x, y.y);
+            }
+            sum[0] = add2(sum[0], sum[1]);
+            l2[e] = sum[0].x + sum[0].y;
+          }
+          slow = __any_sync(kFull, slow || !(l2[0] <= kMost && l2[1] <= kMost));
           if (!slow) {
-            // every row sees every token, and nearly always the reference holds: one straight run
-            uint32_t s[2][32];
-            tc::tmem_ld32_async(tS + h * kStep, s[0]);
-            tc::tmem_ld32_async(tS + h * kStep + 32, s[1]);
-            tc::tmem_wait();
-            tc::tmem_regs_ready(s[0]);
-            tc::tmem_regs_ready(s[1]);
-            const float2 f2 = make_float2(f, f), ref2 = make_float2(-ref, -ref);
-            float2 sum[2][2];
-            uint32_t o[2][16];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              sum[e][0] = sum[e][1] = make_float2(0.f, 0.f);
-#pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                float2 y = fma2(make_float2(__uint_as_float(s[e][2 * k]), __uint_as_float(s[e][2 * k + 1])), f2, ref2);
-                y.x = ex2(y.x);
-                y.y = ex2(y.y);
-                sum[e][k & 1] = add2(sum[e][k & 1], y);
-                o[e][k] = pack2(y.x, y.y);
-              }
-              sum[e][0] = add2(sum[e][0], sum[e][1]);
-            }
-            const float l0 = sum[0][0].x + sum[0][0].y, l1 = sum[1][0].x + sum[1][0].y;
-            slow = __any_sync(kFull, !(l0 <= kMost && l1 <= kMost));
-            if (!slow) {
-              l += l0 + l1;
-              tmem_st16(tS + h * (kStep / 2), o[0]);
-              tmem_st16(tS + h * (kStep / 2) + 16, o[1]);
-            }
+            l += l2[0] + l2[1];
+            tmem_st16(tS + h * (kStep / 2), o[0]);
+            tmem_st16(tS + h * (kStep / 2) + 16, o[1]);
           }
           if (__builtin_expect(slow, 0)) {
+            if (h + 1 < RT) {  // the load under way is over before anything else has the registers
+              tc::tmem_wait();
+              tc::tmem_regs_ready(s[0]);
+            }
             // A chunk at a time: what the row sees of it, its maximum, the reference raised where that passes it by more
             // than kOff, what was summed so far rescaled, and the probabilities.
 #pragma unroll 1
             for (int e = 0; e < 2; ++e) {
               const int c = 2 * h + e;  // of the unit's chunks in this group's columns
               const uint32_t bits = row_bits(a, p, seen, x, rr, lo, lim, tok0 + e * kChunk, ok >> 2 * e);
-              uint32_t s[32];
-              tc::tmem_ld32_async(tS + c * kChunk, s);
+              uint32_t z[32];
+              tc::tmem_ld32_async(tS + c * kChunk, z);
               tc::tmem_wait();
-              tc::tmem_regs_ready(s);
+              tc::tmem_regs_ready(z);
               float y[32], mx = -INFINITY;
 #pragma unroll
               for (int k = 0; k < 32; ++k) {
-                y[k] = bits >> k & 1 ? fmaf(__uint_as_float(s[k]), f, -ref) : -INFINITY;
+                y[k] = bits >> k & 1 ? fmaf(__uint_as_float(z[k]), f, -ref) : -INFINITY;
                 mx = fmaxf(mx, y[k]);
               }
               float up = 0.f, down = 1.f;
@@ -538,7 +535,7 @@ __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendAr
               }
               if (__any_sync(kFull, down != 1.f)) {
                 // O holds the part's earlier units, and P this one's earlier chunks
-                if (RT == 1 && i > 0 && !wait(&bars.pv_done[w], (n - 1) & 1)) return false;
+                if (RT == 1 && i > 0 && !wait(&bars.v_empty[(n - 1) & 1], ((n - 1) >> 1) & 1)) return false;
                 tmem_st_wait();
                 tc::fence_after_sync();
                 if (i > 0)
@@ -562,13 +559,11 @@ __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendAr
         }
         tmem_st_wait();
         tc::fence_before_sync();
-        // The part's end waits for this unit's P V, and a wait for a phase's parity tells it from the phase before only
-        // once that is over: the P V before is waited for here, while this one cannot be (RT = 2: S came behind it).
-        if (RT == 1 && i > 0 && i == m - 1 && !wait(&bars.pv_done[w], (n - 1) & 1)) return false;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.p_full[RT == 2 ? 0 : n & 1][w]);
+        if (lane == 0) mbar_arrive(&bars.p_full[RT == 2 ? w : n & 1]);
       }
-      if (!wait(&bars.pv_done[w], (n - 1) & 1)) return false;
+      // the last product is done (RT = 1: the one two units before was, or S would not have been written)
+      if (!(RT == 2 ? wait(&bars.pv_done[w], seg & 1) : wait(&bars.v_empty[(n - 1) & 1], ((n - 1) >> 1) & 1))) return false;
       tc::fence_after_sync();
       const bool whole = ua == 0 && ub == U;
       if (ua == 0 && threadIdx.x == 0)
@@ -657,7 +652,7 @@ __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendAr
       return true;
     });
     // products under way end before their memory goes
-    if (warp == kIssuer) {
+    if (warp >= kIssuer && warp < kIssuer + kIssuers) {
       if (elect_one()) tc::umma_commit(&bars.drain);  // the lane that issued the products
       __syncwarp();
       const uint64_t since = clock_ns();
