@@ -106,10 +106,10 @@ __device__ __forceinline__ const uint32_t* mask_words(const AttendArgs& a, const
 __device__ __forceinline__ int units_of(const AttendPlan& p, const Stream& x) { return (x.vis + p.unit - 1) / p.unit; }
 __device__ __forceinline__ int cost_of(const AttendPlan& p, const Stream& x) { return x.vis ? units_of(p, x) + p.lead : 0; }
 
-// Cost, in units, before each thread's run of streams and in all (block of kThr threads; every thread calls).
+// Cost, in units, before each thread's run of streams, of it (own) and in all (block of kThr threads; every thread calls).
 template <int kThr, typename M>
 __device__ __forceinline__ int scan_units(const AttendArgs& a, const AttendPlan& p, const M& m, int* sm, int per,
-                                          int* total) {
+                                          int* total, int* own = nullptr) {
   int mine = 0;
   for (int i = 0; i < per; ++i) {
     const int vs = threadIdx.x * per + i;
@@ -131,6 +131,7 @@ __device__ __forceinline__ int scan_units(const AttendArgs& a, const AttendPlan&
     all += v;
   }
   *total = all;
+  if (own) *own = mine;
   return base + incl - mine;
 }
 

@@ -6,7 +6,7 @@
 // fp16 by a power of two per row (bf16 values exact from 2^-25 of the row's largest on, below that off by at most 2^-33
 // of it); a probability is rounded to fp16 once, 2^-11 relative against the bf16 output's 2^-8.
 //
-//   decoders               a part's query rows to fp16; then half of the warps K, half V: codes and scales from global memory
+//   decoders               a part's query rows to fp16 (the first part's are the softmax warps' work); then half of the warps K, half V: codes and scales from global memory
 //                          straight to registers ahead of time, four lanes a token, and as fp16 into the
 //                          128-byte-swizzled tiles (two stages each). V's tile [token][channel] is the second
 //                          product's B operand as it lies (MN-major).
@@ -153,14 +153,15 @@ __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendAr
   griddep_wait();
   const int per = (p.nvs + kThreads - 1) / kThreads;
   int W;
-  int before = scan_units<kThreads>(a, p, seen, sm_scan, per, &W);
+  int mine;
+  int before = scan_units<kThreads>(a, p, seen, sm_scan, per, &W, &mine);
   const Split split(W, p.grid);
   const int w0 = split.first(blockIdx.x), w1 = split.first(blockIdx.x + 1);
   if (w0 >= w1) return;
   for (int i = 0; i < per && before <= w0; ++i) {
     const int vs = threadIdx.x * per + i;
     if (vs >= p.nvs) break;
-    const int u = cost_of(p, stream_of(a, p, seen, vs, false));
+    const int u = per == 1 ? mine : cost_of(p, stream_of(a, p, seen, vs, false));
     if (w0 < before + u) {
       sm_first[0] = vs;
       sm_first[1] = before;
@@ -199,6 +200,51 @@ __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendAr
       left -= cb - ca;
       if (ub > ua && !f(x, vs, ua, ub, C - p.lead, base + p.lead)) return;
     }
+  };
+
+  using std::integral_constant;
+  // A part's query rows, by warp `by` of `of`: each is brought to [256, 512) by a power of two, with the scale's sign, so that
+  // maxima of dot products are maxima of logits. D/8 lanes take a row.
+  auto queries = [&](const Stream& x, uint32_t seg, int by, auto of) {
+    constexpr int kLanes = D / 8, kAt = 32 / kLanes, kQRows = kRows / decltype(of)::value;
+    constexpr int kBatch = kQRows / kAt < 4 ? kQRows / kAt : 4;
+    const int i = lane % kLanes;
+#pragma unroll 1
+    for (int g0 = 0; g0 < kQRows; g0 += kBatch * kAt) {
+      const int q0 = by * kQRows + g0 + lane / kLanes;
+      uint4 v[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int q = q0 + k * kAt;
+        v[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (q < x.rows)
+          v[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + q_row(a, p, x, x.r0 + q)) + i);
+      }
+      // the products on the part before read its queries no more
+      if (g0 == 0 && seg > 0 && !wait(&bars.q_empty, (seg - 1) & 1)) return false;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int q = q0 + k * kAt;
+        const T* e = reinterpret_cast<const T*>(&v[k]);
+        float mx = 0.f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) mx = fmaxf(mx, fabsf(to_f32(e[c])));
+#pragma unroll
+        for (int c = kLanes / 2; c; c >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, c));
+        const int ex = max((int)(__float_as_uint(mx) >> 23), 24);
+        const float mul = copysignf(__uint_as_float((uint32_t)(262 - ex) << 23), a.scale);
+        if (i == 0) row_f[seg & 1][q] = __uint_as_float((uint32_t)(ex - 8) << 23) * (fabsf(a.scale) * kLog2e);
+        uint32_t o[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[c] = pack2(to_f32(e[2 * c]) * mul, to_f32(e[2 * c + 1]) * mul);
+        *reinterpret_cast<uint4*>(smem + (q >> 7) * L::kTile + (i >> 3) * L::kHalf + (q & 127) * 128 +
+                                  (((i & 7) ^ (q & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+    fence_async();
+    __syncwarp();
+    if (lane < kDecWarps / decltype(of)::value) mbar_arrive(&bars.q_full);  // as many arrivals by either role
+    return true;
   };
 
   if (warp >= kIssuer) {
@@ -383,48 +429,7 @@ __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendAr
       uint32_t ok0 = 0, ok1 = 0;
       load(v0, ok0, ua);
       if (RT == 1) load(v1, ok1, ua + 1);
-      {
-        // the query rows, each brought to [256, 512) by a power of two, with the scale's sign, so that maxima of dot
-        // products are maxima of logits. D/8 lanes take a row.
-        constexpr int kLanes = D / 8, kAt = 32 / kLanes, kQRows = kRows / kDecWarps;
-        constexpr int kBatch = kQRows / kAt < 4 ? kQRows / kAt : 4;
-        const int i = lane % kLanes;
-#pragma unroll 1
-        for (int g0 = 0; g0 < kQRows; g0 += kBatch * kAt) {
-          const int q0 = dw * kQRows + g0 + lane / kLanes;
-          uint4 v[kBatch];
-#pragma unroll
-          for (int k = 0; k < kBatch; ++k) {
-            const int q = q0 + k * kAt;
-            v[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (q < x.rows)
-              v[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + q_row(a, p, x, x.r0 + q)) + i);
-          }
-          // the products on the part before read its queries no more
-          if (g0 == 0 && seg > 0 && !wait(&bars.q_empty, (seg - 1) & 1)) return false;
-#pragma unroll
-          for (int k = 0; k < kBatch; ++k) {
-            const int q = q0 + k * kAt;
-            const T* e = reinterpret_cast<const T*>(&v[k]);
-            float mx = 0.f;
-#pragma unroll
-            for (int c = 0; c < 8; ++c) mx = fmaxf(mx, fabsf(to_f32(e[c])));
-#pragma unroll
-            for (int c = kLanes / 2; c; c >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, c));
-            const int ex = max((int)(__float_as_uint(mx) >> 23), 24);
-            const float mul = copysignf(__uint_as_float((uint32_t)(262 - ex) << 23), a.scale);
-            if (i == 0) row_f[seg & 1][q] = __uint_as_float((uint32_t)(ex - 8) << 23) * (fabsf(a.scale) * kLog2e);
-            uint32_t o[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) o[c] = pack2(to_f32(e[2 * c]) * mul, to_f32(e[2 * c + 1]) * mul);
-            *reinterpret_cast<uint4*>(smem + (q >> 7) * L::kTile + (i >> 3) * L::kHalf + (q & 127) * 128 +
-                                      (((i & 7) ^ (q & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-          }
-        }
-        fence_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.q_full);
-      }
+      if (seg > 0 && !queries(x, seg, dw, integral_constant<int, kDecWarps>())) return false;  // the first part's are the softmax warps' work
       ++seg;
       for (int u = ua; u < ub; u += RT == 1 ? 2 : 1) {
         if (!decode(v0, ok0)) return false;
@@ -445,11 +450,17 @@ __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendAr
     uint32_t n = 0, seg = 0;  // units so far
     parts([&](const Stream& x, int vs, int ua, int ub, int U, int base) {
       const int m = ub - ua;
+      if (seg == 0 && !queries(x, 0, warp, integral_constant<int, kSoftWarps>())) return false;
       int lim = x.vis, lo = 0;
       if (rr < x.rows) {
         const RowSeen y = row_seen(a, p, seen, x, x.r0 + rr);
         lo = y.lo;
         lim = y.hi;
+        if (seen.mask) {  // for the units with the own tokens, the part's last
+          const uint32_t* words = mask_words(a, p, seen, x, x.r0 + rr);
+          asm volatile("prefetch.global.L1 [%0];\n" ::"l"(words));
+          asm volatile("prefetch.global.L1 [%0];\n" ::"l"(words + seen.words - 1));
+        }
       }
       const RowSeen all = all_see(p, seen, x);
       float ref = 0.f, l = 0.f, f = 0.f;
@@ -519,12 +530,13 @@ __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendAr
               tc::tmem_ld32_async(tS + c * kChunk, z);
               tc::tmem_wait();
               tc::tmem_regs_ready(z);
-              float y[32], mx = -INFINITY;
+              float y[32], m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
               for (int k = 0; k < 32; ++k) {
                 y[k] = bits >> k & 1 ? fmaf(__uint_as_float(z[k]), f, -ref) : -INFINITY;
-                mx = fmaxf(mx, y[k]);
+                m4[k & 3] = fmaxf(m4[k & 3], y[k]);
               }
+              const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
               float up = 0.f, down = 1.f;
               if (none ? mx > -INFINITY : mx > kOff) {
                 up = ceilf(mx) - kOff;
@@ -546,12 +558,14 @@ __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendAr
                 tmem_st_wait();
               }
               uint32_t o[16];
+              float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
               for (int k = 0; k < 16; ++k) {
                 const float p0 = ex2(y[2 * k] - up), p1 = ex2(y[2 * k + 1] - up);
-                l += p0 + p1;
+                sum[k & 1] = add2(sum[k & 1], make_float2(p0, p1));
                 o[k] = pack2(p0, p1);
               }
+              l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
               tmem_st16(tS + c * (kChunk / 2), o);
             }
             fresh = __any_sync(kFull, none);
