@@ -22,6 +22,8 @@
 // kernel merges them (and writes the rows of empty streams). In a CTA each of the four warps takes every fourth
 // 32-token chunk with its own two-stage ring of bulk copies; nothing but the end of a stream's part
 // synchronises them.
+#include <cooperative_groups.h>
+
 #include "page_attend.cuh"
 
 namespace kvc {
@@ -32,6 +34,7 @@ constexpr int kUnit = 64;    // tokens of a work unit
 constexpr int kChunk32 = 32;  // tokens of a ring stage
 constexpr int kStages = 2;
 constexpr int kMaxGridSMs = 160;
+constexpr int kMostCtas = 8;  // of a cluster
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -76,6 +79,13 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
 
   // this CTA's units, and the stream its first one lies in
   int vs = blockIdx.x, base = 0, ca = 0, left = 1;  // whole: `left` becomes the stream's units
+  int rank = 0, step = kWarps;                       // of the cluster's CTAs; chunks between two of a warp's
+  if constexpr (kPart<M>)
+    if (p.ctas > 1) {
+      rank = blockIdx.x % p.ctas;
+      vs = blockIdx.x / p.ctas;
+      step = kWarps * p.ctas;
+    }
   Split split(0, 1);
   if (!p.whole) {
     const int per = (p.nvs + 32 * kWarps - 1) / (32 * kWarps);
@@ -100,9 +110,9 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
     ca = w0 - base;
     left = w1 - w0;
   } else {
-    const Stream x = stream_of(a, p, m, vs, threadIdx.x == 0);
+    const Stream x = stream_of(a, p, m, vs, threadIdx.x == 0 && rank == 0);
     left = units_of(p, x);
-    if (left == 0)  // rows that see nothing
+    if (left == 0 && rank == 0)  // rows that see nothing
       for (int e = threadIdx.x; e < x.rows * D; e += 32 * kWarps) {
         const size_t at = out_row(a, p, x, x.r0 + e / D);
         static_cast<T*>(a.out)[at * D + e % D] = from_f32<T>(0.f);
@@ -114,22 +124,22 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
   bool alive = true;
 
   for (int C; left > 0; ++vs, ca = 0, base += C) {
-    const Stream x = stream_of(a, p, m, vs, true);
+    const Stream x = stream_of(a, p, m, vs, rank == 0);
     C = cost_of(p, x);
     if (C == 0) continue;
     const int cb = min(C, ca + left), ua = max(ca - p.lead, 0), ub = max(cb - p.lead, 0), U = C - p.lead;
     left -= cb - ca;
     if (ub == ua) continue;  // only the stream's leading cost
     const int c1 = min(2 * ub, (x.vis + kChunk32 - 1) / kChunk32);  // chunks [2 ua, c1) of the stream
-    const int c0 = 2 * ua + warp;
-    const int mine = c1 > c0 ? (c1 - c0 + kWarps - 1) / kWarps : 0;
+    const int c0 = 2 * ua + rank * kWarps + warp;
+    const int mine = c1 > c0 ? (c1 - c0 + step - 1) / step : 0;
     const int32_t* row = a.t.table + (size_t)x.s * a.t.maxp;
 
     // Where this warp's next 32 chunks lie, one a lane (two blocks apart where a page is half a chunk): the
     // lane that knows a chunk's place issues its copy.
     const uint8_t* src[2];
     auto locate = [&](int i) {
-      const int tok = (c0 + kWarps * (i + lane)) * kChunk32;
+      const int tok = (c0 + step * (i + lane)) * kChunk32;
       if constexpr (kPart<M>) {  // the blocks left out may end anywhere in a page
         const bool want = i + lane < mine, want1 = want && tok + 16 < x.vis;
         const int r0 = x.real(tok), r1 = x.real(tok + 16);
@@ -265,7 +275,7 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
         break;
       }
       const uint8_t* buf = ring + st * SM::kStage;
-      const int tok0 = (c0 + kWarps * i) * kChunk32;
+      const int tok0 = (c0 + step * i) * kChunk32;
       const uint32_t ok = *reinterpret_cast<volatile uint32_t*>(&oks[warp][st]);
 
       // S^T of the two 16-token blocks
@@ -519,6 +529,54 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
       }
       __syncthreads();
     }
+    if constexpr (kPart<M>)
+      if (p.ctas > 1) {
+        // the CTAs' parts meet in their shared memories: each leaves its own in one [row][channel], and takes a share of
+        // the elements out of all
+        namespace cg = cooperative_groups;
+        cg::cluster_group cl = cg::this_cluster();
+        float* mb = merge;
+        float2* ml = reinterpret_cast<float2*>(mb + SM::kRows * D);
+        if (warp == 0) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int rr = nt * 8 + 2 * t + e;
+              float2* op = reinterpret_cast<float2*>(mb + rr * D + CPV * g);
+#pragma unroll
+              for (int k = 0; k < KS; ++k) op[k] = make_float2(o[nt][k][e], o[nt][k][e + 2]);
+              if (g == 0) ml[rr] = make_float2(ref[nt][e], l[nt][e]);
+            }
+        }
+        cl.sync();
+        for (int i = rank * 32 * kWarps + (int)threadIdx.x; i < x.rows * D; i += p.ctas * 32 * kWarps) {
+          const int rr = i / D;
+          float2 y[kMostCtas];
+          float z[kMostCtas], top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < kMostCtas; ++c) {
+            if (c >= p.ctas) break;
+            y[c] = cl.map_shared_rank(ml, c)[rr];
+            z[c] = cl.map_shared_rank(mb, c)[i];
+            if (y[c].y > 0.f) top = fmaxf(top, y[c].x);
+          }
+          float sum = 0.f, v = 0.f;
+#pragma unroll
+          for (int c = 0; c < kMostCtas; ++c) {
+            if (c >= p.ctas) break;
+            if (y[c].y == 0.f) continue;
+            const float f0 = ex2(y[c].x - top);
+            sum += y[c].y * f0;
+            v += z[c] * f0;
+          }
+          const size_t at = out_row(a, p, x, x.r0 + rr);
+          static_cast<T*>(a.out)[at * D + i % D] = from_f32<T>(sum == 0.f ? 0.f : v * (a.g.ts[1] / sum));
+          if (a.lse && i % D == 0) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+        }
+        cl.sync();  // no CTA leaves while another reads its shared memory
+        return;     // a cluster has one stream
+      }
     if (warp == 0) {
       const bool whole = ua == 0 && ub == U;
       // who holds the stream's parts, for the combine kernel
@@ -698,6 +756,10 @@ constexpr int kTcLead = 5, kLead = 3;
 // second kernel (8 heads x 256 tokens: 6.9 us split, 5.9 whole; x 2048: 8.5 and 18.7). With two streams an SM
 // and more that pays up to kWholeCapMany tokens (512 heads x 256: 16.8 and 9.3 us; x 2048: 43 and 37.5).
 constexpr int kWholeCap = 512, kWholeCapMany = 2048;
+// Under SeenArgs a cluster of CTAs takes a whole stream up to so many tokens a CTA: 32 x 8 heads of 1024 tokens, two CTAs,
+// 16.5 us against 19.8 split, of 4096 the same; 16 x 8 heads, four CTAs, of 2048 tokens 16.2 and 18.1, of 8192 38.5 and
+// 38.5; eight CTAs only while there is little to do: 4 x 8 heads of 1500 tokens 9.5 and 10.7, 8 x 8 heads of 2048 13.1 and 12.4.
+constexpr int kClusterCap = 1024, kClusterCapMost = 200;
 constexpr int tiles_for(int R) { return R <= 8 ? 1 : 2; }
 constexpr int min_blocks(int nt, int parts) { return nt * parts == 1 ? 4 : nt * parts == 2 ? 3 : 2; }
 
@@ -735,6 +797,20 @@ AttendPlan make_plan(const AttendArgs& a, const M& m, int parts, int sms, size_t
     if (bytes) *bytes = 256;
     return p;
   }
+  if constexpr (kPart<M>) {
+    // A window bounds what a stream has to see, so a fixed share of it for each CTA of a cluster loses little, and saves
+    // the search for the units and the second kernel.
+    int ctas = 1;
+    while (ctas < kMostCtas && (long long)p.nvs * ctas * 2 <= sms * min_blocks(nt, parts)) ctas *= 2;
+    // (the workspace is sized for the other way: fewer SMs than kMaxGridSMs may take it)
+    if (!tc && m.window < kSeenAll && ctas > 1 && cap <= (long long)ctas * (ctas == kMostCtas ? kClusterCapMost : kClusterCap) && !bytes) {
+      p.whole = 1;
+      p.ctas = ctas;
+      p.lead = 0;
+      p.grid = p.nvs * ctas;
+      return p;
+    }
+  }
   const size_t slots = (size_t)p.grid * 2 * p.rb;
   const size_t ml = (slots * sizeof(float2) + 255) & ~(size_t)255;
   const size_t span = ((size_t)p.nvs * sizeof(int2) + 255) & ~(size_t)255;
@@ -752,6 +828,11 @@ int go(const AttendArgs& a, const AttendPlan& p, const M& m, cudaStream_t s) {
   if (smem > 47 * 1024 &&  // beyond the default, beside the kernel's static part
       cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return KVC_ERR_LAUNCH;
+  if constexpr (kPart<M>)
+    if (p.ctas > 1)
+      return launch_pdl_cluster(k, dim3(p.grid), dim3(32 * kWarps), p.ctas, smem, s, a, p, m) == cudaSuccess
+                 ? KVC_OK
+                 : KVC_ERR_LAUNCH;
   return launch_pdl(k, dim3(p.grid), dim3(32 * kWarps), smem, s, false, a, p, m) == cudaSuccess ? KVC_OK
                                                                                                 : KVC_ERR_LAUNCH;
 }
