@@ -427,6 +427,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
         l += (l2.x + l2.y) + (l3.x + l3.y);
         tmem_st_wait();
         tc::fence_before_sync();
+        // The part's end waits for this unit's P V. A wait for a phase's parity tells it from the phase two before only
+        // once that before it is over, and a group may be a unit ahead of the issuer: so that one is waited for here, while
+        // this one cannot be over.
+        if (i > 0 && i == m - 1 && !wait(&bars.pv_done[w], (n - 1) & 1)) return false;
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.p_full[n & 1][w]);
       }
