@@ -598,3 +598,207 @@ def test_binding_refuses_wrong_tensors():
         kvc.kvc_tree_mask(i32(2, 3), i32(2, 3))
     with pytest.raises(ValueError):
         kvc.kvc_tree_verify(i32(2, 3), i32(2, 3), i32(2, 4), i32(2, 3), i32(2))
+
+
+# ---- larger caches, made and checked on the GPU ---------------------------------------------------------------------
+class Made:
+    """A cache of given lengths stored on the GPU, with its rows read back and the model's sums in 64 bits."""
+
+    def __init__(self, dt, D, B, Hkv, G, T, page, lens, seed, maxp=None):
+        kvc = kvc_()
+        self.kvc, self.dt, self.lens = kvc, dt, np.asarray(lens, np.int64).reshape(B, Hkv)
+        n = int(self.lens.max())
+        maxp = maxp or max(1, R.npg(n, page))
+        self.pool, self.pages = kvc.Pool.empty(B * Hkv * R.npg(n, page) + 3, D, page, device=DEV), kvc.Pages.empty(1, B, Hkv, maxp, device=DEV)
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        start = torch.zeros((1, B, Hkv), dtype=torch.int32, device=DEV)
+        kvc.kvc_page_extend(self.pool, self.pages, add_all=n)
+        kvc.kvc_page_store(self.pool, self.pages, *(torch.randn((B, n, Hkv, D), generator=g, device=DEV).to(DT[dt]) for _ in range(2)),
+                           start)
+        self.K, self.V = (torch.zeros((1, B, Hkv, n, D), device=DEV) for _ in range(2))
+        kvc.kvc_page_read(self.pool, self.pages, self.K, self.V)
+        self.pages.len.copy_(up(self.lens.astype(np.int32)[None]))  # the streams' ends differ; what lies behind is not theirs
+        self.q = (2 * torch.randn((B, T, Hkv * G, D), generator=g, device=DEV)).to(DT[dt])
+
+    def check(self, rows=None, n_q=None, window=0, sinks=0, mask=None, depth=None, ws=None):
+        B, T, Hq, D = self.q.shape
+        G = Hq // self.lens.shape[1]
+        out, lse = torch.full_like(self.q, -55.0), torch.full(self.q.shape[:3], -55.0, device=DEV)
+        status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        dev = lambda v: None if v is None else up(np.asarray(v, np.int32))
+        self.kvc.kvc_page_attend_masked(self.pool, self.pages, self.q, out, window=window, sinks=sinks, mask=dev(mask),
+                                        depth=dev(depth), lse=lse, n_q=dev(n_q), status=status, workspace=ws)
+        assert int(status.item()) == 0
+        for b in range(B):
+            nq = Q.drafts(n_q, b, T)
+            assert (out[b, nq:] == -55.0).all() and (lse[b, nq:] == -55.0).all()
+            for h in range(self.lens.shape[1]):
+                m, hs = int(self.lens[b, h]), slice(h * G, (h + 1) * G)
+                for i in (range(nq) if rows is None else sorted({0, nq // 2, nq - 1} & set(range(nq)))):
+                    seen = torch.from_numpy(Q.seen_tokens(m, nq, i, window, sinks, None if mask is None else mask[b, i],
+                                                          None if depth is None else depth[b])).to(DEV)
+                    if len(seen) == 0:
+                        assert (out[b, i, hs] == 0).all() and torch.isneginf(lse[b, i, hs]).all()
+                        continue
+                    ks, vs, qq = self.K[0, b, h, seen].double(), self.V[0, b, h, seen].double(), self.q[b, i, hs].double()
+                    s = qq @ ks.T / D ** 0.5
+                    z = torch.logsumexp(s, -1)
+                    p = torch.exp(s - z[:, None])
+                    ref = dict(out=p @ vs, lse=z, mass=p @ vs.abs(), vmax=vs.abs().amax(0) + 0 * qq,
+                               logit=(qq.abs() @ ks.abs().T / D ** 0.5).amax(-1))
+                    ref = {name: v.cpu().numpy() for name, v in ref.items()}
+                    tol, ltol = R.tolerances(self.dt, len(seen), D, ref)
+                    err = np.abs(out[b, i, hs].double().cpu().numpy() - ref["out"])
+                    assert (err <= tol).all(), (b, h, i, float((err / tol).max()))
+                    assert (np.abs(lse[b, i, hs].double().cpu().numpy() - ref["lse"]) <= ltol).all(), (b, h, i)
+        return out, lse
+
+
+@pytest.mark.parametrize("dt,D,B,Hkv,G,T,page,n,w", [
+    ("bf16", 128, 1, 2, 4, 1, 64, 3000, 1200),   # eight CTAs a cluster
+    ("bf16", 64, 2, 3, 3, 3, 16, 2500, 900),     # two row tiles
+    ("f32", 128, 2, 2, 2, 2, 32, 2000, 700),
+    ("f32", 64, 1, 4, 8, 2, 256, 1500, 1100),
+    ("bf16", 128, 16, 8, 4, 1, 64, 1500, 1000),  # four
+    ("bf16", 64, 32, 8, 2, 1, 64, 1000, 700),    # two
+    ("f32", 64, 16, 8, 1, 1, 64, 1300, 800)])
+def test_a_cluster_of_ctas_a_stream(dt, D, B, Hkv, G, T, page, n, w):
+    """Windows between what one CTA takes and what is split; streams shorter than the window, of one token and of none."""
+    rng = np.random.default_rng(n)
+    lens = rng.integers(1, n + 1, B * Hkv)
+    lens[:2] = n, 0
+    lens[-1] = rng.integers(1, 3)
+    x = Made(dt, D, B, Hkv, G, T, page, lens, n)
+    x.check(window=w, sinks=4)
+    x.check(window=w, sinks=0, n_q=rng.integers(0, T + 1, B) if T > 1 else None)
+    parent = Q.random_trees(rng, B, T)
+    mask, depth, _ = Q.tree_mask(parent, window=w)
+    x.check(window=w, sinks=70, mask=mask, depth=depth)
+
+
+@pytest.mark.parametrize("D,G,T", [(128, 1, 17), (128, 4, 32), (64, 3, 43), (128, 8, 32), (64, 1, 257), (128, 5, 52)])
+def test_rows_around_a_block(D, G, T):
+    """17, 128, 129, 256, 257 and 260 rows a KV head; streams of one unit, of a few, of less than the rows."""
+    rng = np.random.default_rng(T)
+    x = Made("bf16", D, 2, 3, G, T, 64, [1000, 3, 129, 128, 700, T + 1], T)
+    parent = Q.random_trees(rng, 2, T)
+    mask, depth, _ = Q.tree_mask(parent)
+    x.check(mask=mask)
+    x.check(mask=mask, depth=depth, window=100, sinks=130, n_q=[T - 1, T // 2])
+    x.check(window=60, sinks=3)
+    x.check(window=513)
+
+
+@pytest.mark.parametrize("dt,D,T,w", [("bf16", 128, 1, 100), ("bf16", 128, 1, 1500), ("bf16", 64, 3, 40000), ("f32", 128, 2, 20000),
+                                      ("bf16", 128, 24, 30000), ("bf16", 64, 24, 30000), ("bf16", 128, 80, 30000)])
+def test_a_wait_that_runs_out(dt, D, T, w):
+    """As test_gpu_page_faults does it, on every kernel: the first CTA waits for an arrival that nothing makes. The call ends
+    and says so, streams without a share of that CTA keep their results, the next call on the workspace is right."""
+    import time
+    kvc = kvc_()
+    B, Hkv, G, n = 2, 3, 4, 40960
+    x = Made(dt, D, B, Hkv, G, T, 64, [n] * (B * Hkv), T)
+    ws = torch.empty(kvc.kvc_page_attend_masked_workspace_size(x.pool, x.pages, Hkv * G, T, w, 4), dtype=torch.uint8, device=DEV)
+    res = []
+    for mode, fill in ((0, False), (2, False), (2, True), (0, True)):
+        if fill:
+            ws.fill_(0xff)
+        out, lse = torch.full_like(x.q, 9.0), torch.full(x.q.shape[:3], 9.0, device=DEV)
+        status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        torch.cuda.synchronize()
+        kvc.kvc_debug_fault(mode)
+        try:
+            t0 = time.time()
+            kvc.kvc_page_attend_masked(x.pool, x.pages, x.q, out, window=w, sinks=4, lse=lse, status=status, workspace=ws)
+            torch.cuda.synchronize()
+            took = time.time() - t0
+        finally:
+            kvc.kvc_debug_fault(0)
+        assert int(status.item()) == (kvc.KVC_STATUS_TIMEOUT if mode else 0)
+        assert took < 20.0
+        res.append((out, lse))
+    (o0, l0), *bad, (o3, l3) = res
+    assert torch.equal(o0, o3) and torch.equal(l0, l3)
+    for o, l in bad:
+        assert torch.equal(o0[1:], o[1:]) and torch.equal(l0[1:], l[1:])
+        assert torch.equal(o0[0, :, G:], o[0, :, G:]) and torch.equal(l0[0, :, G:], l[0, :, G:])  # the other heads
+        assert not torch.equal(l0[0, :, :G], l[0, :, :G])
+    assert torch.equal(bad[0][0], bad[1][0]) and torch.equal(bad[0][1], bad[1][1])  # nothing stale came in
+    x.check(rows=3, window=w, sinks=4, ws=ws)
+
+
+def test_offsets_past_32_bits():
+    """A stream whose pages lie in a pool of 5 GB: attention under a window and a mask, a slide and accepted drafts there."""
+    kvc = kvc_()
+    D, page, n, T = 128, 256, 700, 40
+    npages = (5 << 30) // kvc.kvc_page_bytes(D, page)
+    pool = kvc.Pool.empty(npages, D, page, device=DEV)
+    pool.free_list.copy_(torch.arange(npages, dtype=torch.int32, device=DEV))  # the last pages first
+    pages = kvc.Pages.empty(1, 1, 2, 6, device=DEV)
+    start = torch.zeros((1, 1, 2), dtype=torch.int32, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    kvc.kvc_page_extend(pool, pages, add_all=n, start=start, status=status)
+    assert int(pages.table[0, 0, 0, 0]) == npages - 1
+    k, v = rand_rows((1, n, 2, D), "bf16", 1).to(DEV), rand_rows((1, n, 2, D), "bf16", 2).to(DEV)
+    kvc.kvc_page_store(pool, pages, k, v, start, status=status)
+    small, same = kvc.Pool.empty(20, D, page, device=DEV), kvc.Pages.empty(1, 1, 2, 6, device=DEV)
+    kvc.kvc_page_extend(small, same, add_all=n)
+    kvc.kvc_page_store(small, same, k, v, start)
+    mask, depth, _ = Q.tree_mask(Q.random_trees(np.random.default_rng(3), 1, T))
+    path = np.full((1, T), -1, np.int32)
+    path[0, :5] = 1, 3, 8, 9, 39
+    for rows in (1, 4, T):
+        q = rand_rows((1, rows, 8, D), "bf16", rows).to(DEV)
+        for kw in (dict(window=300, sinks=4),) + ((dict(mask=up(mask), depth=up(depth)),) if rows == T else ()):
+            a, b = torch.empty_like(q), torch.empty_like(q)
+            kvc.kvc_page_attend_masked(pool, pages, q, a, status=status, **kw)
+            kvc.kvc_page_attend_masked(small, same, q, b, **kw)
+            assert torch.equal(a, b)
+    for x, t in ((pool, pages), (small, same)):
+        kvc.kvc_page_accept(x, t, up(path), up(np.array([5], np.int32)), status=status)
+        kvc.kvc_page_slide(x, t, 200, 3, status=status)
+    assert torch.equal(pages.len, same.len) and int(status.item()) == 0
+    m = int(same.len[0, 0, 0])
+    got = [torch.zeros((1, 1, 2, m, D), device=DEV) for _ in range(4)]
+    kvc.kvc_page_read(pool, pages, *got[:2])
+    kvc.kvc_page_read(small, same, *got[2:])
+    assert torch.equal(got[0], got[2]) and torch.equal(got[1], got[3])
+
+
+def test_prompt_in_chunks_on_a_windowed_layer():
+    """A prompt of 1500 tokens in chunks of 512, slid in between, against the dense rows: every query's window crosses the
+    chunks."""
+    kvc = kvc_()
+    D, Hkv, G, N, w, k, page = 128, 2, 4, 1500, 400, 5, 64
+    pool, pages = kvc.Pool.empty(40, D, page, device=DEV), kvc.Pages.empty(1, 1, Hkv, 20, device=DEV)
+    kk, vv = rand_rows((1, N, Hkv, D), "bf16", 1).to(DEV), rand_rows((1, N, Hkv, D), "bf16", 2).to(DEV)
+    q = rand_rows((1, N, Hkv * G, D), "bf16", 3).to(DEV)
+    big, all_ = kvc.Pool.empty(60, D, page, device=DEV), kvc.Pages.empty(1, 1, Hkv, 30, device=DEV)
+    start, zero = torch.zeros((1, 1, Hkv), dtype=torch.int32, device=DEV), torch.zeros((1, 1, Hkv), dtype=torch.int32, device=DEV)
+    kvc.kvc_page_extend(big, all_, add_all=N)
+    kvc.kvc_page_store(big, all_, kk, vv, zero)
+    K, V = (torch.zeros((1, 1, Hkv, N, D), device=DEV) for _ in range(2))
+    kvc.kvc_page_read(big, all_, K, V)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for a in range(0, N, 512):
+        T = min(512, N - a)
+        kvc.kvc_page_extend(pool, pages, add_all=T, start=start, status=status)
+        kvc.kvc_page_store(pool, pages, kk[:, a:a + T], vv[:, a:a + T], start, status=status)
+        out, lse = torch.empty((1, T, Hkv * G, D), dtype=torch.bfloat16, device=DEV), torch.empty((1, T, Hkv * G), device=DEV)
+        kvc.kvc_page_attend_masked(pool, pages, q[:, a:a + T], out, window=w, sinks=k, lse=lse, status=status)
+        kvc.kvc_page_slide(pool, pages, w, k, status=status)
+        for i in range(0, T, 37):
+            j = a + i
+            seen = torch.tensor([t for t in range(j + 1) if t < k or t > j - w], device=DEV)
+            for h in range(Hkv):
+                ks, vs, qq = K[0, 0, h, seen].double(), V[0, 0, h, seen].double(), q[0, j, h * G:(h + 1) * G].double()
+                s = qq @ ks.T / D ** 0.5
+                z = torch.logsumexp(s, -1)
+                p = torch.exp(s - z[:, None])
+                ref = dict(out=p @ vs, lse=z, mass=p @ vs.abs(), vmax=vs.abs().amax(0) + 0 * qq,
+                           logit=(qq.abs() @ ks.abs().T / D ** 0.5).amax(-1))
+                ref = {name: v.cpu().numpy() for name, v in ref.items()}
+                tol, ltol = R.tolerances("bf16", len(seen), D, ref)
+                assert (np.abs(out[0, i, h * G:(h + 1) * G].double().cpu().numpy() - ref["out"]) <= tol).all()
+                assert (np.abs(lse[0, i, h * G:(h + 1) * G].double().cpu().numpy() - ref["lse"]) <= ltol).all()
+    assert int(status.item()) == 0 and int(pages.len[0, 0, 0]) < 600
