@@ -174,18 +174,23 @@ __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendAr
   tc::fence_after_sync();
   const uint32_t tmem = tmem_slot;
   volatile int* ab = &abort_flag;
-  // in line, and short: a function call has no place between roles that hold different numbers of registers
+  // In line, and short: a function call has no place between roles that hold different numbers of registers. The clock,
+  // which takes long to read, and the other roles' flag are looked at every 64 polls.
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (__all_sync(kFull, mbar_ready(bar, parity))) return true;
-    const uint64_t since = clock_ns();
+    uint64_t since = 0;
 #pragma unroll 1
-    while (!__any_sync(kFull, *ab != 0))
-      if (__all_sync(kFull, mbar_ready(bar, parity))) return true;
-      else if (__any_sync(kFull, clock_ns() - since > kWaitNs)) {
-        status_or(a.status, KVC_STATUS_TIMEOUT);
-        *ab = 1;
+    for (uint32_t i = 1; !__all_sync(kFull, mbar_ready(bar, parity)); ++i)
+      if (i % 64 == 0) {
+        const uint64_t now = clock_ns();
+        if (since == 0) since = now;
+        if (__any_sync(kFull, *ab != 0)) return false;
+        if (__any_sync(kFull, now - since > kWaitNs)) {
+          status_or(a.status, KVC_STATUS_TIMEOUT);
+          *ab = 1;
+          return false;
+        }
       }
-    return false;
+    return true;
   };
 
   // Every role walks the same parts: f(stream, vs, first unit, end unit, units of the stream, cost before them).
