@@ -160,10 +160,11 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t x, uint32_t y) {
 }
 // Under SeenArgs a row's probability of a token that it does not see is 0, whatever the token's bytes: a V scale that the
 // store does not write (NaN, below zero) counts as zero.
-__device__ __forceinline__ uint32_t no_nan2(uint32_t x) {
-  const __half2 r = __hmax2(*reinterpret_cast<const __half2*>(&x), __half2half2(__ushort_as_half(0)));
+__device__ __forceinline__ uint32_t at_least2(uint32_t x, uint32_t least) {  // the other operand where one is no number
+  const __half2 r = __hmax2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&least));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+__device__ __forceinline__ uint32_t no_nan2(uint32_t x) { return at_least2(x, 0u); }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __half2 r = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&r);

@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendAr
     const int dw = warp - kSoftWarps, kv = dw / kPer, wd = dw % kPer;  // K or V; tokens of the unit
     uint64_t* full = kv ? bars.v_full : bars.k_full;
     uint64_t* empty = kv ? bars.v_empty : &bars.s_full[RT - 1];
-    // Lane l has 32 channels, chunk c of a row, of tokens r + kTok * i: a warp's loads are contiguous. Its four 16-byte
+    // A lane has 32 channels, chunk c of a row, of tokens r + kTok * i: a warp's loads are contiguous. Its four 16-byte
     // stores of a vector go chunk by chunk; with c & 2 in another order, so that eight lanes' stores fall on different
     // banks (their rows' chunks c and c + 2 lie a multiple of 128 bytes apart).
     const int r = lane / Sh::kLanes, c = lane % Sh::kLanes, turn = c & 2;
@@ -359,9 +359,10 @@ __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendAr
         st_at[i] = tc::smem_u32(smem + (kv ? L::oV : L::oK)) + (c >> 1) * L::kHalf + row * 128 +
                    ((((c & 1) * 4 + (i ^ turn)) ^ (row & 7)) << 4);
     }
-    const int codes_at = (kv ? piece_off(D, 2) : 0) + (r & 15) * (D / 2) + c * 16;
-    const int scales_at = (kv ? piece_off(D, 3) : piece_off(D, 1)) + (r & 15) * (D / 16) + c * 2;
+    const uint8_t* codes = a.g.data + (kv ? piece_off(D, 2) : 0) + (r & 15) * (D / 2) + c * 16;
+    const uint8_t* scales = a.g.data + (kv ? piece_off(D, 3) : piece_off(D, 1)) + (r & 15) * (D / 16) + c * 2;
     const int pmask = (1 << a.g.lp) - 1;
+    const uint32_t least = kv ? 0u : 0xfc00fc00u;  // a V scale that is no number or below zero counts as zero
     uint32_t n = 0, seg = 0;
     parts([&](const Stream& x, int, int ua, int ub, int, int) {
       const int32_t* row = a.t.table + (size_t)x.s * a.t.maxp;
@@ -382,22 +383,21 @@ __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendAr
           ibase += kAhead;
           ids_next = read_ids(ibase + kAhead);
         }
-        const uint8_t* src[kBlks];
         ok = 0;
 #pragma unroll
         for (int b = 0; b < kBlks; ++b) {
           const int id = __shfl_sync(kFull, ids, (u - ibase) * kBlks + b);
           const int tok = x.real(tok_of(u, b));
-          src[b] = id >= 0 ? block_of(a.g, id, (tok & pmask) >> 4) : nullptr;
+          const uint32_t blk = ((uint32_t)id << (a.g.lp - 4)) + ((tok & pmask) >> 4);  // of the pool's, below 2^32
+          const uint64_t at = (uint64_t)blk * (uint32_t)blk_bytes(D);
           if (id >= 0) ok |= 1u << b;
           if (id == -2 && kv == 0 && lane == 0) status_or(a.status, KVC_STATUS_BAD_PAGE);
-        }
 #pragma unroll
-        for (int i = 0; i < Sh::V; ++i) {
-          const int tk = i * Sh::kTok;  // of the warp's; r is added
-          const uint8_t* s = src[tk >> 4];
-          v.c[i] = s ? ld_stream16(s + codes_at + (tk & 15) * (D / 2)) : make_uint4(0u, 0u, 0u, 0u);
-          v.s[i] = s ? ld_stream2(s + scales_at + (tk & 15) * (D / 16)) : 0u;
+          for (int k = 0; k < Sh::V / kBlks; ++k) {
+            const int i = b * (Sh::V / kBlks) + k;
+            v.c[i] = id >= 0 ? ld_stream16(codes + at + k * Sh::kTok * (D / 2)) : make_uint4(0u, 0u, 0u, 0u);
+            v.s[i] = id >= 0 ? ld_stream2(scales + at + k * Sh::kTok * (D / 16)) : 0u;
+          }
         }
       };
       auto decode = [&](const Sh& v, uint32_t ok) {
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendAr
             const uint32_t y = w[0], z = w[1];
             w[0] = w[2], w[1] = w[3], w[2] = y, w[3] = z;
           }
-          const uint32_t two = no_nan2_if(kv, e4m3x2_f16x2(v.s[i]));
+          const uint32_t two = at_least2(e4m3x2_f16x2(v.s[i]), least);
           const uint32_t s2[2] = {__byte_perm(two, two, scale0), __byte_perm(two, two, scale1)};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -476,14 +476,12 @@ __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendAr
         tc::fence_after_sync();
         // the factors were written before q_full, which precedes every s_full
         if (i == 0) f = *reinterpret_cast<volatile float*>(&row_f[seg & 1][rr]);
-        uint32_t blocks;  // the unit's blocks that are there
-        if constexpr (kDecWarps == 16) {
-          const uint64_t by = *reinterpret_cast<volatile uint64_t*>(&unit_ok[n & 3]);  // a block a byte
-          blocks = (uint32_t)(by * 0x0102040810204080ull >> 56);
-        } else {
-          const uint32_t by = *reinterpret_cast<volatile uint32_t*>(&unit_ok[n & 3]);  // two a byte
-          blocks = by * 0x01041040u >> 24;
-        }
+        // the unit's blocks that are there: one or two a byte, nearly always all
+        using Word = typename std::conditional<kDecWarps == 16, uint64_t, uint32_t>::type;
+        const Word by = *reinterpret_cast<volatile Word*>(&unit_ok[n & 3]);
+        uint32_t blocks = 0xff;
+        if (by != (kDecWarps == 16 ? (Word)0x0101010101010101ull : (Word)0x03030303u))
+          blocks = kDecWarps == 16 ? (uint32_t)(by * 0x0102040810204080ull >> 56) : (uint32_t)by * 0x01041040u >> 24;
         // every row sees every token, and nearly always the reference holds: one straight run, the next chunk's logits on
         // their way
         uint32_t s[2][32];
@@ -661,15 +659,18 @@ __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendAr
   if (__syncthreads_or(*ab)) {
     // a role gave up and the others followed: what this CTA leaves undone must not be taken for what lay in the
     // workspace. Streams that begin here hold no part at all, those that began before nothing of this CTA's.
-    const int done = min(parts_done[0], parts_done[1]);
-    int i = 0;
-    parts([&](const Stream&, int vs, int ua, int, int, int) {
-      if (i++ < done) return true;
-      if (ua == 0 && threadIdx.x == 0) p.span[vs] = make_int2(-1, -1);
-      if (threadIdx.x < kRows)
-        p.ml[((size_t)blockIdx.x * 2 + (ua == 0 ? 1 : 0)) * kRows + threadIdx.x] = make_float2(0.f, 0.f);
-      return true;
-    });
+    if (warp < kSoftWarps) {  // they have the registers for it, and a thread a row
+      static_assert(32 * kSoftWarps >= kRows, "a thread a row");
+      const int done = min(parts_done[0], parts_done[1]);
+      int i = 0;
+      parts([&](const Stream&, int vs, int ua, int, int, int) {
+        if (i++ < done) return true;
+        if (ua == 0 && threadIdx.x == 0) p.span[vs] = make_int2(-1, -1);
+        if (threadIdx.x < kRows)
+          p.ml[((size_t)blockIdx.x * 2 + (ua == 0 ? 1 : 0)) * kRows + threadIdx.x] = make_float2(0.f, 0.f);
+        return true;
+      });
+    }
     // products under way end before their memory goes
     if (warp >= kIssuer && warp < kIssuer + kIssuers) {
       if (elect_one()) tc::umma_commit(&bars.drain);  // the lane that issued the products

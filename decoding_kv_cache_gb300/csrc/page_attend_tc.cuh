@@ -87,6 +87,5 @@ __device__ __forceinline__ void scale_halves16(uint32_t taddr, float c) {  // c 
   }
   tmem_st16(taddr, o);
 }
-__device__ __forceinline__ uint32_t no_nan2_if(bool yes, uint32_t x) { return yes ? no_nan2(x) : x; }
 
 }  // namespace kvc

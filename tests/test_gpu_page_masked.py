@@ -163,6 +163,15 @@ def test_any_mask_and_fewer_queries_than_rows(dt, D, G, T, page, lens):
         check(x, q, dt, n_q=n_q, window=7, sinks=1)
 
 
+@pytest.mark.parametrize("dt,G,T,w", [("bf16", 4, 1, 100), ("bf16", 4, 1, 700), ("bf16", 4, 9, 200), ("bf16", 4, 50, 200), ("f32", 2, 2, 300)])
+def test_no_lse_and_no_status(dt, G, T, w):
+    x, q = make_attend(dt, 64, 2, 2, G, T, 16, [900, 30, 0, 700], seed=4)
+    out, _ = check(x, q, dt, window=w, sinks=2)
+    only = torch.full_like(out, -55.0)
+    kvc_().kvc_page_attend_masked(x.pool, x.pages, q.to(DEV), only, window=w, sinks=2)
+    assert torch.equal(out, only)
+
+
 def test_no_window_and_no_mask_is_the_causal_attention():
     kvc = kvc_()
     for dt, G, T, lens in (("bf16", 4, 1, [900, 30, 0, 700]), ("bf16", 4, 30, [900, 30, 0, 700]), ("f32", 2, 3, [90, 2, 0, 1])):
@@ -676,9 +685,11 @@ def test_a_cluster_of_ctas_a_stream(dt, D, B, Hkv, G, T, page, n, w):
     x.check(window=w, sinks=70, mask=mask, depth=depth)
 
 
-@pytest.mark.parametrize("D,G,T", [(128, 1, 17), (128, 4, 32), (64, 3, 43), (128, 8, 32), (64, 1, 257), (128, 5, 52)])
+@pytest.mark.parametrize("D,G,T", [(128, 1, 17), (128, 4, 32), (64, 3, 43), (128, 8, 32), (64, 1, 257), (128, 5, 52),
+                                   (128, 200, 1), (64, 300, 2), (128, 130, 3)])
 def test_rows_around_a_block(D, G, T):
-    """17, 128, 129, 256, 257 and 260 rows a KV head; streams of one unit, of a few, of less than the rows."""
+    """17, 128, 129, 256, 257 and 260 rows a KV head; streams of one unit, of a few, of less than the rows. Many query heads
+    a KV head: a token's rows lie in several blocks."""
     rng = np.random.default_rng(T)
     x = Made("bf16", D, 2, 3, G, T, 64, [1000, 3, 129, 128, 700, T + 1], T)
     parent = Q.random_trees(rng, 2, T)
