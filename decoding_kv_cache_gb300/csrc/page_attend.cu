@@ -22,6 +22,10 @@
 // kernel merges them (and writes the rows of empty streams). In a CTA each of the four warps takes every fourth
 // 32-token chunk with its own two-stage ring of bulk copies; nothing but the end of a stream's part
 // synchronises them.
+//
+// The same kernels serve kvc_page_attend_masked, with SeenArgs in Causal's place: blocks that no row of a block sees are
+// left out of the stream (page_attend.cuh), a chunk that not every row sees whole is masked by each row's bounds and, in
+// the drafts, its bits, and a windowed stream may be one cluster's work, its parts merged in shared memory.
 #include <cooperative_groups.h>
 
 #include "page_attend.cuh"
@@ -752,6 +756,7 @@ constexpr int kTcMin = 17;
 // counted when the work is split, so that a CTA with two parts gets less (64 new tokens over 4 x 8192: 46.7 us
 // with none, 43.1 with 5; 16 x 8 heads of up to 1000 tokens 13.0 and 10.8 us with 3).
 constexpr int kTcLead = 5, kLead = 3;
+constexpr int kTcLeadPart = 8;  // under SeenArgs, 128 rows a block (16 x 8 heads of up to 4096 tokens: 45.2 us with 5, 43.8)
 // Tables of at most kWholeCap tokens: a CTA takes a whole stream, which saves the search for its units and the
 // second kernel (8 heads x 256 tokens: 6.9 us split, 5.9 whole; x 2048: 8.5 and 18.7). With two streams an SM
 // and more that pays up to kWholeCapMany tokens (512 heads x 256: 16.8 and 9.3 us; x 2048: 43 and 37.5).
@@ -778,7 +783,16 @@ AttendPlan make_plan(const AttendArgs& a, const M& m, int parts, int sms, size_t
   const bool tc = parts == 1 && R >= kTcMin;
   p.unit = tc ? kTcUnit : kUnit;
   p.lead = tc ? kTcLead : kLead;
-  p.rb = !tc ? 8 * nt : kPart<M> && R > kTcRows ? 2 * kTcRows : kTcRows;
+  p.rb = tc ? kTcRows : 8 * nt;
+  if (kPart<M> && tc) {
+    // A block of 256 rows takes as long as 1.75 of 128: a prompt's 4096 rows 88 us and 101, 448 rows 70 and 79, 256 rows
+    // 48.9 and 49.8, but 260 rows (two blocks for three) 70.5 and 63.9.
+    const int n1 = (R + kTcRows - 1) / kTcRows, n2 = (n1 + 1) / 2;
+    if (7LL * n2 < 4LL * n1)
+      p.rb = 2 * kTcRows;
+    else
+      p.lead = kTcLeadPart;
+  }
   p.nrb = (R + p.rb - 1) / p.rb;
   p.nvs = a.t.S * p.nrb;
   p.by_nrb = FastDiv::make(p.nrb);

@@ -6,15 +6,14 @@
 // fp16 by a power of two per row (bf16 values exact from 2^-25 of the row's largest on, below that off by at most 2^-33
 // of it); a probability is rounded to fp16 once, 2^-11 relative against the bf16 output's 2^-8.
 //
-//   decoders               a part's query rows to fp16 (the first part's are the softmax warps' work); then half of the warps K, half V: codes and scales from global memory
-//                          straight to registers ahead of time, four lanes a token, and as fp16 into the
-//                          128-byte-swizzled tiles (two stages each). V's tile [token][channel] is the second
-//                          product's B operand as it lies (MN-major).
-//   issuers                 the products
-//   softmax  (warps 0-7)   two groups, a thread a row. RT = 2: a row tile each. While one group's tile is in its
-//                          softmax the tensor cores work on the other's: P V of a unit, then Q K of the next into the
-//                          same columns. RT = 1: a unit's first and last 64 tokens each, with their own O, reference and
-//                          sum, S double-buffered, O merged at the part's end.
+//   decoders  a part's query rows to fp16 (the first part's are the softmax warps' work); then half of the warps K, half V:
+//             codes and scales from global memory straight to registers ahead of time, four lanes a token, and as fp16
+//             into the 128-byte-swizzled tiles (two stages each). V's tile [token][channel] is the second product's B
+//             operand as it lies (MN-major).
+//   issuers   the products
+//   softmax   two groups, a thread a row. RT = 2: a row tile each. While one group's tile is in its softmax the tensor
+//             cores work on the other's: P V of a unit, then Q K of the next into the same columns. RT = 1: a unit's first
+//             and last 64 tokens each, with their own O, reference and sum, S double-buffered, O merged at the part's end.
 // Both shapes decode a unit once; a 256-row block does so for twice the products.
 //
 // The softmax works on 64 tokens at a time (a step). Probabilities are formed against the reference at hand without
@@ -24,6 +23,13 @@
 // and what was summed so far rescaled. That path lies behind the straight one: instructions between those that always
 // run cost as much as they would run (in line and per element: 870 cycles a chunk of 32, 480 without). P replaces S in
 // tensor memory.
+//
+// What bounds it. RT = 1: some 2000 cycles a unit, of which the tensor cores need 1024; a softmax warp's chain (logits from
+// tensor memory 400, 64 exponentials and what belongs to them 1000, P back and handed on 600) at 0.72 of the SM's issue
+// (80 rows over 64 x 32768 tokens: 124 us, 0.36 of the copy peak, 0.36 of the tensor peak on the rows there are). RT = 2:
+// some 3500 cycles a unit of 256 rows, 2048 of them the tensor cores': a tile's softmax (1700) and its products (1400) take
+// turns, the other tile's lie beside them (a prompt's 1024 tokens under a window of 2048, 2 x 8 heads: 88 us, 0.41 of the
+// tensor peak). At each CTA's beginning 5 us, at its end and between two parts some 3 us.
 //
 // All waits are bounded; a role that gives up raises KVC_STATUS_TIMEOUT and the others follow.
 #include "page_attend.cuh"
@@ -497,8 +503,11 @@ __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendAr
           float l2[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            if (RT == 2 || e == 0) tc::tmem_wait();
-            tc::tmem_regs_ready(s[e]);
+            if (RT == 2 || e == 0) {
+              tc::tmem_wait();
+              tc::tmem_regs_ready(s[e]);
+              if (RT == 1) tc::tmem_regs_ready(s[1]);
+            }
             if (RT == 2 && 2 * h + e < 3) tc::tmem_ld32_async(tS + (2 * h + e + 1) * kChunk, s[e ^ 1]);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
