@@ -617,7 +617,9 @@ KVC_API int kvc_tree_verify(int32_t B, int32_t T, const int32_t* parent, const i
  *                  else the own token base + u exactly where bit u of mask[b,i] is set, as kvc_tree_mask wrote it or
  *                  otherwise (T <= KVC_TREE_MAX; bits at or past n_q do not count)
  *   depth          [B,T] (device) or NULL; only with a mask
- * Tokens are counted in storage order, so after an eviction a window is one of kept tokens.
+ * Tokens are counted in storage order, so after an eviction a window is one of kept tokens. What a query does not see has
+ * no part in its row, whatever its bytes are (a V scale that the store does not write, NaN or negative, counts as zero);
+ * a page that holds no token that a query of the call may see is not read.
  */
 KVC_API size_t kvc_page_attend_masked_workspace_size(const kvc_pool* pool, const kvc_pages* pages, int32_t Hq, int32_t T,
                                                      int32_t window, int32_t sinks);
@@ -667,9 +669,9 @@ KVC_API int kvc_abi_version(void);
  * (bf16 caches with 128-row observation tiles) withholds its exchange partials, so its group's
  * bounded waits give up after about 50 ms: those heads' scores are left unset,
  * KVC_STATUS_TIMEOUT is raised in the status word of kvc_evict, and the launch still returns.
- * mode 2: from the next kvc_page_attend on, the first CTA of the attention kernel waits for an arrival
- * that nothing makes and gives up after about a second: KVC_STATUS_TIMEOUT, the rows it had a share in
- * are incomplete, the call returns.
+ * mode 2: from the next kvc_page_attend or kvc_page_attend_masked on, the first CTA of the attention kernel
+ * waits for an arrival that nothing makes and gives up after about a second: KVC_STATUS_TIMEOUT, the rows it
+ * had a share in are incomplete, the call returns.
  * mode 0 restores normal behaviour. Process-wide, not thread-safe against concurrent calls.
  * Returns KVC_OK or KVC_ERR_INVALID_ARG for any other mode. */
 KVC_API int kvc_debug_fault(int32_t mode);
