@@ -91,17 +91,25 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
       step = kWarps * p.ctas;
     }
   Split split(0, 1);
+  auto nothing = [&](const Stream& x) {  // rows that see nothing
+    for (int e = threadIdx.x; e < x.rows * D; e += 32 * kWarps) {
+      const size_t at = out_row(a, p, x, x.r0 + e / D);
+      static_cast<T*>(a.out)[at * D + e % D] = from_f32<T>(0.f);
+      if (a.lse && e % D == 0) a.lse[at] = -INFINITY;
+    }
+  };
   if (!p.whole) {
     const int per = (p.nvs + 32 * kWarps - 1) / (32 * kWarps);
     int W;
-    int before = scan_units<32 * kWarps>(a, p, m, sm_scan, per, &W);
+    int own;
+    int before = scan_units<32 * kWarps>(a, p, m, sm_scan, per, &W, &own);
     split = Split(W, p.grid);
     const int w0 = split.first(blockIdx.x), w1 = split.first(blockIdx.x + 1);
     if (w0 >= w1) return;
     for (int i = 0; i < per; ++i) {
       const int v = threadIdx.x * per + i;
       if (v >= p.nvs) break;
-      const int u = cost_of(p, stream_of(a, p, m, v, false));
+      const int u = kPart<M> && per == 1 ? own : cost_of(p, stream_of(a, p, m, v, false));
       if (before <= w0 && w0 < before + u) {
         sm_first[0] = v;
         sm_first[1] = before;
@@ -113,15 +121,12 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
     base = sm_first[1];  // cost before the stream
     ca = w0 - base;
     left = w1 - w0;
+  } else if constexpr (kPart<M>) {
+    __syncwarp();  // the barriers of this warp's ring are visible to its lanes; the stream is looked at below
   } else {
-    const Stream x = stream_of(a, p, m, vs, threadIdx.x == 0 && rank == 0);
+    const Stream x = stream_of(a, p, m, vs, threadIdx.x == 0);
     left = units_of(p, x);
-    if (left == 0 && rank == 0)  // rows that see nothing
-      for (int e = threadIdx.x; e < x.rows * D; e += 32 * kWarps) {
-        const size_t at = out_row(a, p, x, x.r0 + e / D);
-        static_cast<T*>(a.out)[at * D + e % D] = from_f32<T>(0.f);
-        if (a.lse && e % D == 0) a.lse[at] = -INFINITY;
-      }
+    if (left == 0) nothing(x);
     __syncwarp();  // the barriers of this warp's ring are visible to its lanes
   }
   uint32_t n = 0;  // chunks this warp has waited for
@@ -130,6 +135,14 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
   for (int C; left > 0; ++vs, ca = 0, base += C) {
     const Stream x = stream_of(a, p, m, vs, rank == 0);
     C = cost_of(p, x);
+    if constexpr (kPart<M>)
+      if (p.whole) {  // one stream
+        if (C == 0) {
+          if (rank == 0) nothing(x);
+          return;
+        }
+        left = C;
+      }
     if (C == 0) continue;
     const int cb = min(C, ca + left), ua = max(ca - p.lead, 0), ub = max(cb - p.lead, 0), U = C - p.lead;
     left -= cb - ca;
@@ -559,16 +572,19 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) attend_kernel(AttendArgs a,
           float2 y[kMostCtas];
           float z[kMostCtas], top = -INFINITY;
 #pragma unroll
+          for (int c = 0; c < kMostCtas; ++c) {  // all reads at once
+            const int from = min(c, p.ctas - 1);
+            y[c] = cl.map_shared_rank(ml, from)[rr];
+            z[c] = cl.map_shared_rank(mb, from)[i];
+          }
+#pragma unroll
           for (int c = 0; c < kMostCtas; ++c) {
-            if (c >= p.ctas) break;
-            y[c] = cl.map_shared_rank(ml, c)[rr];
-            z[c] = cl.map_shared_rank(mb, c)[i];
+            if (c >= p.ctas) y[c].y = 0.f;
             if (y[c].y > 0.f) top = fmaxf(top, y[c].x);
           }
           float sum = 0.f, v = 0.f;
 #pragma unroll
           for (int c = 0; c < kMostCtas; ++c) {
-            if (c >= p.ctas) break;
             if (y[c].y == 0.f) continue;
             const float f0 = ex2(y[c].x - top);
             sum += y[c].y * f0;
