@@ -777,10 +777,11 @@ constexpr int kTcLeadPart = 8;  // under SeenArgs, 128 rows a block (16 x 8 head
 // second kernel (8 heads x 256 tokens: 6.9 us split, 5.9 whole; x 2048: 8.5 and 18.7). With two streams an SM
 // and more that pays up to kWholeCapMany tokens (512 heads x 256: 16.8 and 9.3 us; x 2048: 43 and 37.5).
 constexpr int kWholeCap = 512, kWholeCapMany = 2048;
-// Under SeenArgs a cluster of CTAs takes a whole stream up to so many tokens a CTA: 32 x 8 heads of 1024 tokens, two CTAs,
-// 16.5 us against 19.8 split, of 4096 the same; 16 x 8 heads, four CTAs, of 2048 tokens 16.2 and 18.1, of 8192 38.5 and
-// 38.5; eight CTAs only while there is little to do: 4 x 8 heads of 1500 tokens 9.5 and 10.7, 8 x 8 heads of 2048 13.1 and 12.4.
-constexpr int kClusterCap = 1024, kClusterCapMost = 200;
+// Under SeenArgs a cluster of CTAs takes a whole stream up to so many tokens a CTA (split over all CTAs, in brackets): 8 x 8
+// heads, eight CTAs, window 4096 15.5 us (16.9), 8192 22.2 (22.9), 16384 37.9 (37.1); 16 x 8 heads, four CTAs, 2048 14.7
+// (17.5), 6000 29.5 (31.0), 12000 51.1 (48.7). One CTA does better up to kWholeCap tokens (16 x 8 heads, 400: 8.2 us and
+// 9.2), or to kClusterFrom where there is little to do (1 x 8 heads: 100 5.5 us and 6.5, 250 7.5 and 6.5).
+constexpr int kClusterCap = 2048, kClusterCapMost = 1100, kClusterFrom = 200;
 constexpr int tiles_for(int R) { return R <= 8 ? 1 : 2; }
 constexpr int min_blocks(int nt, int parts) { return nt * parts == 1 ? 4 : nt * parts == 2 ? 3 : 2; }
 
@@ -820,26 +821,25 @@ AttendPlan make_plan(const AttendArgs& a, const M& m, int parts, int sms, size_t
   const long long cap = most_seen(m, (long long)a.t.maxp << a.g.lp, a.T);
   const long long cost = (long long)p.nvs * ((cap + p.unit - 1) / p.unit + p.lead);  // if every stream is full
   if (cost < p.grid) p.grid = (int)cost;
-  if (!tc && cap <= (p.nvs >= 2 * sms ? kWholeCapMany : kWholeCap)) {
-    p.whole = 1;
-    p.lead = 0;
-    p.grid = p.nvs;
-    if (bytes) *bytes = 256;
-    return p;
-  }
   if constexpr (kPart<M>) {
     // A window bounds what a stream has to see, so a fixed share of it for each CTA of a cluster loses little, and saves
-    // the search for the units and the second kernel.
-    int ctas = 1;
-    while (ctas < kMostCtas && (long long)p.nvs * ctas * 2 <= sms * min_blocks(nt, parts)) ctas *= 2;
-    // (the workspace is sized for the other way: fewer SMs than kMaxGridSMs may take it)
-    if (!tc && m.window < kSeenAll && ctas > 1 && cap <= (long long)ctas * (ctas == kMostCtas ? kClusterCapMost : kClusterCap) && !bytes) {
+    // the search for the units and the second kernel. (The workspace is sized for the other way, whatever is taken here.)
+    const int room = sms * min_blocks(nt, parts) / p.nvs, ctas = room < kMostCtas ? room : kMostCtas;
+    if (!tc && !bytes && m.window < kSeenAll && ctas > 1 && cap > (4 * p.nvs <= sms ? kClusterFrom : kWholeCap) &&
+        cap <= (long long)ctas * (ctas == kMostCtas ? kClusterCapMost : kClusterCap)) {
       p.whole = 1;
       p.ctas = ctas;
       p.lead = 0;
       p.grid = p.nvs * ctas;
       return p;
     }
+  }
+  if (!tc && cap <= (p.nvs >= 2 * sms ? kWholeCapMany : kWholeCap)) {
+    p.whole = 1;
+    p.lead = 0;
+    p.grid = p.nvs;
+    if (bytes) *bytes = 256;
+    return p;
   }
   const size_t slots = (size_t)p.grid * 2 * p.rb;
   const size_t ml = (slots * sizeof(float2) + 255) & ~(size_t)255;

@@ -670,7 +670,11 @@ class Made:
     ("f32", 64, 1, 4, 8, 2, 256, 1500, 1100),
     ("bf16", 128, 16, 8, 4, 1, 64, 1500, 1000),  # four
     ("bf16", 64, 32, 8, 2, 1, 64, 1000, 700),    # two
-    ("f32", 64, 16, 8, 1, 1, 64, 1300, 800)])
+    ("f32", 64, 16, 8, 1, 1, 64, 1300, 800),
+    ("bf16", 64, 10, 8, 2, 1, 32, 1000, 900),    # seven, five and three
+    ("bf16", 128, 14, 8, 1, 1, 64, 800, 600),
+    ("bf16", 64, 20, 8, 1, 1, 64, 800, 650),
+    ("bf16", 128, 1, 3, 4, 1, 16, 300, 260)])    # few streams of few tokens
 def test_a_cluster_of_ctas_a_stream(dt, D, B, Hkv, G, T, page, n, w):
     """Windows between what one CTA takes and what is split; streams shorter than the window, of one token and of none."""
     rng = np.random.default_rng(n)
