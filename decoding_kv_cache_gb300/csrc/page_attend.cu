@@ -781,7 +781,9 @@ constexpr int kWholeCap = 512, kWholeCapMany = 2048;
 // heads, eight CTAs, window 4096 15.5 us (16.9), 8192 22.2 (22.9), 16384 37.9 (37.1); 16 x 8 heads, four CTAs, 2048 14.7
 // (17.5), 6000 29.5 (31.0), 12000 51.1 (48.7). One CTA does better up to kWholeCap tokens (16 x 8 heads, 400: 8.2 us and
 // 9.2), or to kClusterFrom where there is little to do (1 x 8 heads: 100 5.5 us and 6.5, 250 7.5 and 6.5).
-constexpr int kClusterCap = 2048, kClusterCapMost = 1100, kClusterFrom = 200;
+// Without a window, few streams, the table's tokens counting: 1 x 8 heads, 8 rows, 4000 10.6 us and 12.1, 16 rows, 8000 18.3
+// and 16.2.
+constexpr int kClusterCap = 2048, kClusterCapMost = 1100, kClusterFrom = 200, kClusterCapFew = 512;
 constexpr int tiles_for(int R) { return R <= 8 ? 1 : 2; }
 constexpr int min_blocks(int nt, int parts) { return nt * parts == 1 ? 4 : nt * parts == 2 ? 3 : 2; }
 
@@ -823,10 +825,11 @@ AttendPlan make_plan(const AttendArgs& a, const M& m, int parts, int sms, size_t
   if (cost < p.grid) p.grid = (int)cost;
   if constexpr (kPart<M>) {
     // A window bounds what a stream has to see, so a fixed share of it for each CTA of a cluster loses little, and saves
-    // the search for the units and the second kernel. (The workspace is sized for the other way, whatever is taken here.)
+    // the search for the units and the second kernel; so it does where a table is short and SMs are left over. (The workspace is sized for the other way, whatever is taken here.)
     const int room = sms * min_blocks(nt, parts) / p.nvs, ctas = room < kMostCtas ? room : kMostCtas;
-    if (!tc && !bytes && m.window < kSeenAll && ctas > 1 && cap > (4 * p.nvs <= sms ? kClusterFrom : kWholeCap) &&
-        cap <= (long long)ctas * (ctas == kMostCtas ? kClusterCapMost : kClusterCap)) {
+    const bool few = 4LL * p.nvs <= sms;
+    const int most = m.window == kSeenAll ? (few ? kClusterCapFew : 0) : ctas == kMostCtas ? kClusterCapMost : kClusterCap;
+    if (!tc && !bytes && ctas > 1 && cap > (few ? kClusterFrom : kWholeCap) && cap <= (long long)ctas * most) {
       p.whole = 1;
       p.ctas = ctas;
       p.lead = 0;
