@@ -825,7 +825,8 @@ AttendPlan make_plan(const AttendArgs& a, const M& m, int parts, int sms, size_t
   if (cost < p.grid) p.grid = (int)cost;
   if constexpr (kPart<M>) {
     // A window bounds what a stream has to see, so a fixed share of it for each CTA of a cluster loses little, and saves
-    // the search for the units and the second kernel; so it does where a table is short and SMs are left over. (The workspace is sized for the other way, whatever is taken here.)
+    // the search for the units and the second kernel; so it does where a table is short and SMs are left over. (The
+    // workspace is sized for the other way, whatever is taken here.)
     const int room = sms * min_blocks(nt, parts) / p.nvs, ctas = room < kMostCtas ? room : kMostCtas;
     const bool few = 4LL * p.nvs <= sms;
     const int most = m.window == kSeenAll ? (few ? kClusterCapFew : 0) : ctas == kMostCtas ? kClusterCapMost : kClusterCap;
