@@ -737,9 +737,14 @@ __global__ void __launch_bounds__(ROWS) combine_tc_kernel(AttendArgs a, AttendPl
         const int c = min(c1 + i, span.y);
         const size_t slot = (size_t)c * 2 + (c == span.x ? 1 : 0);
         ml[i] = p.ml[slot * ROWS + rr];
-        const float* src = p.part + (slot * D + c0) * ROWS + rr;
+        if constexpr (kPart<M>) {
 #pragma unroll
-        for (int e = 0; e < C; ++e) y[i][e] = src[e * ROWS];
+          for (int e = 0; e < C; e += 8) ld_f8(y[i] + e, p.part + slot * D * ROWS + part_at<ROWS>(c0 + e, rr));
+        } else {
+          const float* src = p.part + (slot * D + c0) * ROWS + rr;
+#pragma unroll
+          for (int e = 0; e < C; ++e) y[i][e] = src[e * ROWS];
+        }
       }
 #pragma unroll
       for (int i = 0; i < N; ++i) {

@@ -233,4 +233,22 @@ constexpr int kTcRows = 128, kTcUnit = 128;
 int launch_attend_tc(const AttendArgs& a, const AttendPlan& p, cudaStream_t s);
 int launch_attend_rows(const AttendArgs& a, const AttendPlan& p, const SeenArgs& m, cudaStream_t s);
 
+// Where the tcgen05 kernel under SeenArgs leaves channel k of a part's row: eight channels of a row together, the rows
+// side by side, so that a thread with a row moves 32 bytes at a time and a warp one run of 1 KB (a channel's rows side by
+// side, 4 bytes a thread: 64 drafts x 7 rows 70.5 us and not 69.0, 16 x 5 over 8 x 8 x 32768 123.5 and not 122.3).
+template <int ROWS>
+__device__ __forceinline__ int part_at(int k, int row) {
+  return ((k >> 3) * ROWS + row) * 8 + (k & 7);
+}
+__device__ __forceinline__ void st_f8(float* p, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ void ld_f8(float* v, const float* p) {
+  asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+               : "l"(p));
+}
+
 }  // namespace kvc
