@@ -43,13 +43,19 @@ namespace {
 // share its work; the shares of registers stay within what the block is launched with.
 template <int RT>
 struct Roles;
+constexpr bool fits(int soft, int dec, int soft_regs, int dec_regs, int issue_regs) {  // a split above the launch's total never ends
+  const int warps = soft + dec + 4, regs = 65536 / (32 * warps) / 8 * 8;
+  return soft * soft_regs + dec * dec_regs + 4 * issue_regs <= warps * regs;
+}
 template <>
 struct Roles<1> {  // 896 threads with 72 registers (64512): 2 x 128 x 120 + 4 x 128 x 56 + 128 x 32 = 63488
   static constexpr int kSoft = 8, kDec = 16, kSoftRegs = 120, kDecRegs = 56, kIssueRegs = 32;
+  static_assert(fits(kSoft, kDec, kSoftRegs, kDecRegs, kIssueRegs), "registers");
 };
 template <>
 struct Roles<2> {  // 640 threads with 96 registers (61440): 2 x 128 x 144 + 2 x 128 x 72 + 128 x 48 = 61440
   static constexpr int kSoft = 8, kDec = 8, kSoftRegs = 144, kDecRegs = 72, kIssueRegs = 48;
+  static_assert(fits(kSoft, kDec, kSoftRegs, kDecRegs, kIssueRegs), "registers");
 };
 template <int RT>
 constexpr int kThreadsOf = 32 * (Roles<RT>::kSoft + Roles<RT>::kDec + 4);  // the issuers' warpgroup is not filled
@@ -215,42 +221,77 @@ __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendAr
 
   using std::integral_constant;
   // A part's query rows, by warp `by` of `of`: each is brought to [256, 512) by a power of two, with the scale's sign, so that
-  // maxima of dot products are maxima of logits. D/8 lanes take a row, `most` of their reads are in flight at once: all that
-  // a warp has where the registers are there (a prompt's 1024 tokens 88.3 us with four, 85.6 with sixteen).
-  auto queries = [&](const Stream& x, uint32_t seg, int by, auto of, auto most) {
-    constexpr int kLanes = D / 8, kAt = 32 / kLanes, kQRows = kRows / decltype(of)::value;
-    constexpr int kBatch = kQRows / kAt < decltype(most)::value ? kQRows / kAt : decltype(most)::value;
-    const int i = lane % kLanes;
-#pragma unroll 1
-    for (int g0 = 0; g0 < kQRows; g0 += kBatch * kAt) {
-      const int q0 = by * kQRows + g0 + lane / kLanes;
-      uint4 v[kBatch];
+  // maxima of dot products are maxima of logits. RT = 1: D/8 lanes take a row, all of a warp's reads into registers, under way
+  // before the products on the part before are over. RT = 2: they are four times as many, and are copied to the places of
+  // their 16-byte chunks, all at once; from there four lanes take a row, each every fourth chunk, those of odd rows the second
+  // of two first, so that eight lanes find different banks. (A prompt's 1024 tokens 80.8 us so and 84.6 by registers, four
+  // reads at a time; 16 x 5 rows over 8 x 8 x 32768 124.6 and 123.0.)
+  auto queries = [&](const Stream& x, uint32_t seg, int by, auto of) {
+    static_assert(sizeof(T) == 2, "bf16");
+    constexpr int kQRows = kRows / decltype(of)::value, kChunks = D / 8, kAt = 32 / kChunks;
+    const int q0 = by * kQRows;
+    auto place = [&](int q, int c) { return smem + (q >> 7) * L::kTile + (c >> 3) * L::kHalf + (q & 127) * 128 + (((c & 7) ^ (q & 7)) << 4); };
+    // the row's power of two from its largest magnitude's bits, and what undoes it
+    auto factor = [&](int q, uint32_t top, bool one) {
+      const int ex = max((int)(max(top & 0xffffu, top >> 16) >> 7), 24);
+      if (one) row_f[seg & 1][q] = __uint_as_float((uint32_t)(ex - 8) << 23) * (fabsf(a.scale) * kLog2e);
+      return copysignf(__uint_as_float((uint32_t)(262 - ex) << 23), a.scale);
+    };
+    auto top_of = [](uint32_t top, const uint4& w) {  // two magnitudes at a time: bf16 bits without the sign, in their order
+      constexpr uint32_t m = 0x7fff7fffu;
+      return __vmaxu2(__vmaxu2(top, __vmaxu2(w.x & m, w.y & m)), __vmaxu2(w.z & m, w.w & m));
+    };
+    auto times = [](const uint4& w, float mul) {
+      auto two = [&](uint32_t v) { return pack2(__uint_as_float(v << 16) * mul, __uint_as_float(v & 0xffff0000u) * mul); };
+      return make_uint4(two(w.x), two(w.y), two(w.z), two(w.w));
+    };
+    auto from = [&](int q, int c) { return static_cast<const T*>(a.q) + (q < x.rows ? q_row(a, p, x, x.r0 + q) : 0) + 8 * c; };
+    // the products on the part before read its queries no more
+    auto free = [&] { return seg == 0 || wait(&bars.q_empty, (seg - 1) & 1); };
+    if constexpr (RT == 1) {
+      const int c = lane % kChunks;
+      uint4 v[kQRows / kAt];
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const int q = q0 + k * kAt;
+      for (int k = 0; k < kQRows / kAt; ++k) {
+        const int q = q0 + k * kAt + lane / kChunks;
         v[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (q < x.rows)
-          v[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + q_row(a, p, x, x.r0 + q)) + i);
+        if (q < x.rows) v[k] = __ldg(reinterpret_cast<const uint4*>(from(q, c)));
       }
-      // the products on the part before read its queries no more
-      if (g0 == 0 && seg > 0 && !wait(&bars.q_empty, (seg - 1) & 1)) return false;
+      if (!free()) return false;
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const int q = q0 + k * kAt;
-        const T* e = reinterpret_cast<const T*>(&v[k]);
-        float mx = 0.f;
+      for (int k = 0; k < kQRows / kAt; ++k) {
+        const int q = q0 + k * kAt + lane / kChunks;
+        uint32_t top = top_of(0u, v[k]);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) mx = fmaxf(mx, fabsf(to_f32(e[c])));
+        for (int o = kChunks / 2; o; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(kFull, top, o));
+        *reinterpret_cast<uint4*>(place(q, c)) = times(v[k], factor(q, top, c == 0));
+      }
+    } else {
+      if (!free()) return false;
+#pragma unroll 4
+      for (int k = 0; k < kQRows; k += kAt) {
+        const int q = q0 + k + lane / kChunks, c = lane % kChunks;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(tc::smem_u32(place(q, c))), "l"(from(q, c)),
+                     "r"(q < x.rows ? 16 : 0)
+                     : "memory");
+      }
+      asm volatile("cp.async.wait_all;\n" ::: "memory");
+      __syncwarp();
+#pragma unroll 2
+      for (int k = 0; k < kQRows; k += 8) {
+        const int q = q0 + k + lane / 4, c0 = lane & 3;
+        uint4 v[kChunks / 4];
+        uint32_t top = 0;
 #pragma unroll
-        for (int c = kLanes / 2; c; c >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, c));
-        const int ex = max((int)(__float_as_uint(mx) >> 23), 24);
-        const float mul = copysignf(__uint_as_float((uint32_t)(262 - ex) << 23), a.scale);
-        if (i == 0) row_f[seg & 1][q] = __uint_as_float((uint32_t)(ex - 8) << 23) * (fabsf(a.scale) * kLog2e);
-        uint32_t o[4];
+        for (int j = 0; j < kChunks / 4; ++j) {
+          v[j] = *reinterpret_cast<const uint4*>(place(q, c0 + 4 * (j ^ (q & 1))));
+          top = top_of(top, v[j]);
+        }
+        top = __vmaxu2(top, __shfl_xor_sync(kFull, top, 1));
+        top = __vmaxu2(top, __shfl_xor_sync(kFull, top, 2));
+        const float mul = factor(q, top, c0 == 0);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) o[c] = pack2(to_f32(e[2 * c]) * mul, to_f32(e[2 * c + 1]) * mul);
-        *reinterpret_cast<uint4*>(smem + (q >> 7) * L::kTile + (i >> 3) * L::kHalf + (q & 127) * 128 +
-                                  (((i & 7) ^ (q & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        for (int j = 0; j < kChunks / 4; ++j) *reinterpret_cast<uint4*>(place(q, c0 + 4 * (j ^ (q & 1)))) = times(v[j], mul);
       }
     }
     fence_async();
@@ -442,7 +483,7 @@ __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendAr
       load(v0, ok0, ua);
       if (RT == 1) load(v1, ok1, ua + 1);
       // the first part's are the softmax warps' work
-      if (seg > 0 && !queries(x, seg, dw, integral_constant<int, kDecWarps>(), integral_constant<int, 4>())) return false;
+      if (seg > 0 && !queries(x, seg, dw, integral_constant<int, kDecWarps>())) return false;
       ++seg;
       for (int u = ua; u < ub; u += RT == 1 ? 2 : 1) {
         if (!decode(v0, ok0)) return false;
@@ -463,7 +504,7 @@ __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendAr
     uint32_t n = 0, seg = 0;  // units so far
     parts([&](const Stream& x, int vs, int ua, int ub, int U, int base) {
       const int m = ub - ua;
-      if (seg == 0 && !queries(x, 0, warp, integral_constant<int, kSoftWarps>(), integral_constant<int, 16>())) return false;
+      if (seg == 0 && !queries(x, 0, warp, integral_constant<int, kSoftWarps>())) return false;
       int lim = x.vis, lo = 0;
       if (rr < x.rows) {
         const RowSeen y = row_seen(a, p, seen, x, x.r0 + rr);
