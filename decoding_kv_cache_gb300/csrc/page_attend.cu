@@ -809,10 +809,10 @@ AttendPlan make_plan(const AttendArgs& a, const M& m, int parts, int sms, size_t
   p.lead = tc ? kTcLead : kLead;
   p.rb = tc ? kTcRows : 8 * nt;
   if (kPart<M> && tc) {
-    // A block of 256 rows takes as long as 1.75 of 128: a prompt's 4096 rows 88 us and 101, 448 rows 70 and 79, 256 rows
-    // 48.9 and 49.8, but 260 rows (two blocks for three) 70.5 and 63.9.
+    // A block of 256 rows takes as long as some 1.6 of 128: a prompt's 4096 rows 80.7 us and 101, 448 rows 65.5 and 77.7, 256
+    // rows 42.8 and 46.4, 640 rows (three blocks for five) 94.4 and 99.8, but 384 rows (two for three) 65.7 and 64.2.
     const int n1 = (R + kTcRows - 1) / kTcRows, n2 = (n1 + 1) / 2;
-    if (7LL * n2 < 4LL * n1)
+    if (8LL * n2 < 5LL * n1)
       p.rb = 2 * kTcRows;
     else
       p.lead = kTcLeadPart;

@@ -6,7 +6,7 @@
 // fp16 by a power of two per row (bf16 values exact from 2^-25 of the row's largest on, below that off by at most 2^-33
 // of it); a probability is rounded to fp16 once, 2^-11 relative against the bf16 output's 2^-8.
 //
-//   decoders  a part's query rows to fp16 (the first part's are the softmax warps' work); then half of the warps K, half V:
+//   decoders  a part's query rows to fp16 (the first part's are the softmax warps' work), for RT = 2 in place; then half of the warps K, half V:
 //             codes and scales from global memory straight to registers ahead of time, four lanes a token, and as fp16
 //             into the 128-byte-swizzled tiles (two stages each). V's tile [token][channel] is the second product's B
 //             operand as it lies (MN-major).
@@ -28,7 +28,7 @@
 // tensor memory 400, 64 exponentials and what belongs to them 1000, P back and handed on 600) at 0.72 of the SM's issue
 // (80 rows over 64 x 32768 tokens: 124 us, 0.36 of the copy peak, 0.36 of the tensor peak on the rows there are). RT = 2:
 // some 3500 cycles a unit of 256 rows, 2048 of them the tensor cores': a tile's softmax (1700) and its products (1400) take
-// turns, the other tile's lie beside them (a prompt's 1024 tokens under a window of 2048, 2 x 8 heads: 88 us, 0.41 of the
+// turns, the other tile's lie beside them (a prompt's 1024 tokens under a window of 2048, 2 x 8 heads: 81 us, 0.45 of the
 // tensor peak). At each CTA's beginning 5 us, at its end and between two parts some 3 us.
 //
 // All waits are bounded; a role that gives up raises KVC_STATUS_TIMEOUT and the others follow.
