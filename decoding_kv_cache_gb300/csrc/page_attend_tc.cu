@@ -45,7 +45,8 @@ struct Lay {
 
 struct Bars {
   uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[kTiles], k_empty[kTiles], v_full[kTiles], v_empty[kTiles];
-  uint64_t s_full[2], p_full[2][2], pv_done[2], q_full, merge, drain;  // p_full: S buffer, group (a group may be a unit ahead)
+  uint64_t s_full[2], p_full[2][2], pv_done[2], part_done[2];  // p_full: S buffer, group (a group may be a unit ahead)
+  uint64_t q_full, merge, drain;
 };
 
 // A token's codes and scales to a row of fp16 in the swizzled tile; zero: the row stands for nothing.
@@ -105,6 +106,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
       // test-only fault (kvc_debug_fault 2): the first CTA's second unit waits for an arrival that nothing makes
       tc::mbar_init(&bars.s_full[i], a.fault && blockIdx.x == 0 && i == 1 ? 2 : 1);
       tc::mbar_init(&bars.pv_done[i], 1);
+      tc::mbar_init(&bars.part_done[i], 1);
       tc::mbar_init(&bars.p_full[i][0], 4);
       tc::mbar_init(&bars.p_full[i][1], 4);
     }
@@ -231,6 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
                 umma_ts(tmem + kColO + w * 128, tmem + t * 128 + w * kHalfTok + 8 * j, d + j * (2048 >> 4), id_pv,
                         i > 1 || j > 0);
               tc::umma_commit(&bars.pv_done[w]);
+              if (i == m) tc::umma_commit(&bars.part_done[w]);
             }
             __syncwarp();
           }
@@ -427,15 +430,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs a, At
         l += (l2.x + l2.y) + (l3.x + l3.y);
         tmem_st_wait();
         tc::fence_before_sync();
-        // The part's end waits for this unit's P V. A wait for a phase's parity tells it from the phase two before only
-        // once that before it is over, and a group may be a unit ahead of the issuer: so that one is waited for here, while
-        // this one cannot be over.
-        if (i > 0 && i == m - 1 && !wait(&bars.pv_done[w], (n - 1) & 1)) return false;
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.p_full[n & 1][w]);
       }
-      // ---- the groups' results together
-      if (!wait(&bars.pv_done[w], (n - 1) & 1)) return false;
+      // ---- the groups' results together. A wait for a phase's parity tells it from the phase two before only once the one
+      // between is over, and this group may be a unit ahead of the issuer: a barrier of its own, once a part.
+      if (!wait(&bars.part_done[w], seg >> 1 & 1)) return false;  // seg counts the merges, two a part
       tc::fence_after_sync();
       row_ml[w][rr] = make_float2(ref, l);
       tc::fence_before_sync();
