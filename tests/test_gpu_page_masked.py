@@ -704,6 +704,34 @@ def test_rows_around_a_block(D, G, T):
     x.check(window=513)
 
 
+@pytest.mark.parametrize("D,T", [(128, 120), (64, 70), (128, 45)])
+def test_uneven_query_rows_in_several_parts_a_cta(D, T):
+    """Blocks of 256 and of 128 rows, more streams than CTAs have whole: rows of very different magnitudes, of none, strided,
+    scaled by less than zero; and a row that is no number, which is no other row's matter."""
+    rng = np.random.default_rng(T)
+    B, Hkv, G = 12, 8, 2
+    lens = rng.integers(T, 400, B * Hkv)
+    lens[:3] = T, 1, 0
+    x, q0 = make_attend("bf16", D, B, Hkv, G, T, 64, lens.tolist(), seed=T)
+    up2 = 2.0 ** rng.integers(-30, 3, (B, T, G * Hkv, 1)) * 2.0 ** rng.integers(-12, 1, D)
+    q0 = (q0.double() * torch.from_numpy(up2)).to(q0.dtype)  # powers of two: exact
+    q0[:, 3] = 0
+    q0[1, :, 1] = 0
+    wide = torch.full((B, T, G * Hkv + 3, D), 7.0, dtype=torch.bfloat16, device=DEV)
+    wide[:, :, 1:-2] = q0.to(DEV)
+    qd = wide[:, :, 1:-2]
+    mask, depth, _ = Q.tree_mask(Q.random_trees(rng, B, T))
+    check(x, q0, "bf16", scale=0.5, mask=mask, depth=depth, q_dev=qd)
+    out, lse = check(x, q0, "bf16", scale=-0.5, window=150, sinks=5, q_dev=qd)
+    b, t, h = 5, T - 1, 6
+    qd[b, t, h, 3] = float("nan")
+    got, gl = torch.full_like(out, -55.0), torch.full_like(lse, -55.0)
+    kvc_().kvc_page_attend_masked(x.pool, x.pages, qd, got, window=150, sinks=5, scale=-0.5, lse=gl, status=x.status)
+    assert got[b, t, h].isnan().all() and gl[b, t, h].isnan()
+    got[b, t, h], gl[b, t, h] = out[b, t, h], lse[b, t, h]
+    assert torch.equal(got, out) and torch.equal(gl, lse) and int(x.status.item()) == 0
+
+
 @pytest.mark.parametrize("dt,D,T,w", [("bf16", 128, 1, 100), ("bf16", 128, 1, 1500), ("bf16", 64, 3, 40000), ("f32", 128, 2, 20000),
                                       ("bf16", 128, 24, 30000), ("bf16", 64, 24, 30000), ("bf16", 128, 80, 30000)])
 def test_a_wait_that_runs_out(dt, D, T, w):
