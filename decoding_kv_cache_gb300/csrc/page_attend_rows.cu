@@ -80,6 +80,18 @@ struct Lay {
   static constexpr int bytes = oV + kTiles * kTile + 1024;
 };
 
+// A wait for a phase's parity tells that phase from the one two before or two behind it only where the barrier cannot be that
+// far from it. Why it cannot, parts of one unit included (tests/barrier_model.py runs all of them in any order):
+//   k_full, v_full   a stage is filled again only when it is free, and it is so by the products that the waiting issuer issues
+//   s_full           by stage (RT = 2: by row tile, and the second's by stage): the next S there needs the waiting softmax
+//                    warps' P, and for the K decoders, who take it for "the tile is free", their next keys
+//   v_empty          the next products on a stage need those who wait for this: its V decoders, its softmax and, RT = 1, its
+//                    Q K; and Q K of a unit is issued when the unit two before is over, so the softmax finds at most one open
+//   p_full, pv_done  the next phase needs an S that the waiting issuer issues; a product on the waiting softmax warps' next P
+//   merge            all who wait arrive at every phase
+//   q_full           who issues Q K waits for it, and the next phase needs q_empty, its own commit. P V reads no queries, and
+//                    while it waits for a P those of two more parts may come: who issues P V does not wait for q_full.
+//   q_empty          every decoder warp waits for it, and only then arrives at the q_full that the next phase needs
 struct Bars {
   uint64_t k_full[kTiles], v_full[kTiles], v_empty[kTiles];
   // RT = 1: by S buffer, which is the tile's stage; 2: of the first row tile, and of the second by the stage. The last one
@@ -331,7 +343,7 @@ __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendAr
     };
     parts([&](const Stream&, int, int ua, int ub, int, int) {
       const int m = ub - ua;
-      if (!wait(&bars.q_full, seg++ & 1)) return false;
+      if ((RT == 2 || iw == 0) && !wait(&bars.q_full, seg++ & 1)) return false;
       if constexpr (RT == 2) {
         for (int i = 0; i <= m; ++i) {  // unit i - 1's second product and unit i's first, a row tile after the other
           const int tk = nk & 1, tv = nv & 1;

@@ -1,0 +1,110 @@
+"""Serving batches of short streams: many of them for every CTA of the tcgen05 kernels, whose roles are then parts apart.
+Against the definition in 64 bits, formed for whole batches on the GPU, within page_util.tolerances."""
+import numpy as np
+import pytest
+import torch
+
+import page_util as R
+import tree_util as Q
+from test_gpu_page import DEV, up
+from test_gpu_page_masked import Made, kvc_
+
+pytestmark = pytest.mark.gpu
+
+
+def seen_by_all(lens, nq, T, N, window, sinks, mask=None, depth=None):
+    """[B, Hkv, T, N]: query i of sequence b sees token j of a stream; lens [B, Hkv], nq [B], mask and depth numpy."""
+    lens, nq = torch.from_numpy(lens).to(DEV), torch.from_numpy(nq).to(DEV)
+    B = lens.shape[0]
+    j, i = torch.arange(N, device=DEV), torch.arange(T, device=DEV)
+    base = (lens - nq[:, None])[..., None, None]
+    d = i.expand(B, T) if depth is None else torch.minimum(up(depth).long().clamp(min=0), nq[:, None] - 1)
+    pos = base + d[:, None, :, None]
+    near = (j < sinks) | (j > pos - window) if window else torch.ones((1, 1, 1, N), dtype=torch.bool, device=DEV)
+    u = (j - base).expand(B, lens.shape[1], 1, N)
+    if mask is None:
+        own = near & (u <= i[:, None])
+    else:
+        words = torch.from_numpy(np.ascontiguousarray(mask).view(np.uint32).astype(np.int64)).to(DEV)
+        bits = (words[..., None] >> torch.arange(32, device=DEV) & 1).flatten(2)[:, :, :T] > 0  # [B, T, T]
+        own = torch.gather(bits[:, None].expand(B, lens.shape[1], T, T), 3, u.clamp(0, T - 1).expand(-1, -1, T, -1))
+    there = (j < lens[..., None, None]) & (i[:, None] < nq[:, None, None, None])
+    return there & torch.where(u < 0, near, own)
+
+
+def check(x, window=0, sinks=0, mask=None, depth=None, n_q=None, causal=False):
+    """One call on a Made cache. Returns out, lse."""
+    kvc = kvc_()
+    q = x.q
+    B, T, Hq, D = q.shape
+    Hkv = x.lens.shape[1]
+    out, lse = torch.full_like(q, -55.0), torch.full(q.shape[:3], -55.0, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    dev = lambda v: None if v is None else up(np.asarray(v, np.int32))
+    if causal:
+        kvc.kvc_page_attend(x.pool, x.pages, q, out, lse=lse, n_q=dev(n_q), status=status)
+    else:
+        kvc.kvc_page_attend_masked(x.pool, x.pages, q, out, window=window, sinks=sinks, mask=dev(mask), depth=dev(depth), lse=lse,
+                                   n_q=dev(n_q), status=status)
+    assert int(status.item()) == 0
+    nq = np.array([Q.drafts(n_q, b, T) for b in range(B)])
+    N = x.K.shape[3]
+    seen = seen_by_all(x.lens, nq, T, N, window, sinks, mask, depth)
+    r = np.random.default_rng(T)
+    for _ in range(20):  # the batch's rule against the model's, one query at a time
+        b, h = int(r.integers(B)), int(r.integers(Hkv))
+        if nq[b]:
+            i = int(r.integers(nq[b]))
+            one = Q.seen_tokens(int(x.lens[b, h]), int(nq[b]), i, window, sinks, None if mask is None else mask[b, i],
+                                None if depth is None else depth[b])
+            np.testing.assert_array_equal(torch.nonzero(seen[b, h, i]).view(-1).cpu().numpy(), one)
+    behind = torch.arange(T, device=DEV) >= torch.from_numpy(nq).to(DEV)[:, None]
+    assert (out[behind] == -55.0).all() and (lse[behind] == -55.0).all(), "rows behind the last query"
+    for b0 in range(0, B, 16):
+        s = slice(b0, min(B, b0 + 16))
+        qq = q[s].double().unflatten(2, (Hkv, -1)).transpose(1, 2)  # [b, Hkv, T, G, D]
+        k, v, see = x.K[0, s].double(), x.V[0, s].double(), seen[s][:, :, :, None]
+        far = lambda z, other: torch.where(see, z, other)
+        z = far(torch.einsum("bhtgd,bhnd->bhtgn", qq, k) / D ** 0.5, -torch.inf)
+        lz = torch.logsumexp(z, -1)
+        p = torch.exp(z - torch.where(torch.isinf(lz), 0.0, lz)[..., None])
+        live = torch.arange(N, device=DEV) < torch.from_numpy(x.lens[s]).to(DEV)[..., None]
+        ref = dict(out=torch.einsum("bhtgn,bhnd->bhtgd", p, v), lse=lz, mass=torch.einsum("bhtgn,bhnd->bhtgd", p, v.abs()),
+                   vmax=(v.abs() * live[..., None]).amax(2)[:, :, None, None] + 0 * qq,
+                   logit=far(torch.einsum("bhtgd,bhnd->bhtgn", qq.abs(), k.abs()) / D ** 0.5, 0.0).amax(-1))
+        ref = {name: y.transpose(1, 2).flatten(2, 3).cpu().numpy() for name, y in ref.items()}  # [b, T, Hq, .]
+        tol, ltol = R.tolerances(x.dt, int(x.lens.max()), D, ref)
+        there = ~behind[s].cpu().numpy()[..., None]
+        got, gl = out[s].double().cpu().numpy(), lse[s].double().cpu().numpy()
+        err = np.where(there[..., None], np.abs(got - ref["out"]), 0.0)
+        assert (err <= tol).all(), (b0, "out", float((err / tol).max()))
+        empty = np.isneginf(ref["lse"]) & there
+        assert (np.isneginf(gl) == empty).all() and (got[empty] == 0).all()
+        le = np.abs(np.where(there & ~empty, gl, 0.0) - np.where(there & ~empty, ref["lse"], 0.0))
+        assert (le <= ltol).all(), (b0, "lse", float((le / ltol).max()))
+    return out, lse
+
+
+def one_exponent(q):
+    """The rows with their largest magnitude in [4, 8): they are all brought to fp16 by the same power of two."""
+    q.clamp_(-3.75, 3.75)
+    q[..., 5] = torch.where(q[..., 5] < 0, -4.0, 4.0)
+
+
+@pytest.mark.parametrize("D,G,T,B,n", [(128, 4, 5, 75, 128), (64, 4, 32, 188, 128), (128, 1, 17, 188, 100), (64, 8, 3, 75, 60)])
+def test_four_and_ten_streams_of_one_unit_a_cta(D, G, T, B, n):
+    """600 and 1504 streams of at most 128 tokens, a work unit each: a CTA's roles are several streams apart."""
+    rng = np.random.default_rng(B + T)
+    lens = rng.integers(1, n + 1, B * 8)
+    lens[::50] = n
+    lens[7::40] = 0
+    x = Made("bf16", D, B, 8, G, T, 16, lens, B + T)
+    one_exponent(x.q)
+    mask, depth, _ = Q.tree_mask(Q.random_trees(rng, B, T))
+    a = check(x, mask=mask, depth=depth)
+    for _ in range(3):  # the same again, bit for bit
+        b = check(x, mask=mask, depth=depth)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    check(x, window=40, sinks=3)
+    check(x, window=60, sinks=0, mask=mask, depth=depth)
+    check(x, causal=True)
