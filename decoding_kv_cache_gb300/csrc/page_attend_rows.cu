@@ -152,7 +152,11 @@ __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendAr
   __shared__ uint64_t unit_ok[4];  // a byte a K warp: its blocks
   __shared__ int sm_scan[kThreads / 32], sm_first[2];
   __shared__ int abort_flag, parts_done[2];
-  __shared__ float row_f[2][kRows];  // of this part and the next
+  // The rows' factors, by part. When those of part s are written, its predecessor's last Q K is over. RT = 2: before that Q K
+  // was issued, part s - 2's last P was there, so its factors had been read: two parts' are alive. RT = 1: the P of the unit two
+  // before was, which in parts of one unit is part s - 3's: three are alive.
+  constexpr int kFactors = RT == 1 ? 4 : 2;
+  __shared__ float row_f[kFactors][kRows];
   __shared__ float2 row_ml[RT == 1 ? 2 : 1][128];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -246,7 +250,7 @@ __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendAr
     // the row's power of two from its largest magnitude's bits, and what undoes it
     auto factor = [&](int q, uint32_t top, bool one) {
       const int ex = max((int)(max(top & 0xffffu, top >> 16) >> 7), 24);
-      if (one) row_f[seg & 1][q] = __uint_as_float((uint32_t)(ex - 8) << 23) * (fabsf(a.scale) * kLog2e);
+      if (one) row_f[seg % kFactors][q] = __uint_as_float((uint32_t)(ex - 8) << 23) * (fabsf(a.scale) * kLog2e);
       return copysignf(__uint_as_float((uint32_t)(262 - ex) << 23), a.scale);
     };
     auto top_of = [](uint32_t top, const uint4& w) {  // two magnitudes at a time: bf16 bits without the sign, in their order
@@ -536,7 +540,7 @@ __global__ void __launch_bounds__(kThreadsOf<RT>, 1) attend_rows_kernel(AttendAr
         if (!(RT == 2 && w == 0 ? wait(&bars.s_full[0], n & 1) : wait(&bars.s_full[RT - 1 + (n & 1)], (n >> 1) & 1))) return false;
         tc::fence_after_sync();
         // the factors were written before q_full, which precedes every s_full
-        if (i == 0) f = *reinterpret_cast<volatile float*>(&row_f[seg & 1][rr]);
+        if (i == 0) f = *reinterpret_cast<volatile float*>(&row_f[seg % kFactors][rr]);
         // the unit's blocks that are there: one or two a byte, nearly always all
         using Word = typename std::conditional<kDecWarps == 16, uint64_t, uint32_t>::type;
         const Word by = *reinterpret_cast<volatile Word*>(&unit_ok[n & 3]);

@@ -82,8 +82,9 @@ class Cta:
         return self.faults
 
 
-def rows128(parts, pv_waits_for_queries=False):
-    """attend_rows_kernel, 128 rows: two issuers, S double-buffered. parts: the units of a CTA's parts."""
+def rows128(parts, pv_waits_for_queries=False, factors=4):
+    """attend_rows_kernel, 128 rows: two issuers, S double-buffered. parts: the units of a CTA's parts; factors: the places
+    for rows' factors."""
     c = Cta(parts)
     dec, soft = 2, 2  # warps of K and of V, and of each softmax group
     c.bars(k_full=(2, dec), v_full=(2, dec), v_empty=(2, 1), s_full=(2, 1), p_full=(2, 2 * soft), q_full=2 * dec, q_empty=1, merge=2 * soft)
@@ -93,6 +94,7 @@ def rows128(parts, pv_waits_for_queries=False):
             yield ("wait", c.q_empty, seg - 1)
         yield ("step",)
         c.put("q", seg)
+        c.put(("f", seg % factors), seg)
         c.q_full.arrive()
 
     def decoder(kv, one):
@@ -154,6 +156,8 @@ def rows128(parts, pv_waits_for_queries=False):
             for i in range(m):
                 t = n & 1
                 yield ("wait", c.s_full[t], n >> 1)
+                if i == 0:
+                    c.look(("f", seg % factors), seg, "factors")
                 if c.held.get(("s", t)) != ("p", n):  # the other warps' columns may be P by now
                     c.look(("s", t), n, "s")
                 c.look(("ok", n & 3), n, "unit_ok")
@@ -179,7 +183,7 @@ def rows128(parts, pv_waits_for_queries=False):
     return c
 
 
-def rows256(parts):
+def rows256(parts, factors=2):
     """attend_rows_kernel, 256 rows: one issuer, a softmax group a row tile, the next unit's S over this one's P."""
     c = Cta(parts)
     dec, soft = 2, 2
@@ -190,6 +194,7 @@ def rows256(parts):
             yield ("wait", c.q_empty, seg - 1)
         yield ("step",)
         c.put("q", seg)
+        c.put(("f", seg % factors), seg)
         c.q_full.arrive()
 
     def decoder(kv, one):
@@ -246,6 +251,8 @@ def rows256(parts):
                 yield from queries(0)
             for i in range(m):
                 yield ("wait", c.s_full[1 + (n & 1)], n >> 1) if w else ("wait", c.s_full[0], n)
+                if i == 0:
+                    c.look(("f", seg % factors), seg, "factors")
                 if c.held.get(("s", w)) != ("p", n):
                     c.look(("s", w), n, "s")
                 c.look(("ok", n & 3), n, "unit_ok")

@@ -41,3 +41,11 @@ def test_a_part_s_end_by_its_last_product_s_phase():
     take the product before the last for it."""
     wrong = lambda parts: M.causal(parts, end_by_product=True)
     assert "phase" in faults(wrong, [2] * 4, 60) or "phase" in faults(wrong, [3, 3, 3], 60)
+
+
+def test_places_for_the_factors():
+    """Three parts' factors are alive in the 128-row kernel where parts have one unit, two in the other."""
+    assert "factors" in faults(lambda parts: M.rows128(parts, factors=2), [1] * 6, 40)
+    assert not faults(lambda parts: M.rows128(parts, factors=3), [1] * 8, 40)
+    assert not faults(lambda parts: M.rows128(parts, factors=2), [2] * 4, 40)
+    assert "factors" in faults(lambda parts: M.rows256(parts, factors=1), [1] * 6, 40)

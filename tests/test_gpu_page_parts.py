@@ -108,3 +108,77 @@ def test_four_and_ten_streams_of_one_unit_a_cta(D, G, T, B, n):
     check(x, window=40, sinks=3)
     check(x, window=60, sinks=0, mask=mask, depth=depth)
     check(x, causal=True)
+
+
+def uneven(q, rng):
+    """Rows times powers of two that differ from sequence to sequence, token to token and head to head (exact): each has
+    another factor."""
+    B, T, Hq, _ = q.shape
+    two = 2.0 ** rng.integers(-7, 2, (B, T, Hq, 1)) * 2.0 ** rng.integers(-4, 2, (B, 1, 1, 1))
+    q.copy_((q.double() * torch.from_numpy(two).to(DEV)).to(q.dtype))
+
+
+@pytest.mark.parametrize("D,G,T,B,n,w", [
+    (128, 4, 5, 75, 128, 40), (128, 4, 5, 188, 128, 60), (64, 4, 32, 75, 128, 100), (64, 2, 60, 188, 128, 30), (128, 3, 6, 188, 128, 7),
+    (128, 4, 65, 25, 128, 100), (64, 1, 257, 66, 128, 60), (128, 6, 64, 25, 128, 128),  # three blocks a stream
+    (128, 4, 9, 100, 256, 50), (64, 4, 65, 30, 256, 200), (128, 8, 16, 130, 300, 150), (64, 5, 7, 90, 520, 260)])  # one unit to five
+def test_uneven_rows_of_many_short_streams(D, G, T, B, n, w):
+    """Streams of one unit and of a few, 600 to 1584 row blocks: four to ten a CTA. Every row has its own factor, sequences
+    have all, some or none of their queries, streams hold more tokens than the window or fewer than the queries, or none."""
+    rng = np.random.default_rng(B * T)
+    lens = rng.integers(1, n + 1, B * 8)
+    lens[::5] = n
+    lens[3::40] = 0
+    lens[5::30] = rng.integers(1, 5)
+    x = Made("bf16", D, B, 8, G, T, 64, lens, B + T)
+    uneven(x.q, rng)
+    n_q = rng.integers(0, T + 1, B)
+    n_q[::3] = T
+    mask, depth, _ = Q.tree_mask(Q.random_trees(rng, B, T))
+    check(x, mask=mask, depth=depth)
+    check(x, mask=mask, depth=depth, n_q=n_q)
+    check(x, window=w, sinks=5, n_q=n_q)
+    check(x, window=w, sinks=0, mask=mask, depth=depth, n_q=n_q)
+    check(x, causal=True, n_q=n_q)
+
+
+@pytest.mark.parametrize("D,G,T,B,n,w", [(128, 4, 5, 100, 1500, 40), (64, 4, 32, 90, 1100, 30), (128, 4, 65, 30, 1200, 60), (128, 2, 100, 80, 900, 20)])
+def test_windows_of_a_few_tokens_over_longer_streams(D, G, T, B, n, w):
+    """A row block sees a unit or two of streams that are longer, blocks of 256 rows among them."""
+    rng = np.random.default_rng(B + T)
+    x = Made("bf16", D, B, 8, G, T, 64, rng.integers(1, n + 1, B * 8), B * T)
+    uneven(x.q, rng)
+    mask, depth, _ = Q.tree_mask(Q.random_trees(rng, B, T), window=w)
+    check(x, window=w, sinks=3)
+    check(x, window=w, sinks=0, mask=mask, depth=depth, n_q=rng.integers(0, T + 1, B))
+
+
+def test_captured_and_replayed_with_new_lengths():
+    """768 streams of other lengths and queries at each replay, an eager call on the same workspace between."""
+    kvc, rng = kvc_(), np.random.default_rng(1)
+    B, T, G, D, n = 96, 6, 4, 128, 256
+    x = Made("bf16", D, B, 8, G, T, 64, [n] * (B * 8), 1)
+    mask, depth, _ = Q.tree_mask(Q.random_trees(rng, B, T))
+    first, q, m, d = x.q, x.q.clone(), up(mask), up(depth)
+    out, lse, status = torch.zeros_like(q), torch.zeros(q.shape[:3], device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    ws = torch.empty(kvc.kvc_page_attend_masked_workspace_size(x.pool, x.pages, 8 * G, T), dtype=torch.uint8, device=DEV)
+    call = lambda: kvc.kvc_page_attend_masked(x.pool, x.pages, q, out, mask=m, depth=d, lse=lse, status=status, workspace=ws)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for _ in range(5):
+        x.lens = rng.integers(0, n + 1, (B, 8))
+        x.pages.len.copy_(up(x.lens.astype(np.int32)[None]))
+        q.copy_(first)
+        uneven(q, rng)
+        x.q = q.clone()
+        graph.replay()
+        torch.cuda.synchronize()
+        o, l = check(x, mask=mask, depth=depth)
+        assert torch.equal(o, out) and torch.equal(l, lse) and int(status.item()) == 0
+        kvc.kvc_page_attend_masked(x.pool, x.pages, q, torch.empty_like(q), window=50, sinks=2, status=status, workspace=ws)
