@@ -151,6 +151,13 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _i32(n, what: str) -> int:
+    """A whole number for an int32 argument: of a larger one ctypes would keep the low bits."""
+    if not -0x80000000 <= n <= 0x7fffffff:
+        raise ValueError(f"{what} must fit 32 bits")
+    return n
+
+
 def _dtype_code(t: torch.Tensor) -> int:
     if t.dtype == torch.bfloat16:
         return KVC_BF16
@@ -175,8 +182,8 @@ class Cache:
         self.layers_K, self.layers_V = Ks, Vs
         self._kp = (C.c_void_p * len(Ks))(*[t.data_ptr() for t in Ks])
         self._vp = (C.c_void_p * len(Vs))(*[t.data_ptr() for t in Vs])
-        self.c = kvc_cache(dtype=_dtype_code(Ks[0]), L=len(Ks), B=B, Hq=Hq, Hkv=Hkv, D=D,
-                           N=ncap if N is None else N, pad_=0, ncap=ncap,
+        self.c = kvc_cache(dtype=_dtype_code(Ks[0]), L=len(Ks), B=B, Hq=_i32(Hq, "Hq"), Hkv=Hkv, D=D,
+                           N=ncap if N is None else _i32(N, "N"), pad_=0, ncap=ncap,
                            K=C.cast(self._kp, C.POINTER(C.c_void_p)), V=C.cast(self._vp, C.POINTER(C.c_void_p)))
 
     @property
@@ -217,21 +224,21 @@ def kvc_append(q_pre: torch.Tensor, qbuf: torch.Tensor, count: torch.Tensor, q_r
 
 
 def kvc_score_workspace_size(cache: Cache, n_r: int, n_b: int) -> int:
-    return int(lib().kvc_score_workspace_size(cache.ref, n_r, n_b))
+    return int(lib().kvc_score_workspace_size(cache.ref, _i32(n_r, "n_r"), _i32(n_b, "n_b")))
 
 
 def kvc_evict_workspace_size(cache: Cache, n_r: int, n_b: int) -> int:
-    return int(lib().kvc_evict_workspace_size(cache.ref, n_r, n_b))
+    return int(lib().kvc_evict_workspace_size(cache.ref, _i32(n_r, "n_r"), _i32(n_b, "n_b")))
 
 
 def kvc_evict_launch_count(cache: Cache, n_r: int, n_b: int) -> int:
-    return int(lib().kvc_evict_launch_count(cache.ref, n_r, n_b))
+    return int(lib().kvc_evict_launch_count(cache.ref, _i32(n_r, "n_r"), _i32(n_b, "n_b")))
 
 
 def kvc_debug_fault(mode: int) -> None:
     """Test-only fault switch (see include/kvc.h): 1 makes the scoring exchange wait run out, 2 a wait of
     the paged attention."""
-    _check(lib().kvc_debug_fault(int(mode)))
+    _check(lib().kvc_debug_fault(_i32(int(mode), "mode")))
 
 
 def make_opts(row_agg: str = "max", group_agg: str = "max", head_budget: str = "given",
@@ -262,8 +269,9 @@ def kvc_score(cache: Cache, q_recent: torch.Tensor, qbuf: torch.Tensor, count: t
     n_r, qmax = q_recent.shape[-2], qbuf.shape[-2]
     ws = _workspace(kvc_score_workspace_size(cache, n_r, n_b), scores.device, workspace)
     o = make_opts(row_agg, group_agg, "given", entropy, kernel)
-    _check(lib().kvc_score(cache.ref, _p(q_recent), n_r, _p(qbuf), _p(count), qmax, n_b, int(t), float(rope_theta),
-                           _p(scores), _p(beacon_picks), _opts_ref(o), _p(ws), ws.numel() * ws.element_size(),
+    _check(lib().kvc_score(cache.ref, _p(q_recent), n_r, _p(qbuf), _p(count), qmax, _i32(n_b, "n_b"), int(t),
+                           float(rope_theta), _p(scores), _p(beacon_picks), _opts_ref(o), _p(ws),
+                           ws.numel() * ws.element_size(),
                            _stream(stream)))
 
 
@@ -275,7 +283,7 @@ def kvc_score_static(cache: Cache, q_recent: torch.Tensor, qbuf: torch.Tensor, c
     see kvc.h for the size limit and the sharing rules)."""
     n_r, qmax = q_recent.shape[-2], qbuf.shape[-2]
     o = make_opts(row_agg, group_agg, "given", entropy, kernel)
-    _check(lib().kvc_score_static(cache.ref, _p(q_recent), n_r, _p(qbuf), _p(count), qmax, n_b, int(t),
+    _check(lib().kvc_score_static(cache.ref, _p(q_recent), n_r, _p(qbuf), _p(count), qmax, _i32(n_b, "n_b"), int(t),
                                   float(rope_theta), _p(scores), _p(beacon_picks), _opts_ref(o), _stream(stream)))
 
 
@@ -283,8 +291,8 @@ def kvc_select(scores: torch.Tensor, prefix: int, recent: int, kept_idx: torch.T
                budget: Optional[torch.Tensor] = None, budget_all: int = 0, status: Optional[torch.Tensor] = None,
                stream=None):
     L, B, Hkv, N = scores.shape
-    _check(lib().kvc_select(_p(scores), L, B, Hkv, N, prefix, recent, _p(budget), int(budget_all), _p(kept_idx),
-                            _p(kept_len), _p(status), _stream(stream)))
+    _check(lib().kvc_select(_p(scores), L, B, Hkv, N, _i32(prefix, "prefix"), _i32(recent, "recent"), _p(budget),
+                            _i32(int(budget_all), "budget_all"), _p(kept_idx), _p(kept_len), _p(status), _stream(stream)))
 
 
 def kvc_compact(cache: Cache, kept_idx: torch.Tensor, kept_len: torch.Tensor, status: Optional[torch.Tensor] = None,
@@ -303,8 +311,9 @@ def kvc_evict(cache: Cache, q_recent: torch.Tensor, qbuf: torch.Tensor, count: t
     n_r, qmax = q_recent.shape[-2], qbuf.shape[-2]
     ws = _workspace(kvc_evict_workspace_size(cache, n_r, n_b), kept_len.device, workspace)
     o = make_opts(row_agg, group_agg, head_budget, entropy, kernel)
-    _check(lib().kvc_evict(cache.ref, _p(q_recent), n_r, _p(qbuf), _p(count), qmax, n_b, int(t), float(rope_theta),
-                           prefix, recent, _p(budget), int(budget_all), _p(kept_idx), _p(kept_len), _p(scores),
+    _check(lib().kvc_evict(cache.ref, _p(q_recent), n_r, _p(qbuf), _p(count), qmax, _i32(n_b, "n_b"), int(t),
+                           float(rope_theta), _i32(prefix, "prefix"), _i32(recent, "recent"), _p(budget),
+                           _i32(int(budget_all), "budget_all"), _p(kept_idx), _p(kept_len), _p(scores),
                            _p(status), _opts_ref(o), _p(ws), ws.numel() * ws.element_size(), _stream(stream)))
 
 
@@ -313,12 +322,14 @@ def kvc_head_budget(entropy: torch.Tensor, N: int, prefix: int, recent: int, bud
                     stream=None):
     """Each (layer, sequence)'s budgets reallocated over its heads by entropy (see kvc.h)."""
     L, B, Hkv = entropy.shape
-    _check(lib().kvc_head_budget(_p(entropy), L, B, Hkv, int(N), int(prefix), int(recent), _p(budget),
-                                 int(budget_all), _p(budget_out), _p(status), _stream(stream)))
+    _check(lib().kvc_head_budget(_p(entropy), L, B, Hkv, _i32(int(N), "N"), _i32(int(prefix), "prefix"),
+                                 _i32(int(recent), "recent"), _p(budget),
+                                 _i32(int(budget_all), "budget_all"), _p(budget_out), _p(status),
+                                 _stream(stream)))
 
 
 def kvc_epikv_workspace_size(B: int, N: int) -> int:
-    return int(lib().kvc_epikv_workspace_size(B, N))
+    return int(lib().kvc_epikv_workspace_size(_i32(B, "B"), _i32(N, "N")))
 
 
 def kvc_epikv_score(hA: torch.Tensor, hB: torch.Tensor, window: int, eps: float, scores: torch.Tensor,
@@ -329,7 +340,7 @@ def kvc_epikv_score(hA: torch.Tensor, hB: torch.Tensor, window: int, eps: float,
     if tuple(hB.shape) != (B, N, dm) or hB.dtype != hA.dtype:
         raise ValueError("hA and hB must be [B, N, dm] tensors of one dtype")
     ws = _workspace(kvc_epikv_workspace_size(B, N), hA.device, workspace)
-    _check(lib().kvc_epikv_score(_dtype_code(hA), B, N, dm, _p(hA), _p(hB), int(window), float(eps), _p(g),
+    _check(lib().kvc_epikv_score(_dtype_code(hA), B, N, dm, _p(hA), _p(hB), _i32(int(window), "window"), float(eps), _p(g),
                                  _p(scores), _p(ws), ws.numel() * ws.element_size(), _stream(stream)))
 
 
@@ -340,8 +351,9 @@ def kvc_epikv_evict(cache: Cache, hA: torch.Tensor, hB: torch.Tensor, window: in
     """Eviction by the EPIKV score: one kept list per sequence compacts all its layers and heads."""
     B, N, dm = hA.shape
     ws = _workspace(kvc_epikv_workspace_size(B, N), hA.device, workspace)
-    _check(lib().kvc_epikv_evict(cache.ref, _p(hA), _p(hB), dm, int(window), float(eps), int(prefix), int(recent),
-                                 _p(budget), int(budget_all), _p(kept_idx), _p(kept_len), _p(scores), _p(status),
+    _check(lib().kvc_epikv_evict(cache.ref, _p(hA), _p(hB), dm, _i32(int(window), "window"), float(eps),
+                                 _i32(int(prefix), "prefix"), _i32(int(recent), "recent"), _p(budget),
+                                 _i32(int(budget_all), "budget_all"), _p(kept_idx), _p(kept_len), _p(scores), _p(status),
                                  _p(ws), ws.numel() * ws.element_size(), _stream(stream)))
 
 
@@ -349,7 +361,7 @@ def kvc_epikv_evict(cache: Cache, hA: torch.Tensor, hB: torch.Tensor, window: in
 # the paged 4-bit cache
 # ---------------------------------------------------------------------------------------------
 def kvc_page_bytes(D: int, page: int) -> int:
-    return int(lib().kvc_page_bytes(D, page))
+    return int(lib().kvc_page_bytes(_i32(D, "D"), _i32(page, "page")))
 
 
 def _ints(t: Optional[torch.Tensor], shape, dev, what: str, dtype=torch.int32):
@@ -450,7 +462,7 @@ def kvc_page_workspace_size(pool: Pool, pages: Pages) -> int:
 
 
 def kvc_page_attend_workspace_size(pool: Pool, pages: Pages, Hq: int, T: int) -> int:
-    return int(lib().kvc_page_attend_workspace_size(pool.ref, pages.ref, Hq, T))
+    return int(lib().kvc_page_attend_workspace_size(pool.ref, pages.ref, _i32(Hq, "Hq"), _i32(T, "T")))
 
 
 def kvc_page_init(pool: Pool, pages: Optional[Pages] = None, stream=None):
@@ -466,8 +478,8 @@ def kvc_page_extend(pool: Pool, pages: Pages, add: Optional[torch.Tensor] = None
     dev = pool.device
     wp, wb, ws = _page_ws(lambda: kvc_page_workspace_size(pool, pages), pool, workspace, stream)
     _page_call("kvc_page_extend", pool, pages, stream,
-               (_ints(add, (pages.shape[1],), dev, "add"), int(add_all), _ints(start, pages.shape, dev, "start"),
-                _word(status, pool), wp, wb))
+               (_ints(add, (pages.shape[1],), dev, "add"), _i32(int(add_all), "add_all"),
+                _ints(start, pages.shape, dev, "start"), _word(status, pool), wp, wb))
 
 
 def kvc_page_free(pool: Pool, pages: Pages, drop: Optional[torch.Tensor] = None, drop_all: int = 0,
@@ -475,7 +487,8 @@ def kvc_page_free(pool: Pool, pages: Pages, drop: Optional[torch.Tensor] = None,
     """The last ``drop`` [B] (or ``drop_all``) tokens of every stream go, with the pages they leave empty."""
     wp, wb, ws = _page_ws(lambda: kvc_page_workspace_size(pool, pages), pool, workspace, stream)
     _page_call("kvc_page_free", pool, pages, stream,
-               (_ints(drop, (pages.shape[1],), pool.device, "drop"), int(drop_all), _word(status, pool), wp, wb))
+               (_ints(drop, (pages.shape[1],), pool.device, "drop"), _i32(int(drop_all), "drop_all"), _word(status, pool),
+                wp, wb))
 
 
 def kvc_page_fork(pool: Pool, pages: Pages, parent: torch.Tensor, out: Pages, status: Optional[torch.Tensor] = None,
@@ -546,8 +559,8 @@ def kvc_page_read(pool: Pool, pages: Pages, k: Optional[torch.Tensor] = None, v:
         raise ValueError("k and v must be [L, B, Hkv, ncap, D] tensors")
     ncap = shape[3]
     _page_call("kvc_page_read", pool, pages, stream,
-               (_dtype_code(x), _ints(first, pages.shape, pool.device, "first"), int(first_all),
-                ncap if count is None else int(count), _ints(k, shape, pool.device, "k", x.dtype),
+               (_dtype_code(x), _ints(first, pages.shape, pool.device, "first"), _i32(int(first_all), "first_all"),
+                ncap if count is None else _i32(int(count), "count"), _ints(k, shape, pool.device, "k", x.dtype),
                 _ints(v, shape, pool.device, "v", x.dtype), ncap, _word(status, pool)))
 
 
@@ -602,7 +615,7 @@ def kvc_tree_mask(parent: torch.Tensor, mask: torch.Tensor, depth: Optional[torc
     its ancestors (the nearest ``window`` of them, 0: all) and its ``depth`` [B, T]; once a step, for all layers."""
     B, T, dev = _tree(parent)
     _tree_call("kvc_tree_mask", parent, stream,
-               (_ints(n_q, (B,), dev, "n_q"), int(window), _ints(mask, (B, T, (T + 31) // 32), dev, "mask"),
+               (_ints(n_q, (B,), dev, "n_q"), _i32(int(window), "window"), _ints(mask, (B, T, (T + 31) // 32), dev, "mask"),
                 _ints(depth, (B, T), dev, "depth"), _ints(status, (1,), dev, "status")))
 
 
@@ -620,7 +633,8 @@ def kvc_tree_verify(parent: torch.Tensor, draft: torch.Tensor, target: torch.Ten
 
 def kvc_page_attend_masked_workspace_size(pool: Pool, pages: Pages, Hq: int, T: int, window: int = 0,
                                           sinks: int = 0) -> int:
-    return int(lib().kvc_page_attend_masked_workspace_size(pool.ref, pages.ref, Hq, T, window, sinks))
+    return int(lib().kvc_page_attend_masked_workspace_size(pool.ref, pages.ref, _i32(Hq, "Hq"), _i32(T, "T"),
+                                                           _i32(window, "window"), _i32(sinks, "sinks")))
 
 
 def kvc_page_attend_masked(pool: Pool, pages: Pages, q: torch.Tensor, out: torch.Tensor, window: int = 0, sinks: int = 0,
@@ -641,8 +655,8 @@ def kvc_page_attend_masked(pool: Pool, pages: Pages, q: torch.Tensor, out: torch
     wp, wb, ws = _page_ws(lambda: kvc_page_attend_masked_workspace_size(pool, pages, Hq, T, window, sinks), pool,
                           workspace, stream)
     _page_call("kvc_page_attend_masked", pool, pages, stream,
-               (_dtype_code(q), Hq, T, qp, qs, _ints(n_q, (B,), dev, "n_q"), int(window), int(sinks),
-                _ints(mask, (B, T, (T + 31) // 32), dev, "mask"), _ints(depth, (B, T), dev, "depth"),
+               (_dtype_code(q), Hq, T, qp, qs, _ints(n_q, (B,), dev, "n_q"), _i32(int(window), "window"),
+                _i32(int(sinks), "sinks"), _ints(mask, (B, T, (T + 31) // 32), dev, "mask"), _ints(depth, (B, T), dev, "depth"),
                 float(D ** -0.5 if scale is None else scale), _ints(out, shape, dev, "out", q.dtype),
                 _ints(lse, (B, T, Hq), dev, "lse", torch.float32), _word(status, pool), wp, wb))
 
@@ -653,7 +667,8 @@ def kvc_page_slide(pool: Pool, pages: Pages, window: int, sinks: int = 0, gone: 
     [L, B, Hkv] receives the tokens that went."""
     wp, wb, ws = _page_ws(lambda: kvc_page_workspace_size(pool, pages), pool, workspace, stream)
     _page_call("kvc_page_slide", pool, pages, stream,
-               (int(window), int(sinks), _ints(gone, pages.shape, pool.device, "gone"), _word(status, pool), wp, wb))
+               (_i32(int(window), "window"), _i32(int(sinks), "sinks"), _ints(gone, pages.shape, pool.device, "gone"),
+                _word(status, pool), wp, wb))
 
 
 def kvc_page_accept(pool: Pool, pages: Pages, path: torch.Tensor, n_path: torch.Tensor,
