@@ -10,6 +10,8 @@ namespace {
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 bool at16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool at4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+template <typename... P>
+bool all4(P... p) { return (at4(p) && ...); }
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + nb && y < x + na;
@@ -111,7 +113,7 @@ int check_attend(const kvc_pool* pool, const kvc_pages* pages, int32_t dtype, in
   a->T = T;
   if (!attend_fits(*a)) return KVC_ERR_TOO_LARGE;
   if ((rc = check_rows(q, q_strides, es, &a->qs))) return rc;
-  if (!at16(out) || !at4(lse)) return KVC_ERR_ALIGNMENT;
+  if (!at16(out) || !all4(lse, n_q, status)) return KVC_ERR_ALIGNMENT;
   a->q = q;
   a->out = out;
   a->lse = lse;
@@ -131,10 +133,10 @@ SeenArgs seen_args(int32_t window, int32_t sinks, const uint32_t* mask, const in
                   (T + 31) / 32};
 }
 
-int check_tree(int32_t B, int32_t T, const int32_t* parent) {
+int check_tree(int32_t B, int32_t T, const int32_t* parent, const int32_t* status) {
   if (B < 1 || T < 1 || !parent) return KVC_ERR_INVALID_ARG;
   if (T > KVC_TREE_MAX || B > (1 << 20)) return KVC_ERR_TOO_LARGE;
-  return at4(parent) ? KVC_OK : KVC_ERR_ALIGNMENT;
+  return all4(parent, status) ? KVC_OK : KVC_ERR_ALIGNMENT;
 }
 
 }  // namespace
@@ -173,6 +175,7 @@ int kvc_page_extend(const kvc_pool* pool, const kvc_pages* pages, const int32_t*
   int rc = check_pool(pool, &g);
   if (rc || (rc = check_pages(pages, g.lp, &t))) return rc;
   if (!add && add_all < 0) return KVC_ERR_INVALID_ARG;
+  if (!all4(add, start, status)) return KVC_ERR_ALIGNMENT;
   if ((rc = check_ws(g, t, workspace, ws_bytes, &w))) return rc;
   return launch_page_extend(g, t, add, add_all, start, status, w, static_cast<cudaStream_t>(stream));
 }
@@ -185,6 +188,7 @@ int kvc_page_free(const kvc_pool* pool, const kvc_pages* pages, const int32_t* d
   int rc = check_pool(pool, &g);
   if (rc || (rc = check_pages(pages, g.lp, &t))) return rc;
   if (!drop && drop_all < 0) return KVC_ERR_INVALID_ARG;
+  if (!all4(drop, status)) return KVC_ERR_ALIGNMENT;
   if ((rc = check_ws(g, t, workspace, ws_bytes, &w))) return rc;
   return launch_page_free(g, t, drop, drop_all, status, w, static_cast<cudaStream_t>(stream));
 }
@@ -201,6 +205,7 @@ int kvc_page_fork(const kvc_pool* pool, const kvc_pages* pages, const int32_t* p
   if (overlap(t.table, nt, o.table, no) || overlap(t.len, lt, o.len, lo) || overlap(t.table, nt, o.len, lo) ||
       overlap(t.len, lt, o.table, no) || overlap(o.table, no, o.len, lo))
     return KVC_ERR_INVALID_ARG;
+  if (!all4(parent, status)) return KVC_ERR_ALIGNMENT;
   if ((rc = check_ws(g, t, workspace, ws_bytes, &w))) return rc;
   return launch_page_fork(g, t, parent, o, status, w, static_cast<cudaStream_t>(stream));
 }
@@ -214,6 +219,7 @@ int kvc_page_compact(const kvc_pool* pool, const kvc_pages* pages, const int32_t
   int rc = check_pool(pool, &g);
   if (rc || (rc = check_pages(pages, g.lp, &t))) return rc;
   if (!kept_idx || !kept_len || kept_stride < 1 || (list_per_seq != 0 && list_per_seq != 1)) return KVC_ERR_INVALID_ARG;
+  if (!all4(kept_idx, kept_len, status)) return KVC_ERR_ALIGNMENT;
   if ((rc = check_ws(g, t, workspace, ws_bytes, &w))) return rc;
   return launch_page_compact(g, t, kept_idx, kept_len, kept_stride, list_per_seq, status, w,
                              static_cast<cudaStream_t>(stream));
@@ -229,6 +235,7 @@ int kvc_page_store(const kvc_pool* pool, const kvc_pages* pages, int32_t dtype, 
   if (!es) return KVC_ERR_UNSUPPORTED_DTYPE;
   if (a.t.L != 1 || T < 1 || !start) return KVC_ERR_INVALID_ARG;
   if ((rc = check_rows(k, k_strides, es, &a.xs[0])) || (rc = check_rows(v, v_strides, es, &a.xs[1]))) return rc;
+  if (!all4(n, start, status)) return KVC_ERR_ALIGNMENT;
   a.x[0] = k;
   a.x[1] = v;
   a.T = T;
@@ -248,7 +255,7 @@ int kvc_page_read(const kvc_pool* pool, const kvc_pages* pages, int32_t dtype, c
   if (rc || (rc = check_pages(pages, a.g.lp, &a.t))) return rc;
   if (!elem_size(dtype)) return KVC_ERR_UNSUPPORTED_DTYPE;
   if ((!k && !v) || count < 1 || ncap < count || (!first && first_all < 0)) return KVC_ERR_INVALID_ARG;
-  if (!at16(k) || !at16(v)) return KVC_ERR_ALIGNMENT;
+  if (!at16(k) || !at16(v) || !all4(first, status)) return KVC_ERR_ALIGNMENT;
   a.out[0] = k;
   a.out[1] = v;
   a.first = first;
@@ -299,7 +306,7 @@ int kvc_page_attend_masked(const kvc_pool* pool, const kvc_pages* pages, int32_t
   if (rc) return rc;
   if (window < 0 || sinks < 0 || (depth && !mask)) return KVC_ERR_INVALID_ARG;
   if (mask && T > KVC_TREE_MAX) return KVC_ERR_TOO_LARGE;
-  if (!at4(mask) || !at4(depth)) return KVC_ERR_ALIGNMENT;
+  if (!all4(mask, depth)) return KVC_ERR_ALIGNMENT;
   const SeenArgs m = seen_args(window, sinks, mask, depth, T);
   if (!ws_fits(workspace, ws_bytes, attend_masked_ws_bytes(a.g, a.t, Hq, T, m))) return KVC_ERR_WORKSPACE;
   a.ws = workspace;
@@ -314,7 +321,7 @@ int kvc_page_slide(const kvc_pool* pool, const kvc_pages* pages, int32_t window,
   int rc = check_pool(pool, &g);
   if (rc || (rc = check_pages(pages, g.lp, &t))) return rc;
   if (window < 1 || sinks < 0) return KVC_ERR_INVALID_ARG;
-  if (!at4(gone)) return KVC_ERR_ALIGNMENT;
+  if (!all4(gone, status)) return KVC_ERR_ALIGNMENT;
   if ((rc = check_ws(g, t, workspace, ws_bytes, &w))) return rc;
   return launch_page_slide(g, t, window, sinks < kSeenAll ? sinks : kSeenAll, gone, status, w,
                            static_cast<cudaStream_t>(stream));
@@ -329,26 +336,26 @@ int kvc_page_accept(const kvc_pool* pool, const kvc_pages* pages, int32_t T, con
   if (rc || (rc = check_pages(pages, g.lp, &t))) return rc;
   if (T < 1 || !path || !n_path) return KVC_ERR_INVALID_ARG;
   if (T > KVC_TREE_MAX) return KVC_ERR_TOO_LARGE;
-  if (!at4(path) || !at4(n_path) || !at4(n_q)) return KVC_ERR_ALIGNMENT;
+  if (!all4(path, n_path, n_q, status)) return KVC_ERR_ALIGNMENT;
   if ((rc = check_ws(g, t, workspace, ws_bytes, &w))) return rc;
   return launch_page_accept(g, t, T, path, n_path, n_q, status, w, static_cast<cudaStream_t>(stream));
 }
 
 int kvc_tree_mask(int32_t B, int32_t T, const int32_t* parent, const int32_t* n_q, int32_t window, uint32_t* mask,
                   int32_t* depth, int32_t* status, void* stream) {
-  const int rc = check_tree(B, T, parent);
+  const int rc = check_tree(B, T, parent, status);
   if (rc) return rc;
   if (window < 0 || !mask) return KVC_ERR_INVALID_ARG;
-  if (!at4(n_q) || !at4(mask) || !at4(depth)) return KVC_ERR_ALIGNMENT;
+  if (!all4(n_q, mask, depth)) return KVC_ERR_ALIGNMENT;
   return launch_tree_mask(B, T, parent, n_q, window, mask, depth, status, static_cast<cudaStream_t>(stream));
 }
 
 int kvc_tree_verify(int32_t B, int32_t T, const int32_t* parent, const int32_t* draft, const int32_t* target,
                     const int32_t* n_q, int32_t* path, int32_t* n_path, int32_t* next, int32_t* status, void* stream) {
-  const int rc = check_tree(B, T, parent);
+  const int rc = check_tree(B, T, parent, status);
   if (rc) return rc;
   if (!draft || !target || !path || !n_path) return KVC_ERR_INVALID_ARG;
-  if (!at4(draft) || !at4(target) || !at4(n_q) || !at4(path) || !at4(n_path) || !at4(next)) return KVC_ERR_ALIGNMENT;
+  if (!all4(draft, target, n_q, path, n_path, next)) return KVC_ERR_ALIGNMENT;
   return launch_tree_verify(B, T, parent, draft, target, n_q, path, n_path, next, status,
                             static_cast<cudaStream_t>(stream));
 }

@@ -64,7 +64,7 @@ enum {
   KVC_ERR_NOT_DIVISIBLE = -5,        /* Hq % Hkv != 0, or an odd FPS buffer size */
   KVC_ERR_LAUNCH = -6,               /* a CUDA launch or attribute call failed */
   KVC_ERR_WORKSPACE = -7,            /* workspace missing or smaller than *_workspace_size() */
-  KVC_ERR_ALIGNMENT = -8,            /* a device pointer is not 16-byte aligned */
+  KVC_ERR_ALIGNMENT = -8,            /* a device pointer is not 16-byte aligned (the paged cache's int32 and float arrays: 4) */
   KVC_ERR_TOO_LARGE = -9             /* a size exceeds what the kernels index with 32 bits */
 };
 
