@@ -182,3 +182,35 @@ def test_captured_and_replayed_with_new_lengths():
         o, l = check(x, mask=mask, depth=depth)
         assert torch.equal(o, out) and torch.equal(l, lse) and int(status.item()) == 0
         kvc.kvc_page_attend_masked(x.pool, x.pages, q, torch.empty_like(q), window=50, sinks=2, status=status, workspace=ws)
+
+
+@pytest.mark.parametrize("D,G,T,B,n", [(128, 4, 5, 75, 128), (64, 2, 60, 75, 250), (128, 4, 50, 75, 250)])
+def test_a_wait_that_runs_out_among_many_streams(D, G, T, B, n):
+    """The first CTA, with several streams of a unit or two, waits for an arrival that nothing makes: the call ends and says so, the
+    other CTAs' streams keep their results, nothing of a workspace's former contents comes in, the next call is right."""
+    kvc = kvc_()
+    rng = np.random.default_rng(T)
+    x = Made("bf16", D, B, 8, G, T, 64, rng.integers(n // 2, n + 1, B * 8), T)
+    uneven(x.q, rng)
+    ws = torch.empty(kvc.kvc_page_attend_masked_workspace_size(x.pool, x.pages, 8 * G, T, 40, 3), dtype=torch.uint8, device=DEV)
+    res = []
+    for mode, fill in ((0, 0x00), (2, 0x00), (2, 0xff), (0, 0xff)):
+        ws.fill_(fill)
+        out, lse = torch.full_like(x.q, 9.0), torch.full(x.q.shape[:3], 9.0, device=DEV)
+        status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        torch.cuda.synchronize()
+        kvc.kvc_debug_fault(mode)
+        try:
+            kvc.kvc_page_attend_masked(x.pool, x.pages, x.q, out, window=40, sinks=3, lse=lse, status=status, workspace=ws)
+            torch.cuda.synchronize()
+        finally:
+            kvc.kvc_debug_fault(0)
+        assert int(status.item()) == (kvc.KVC_STATUS_TIMEOUT if mode else 0)
+        res.append((out, lse))
+    (o0, l0), *late, (o3, l3) = res
+    assert torch.equal(o0, o3) and torch.equal(l0, l3)
+    for o, l in late:
+        assert torch.equal(o[2:], o0[2:]) and torch.equal(l[2:], l0[2:])  # a CTA has fewer than 16 streams
+        assert not torch.equal(l[:2], l0[:2])
+    assert torch.equal(late[0][0], late[1][0]) and torch.equal(late[0][1], late[1][1])
+    check(x, window=40, sinks=3)
