@@ -711,7 +711,8 @@ __global__ void __launch_bounds__(kCombThreads) combine_kernel(AttendArgs a, Att
   if (a.lse && lane == 0) a.lse[at] = r.l == 0.f ? -INFINITY : (r.m + log2f(r.l)) * 0.6931471805599453f;
 }
 
-// The tcgen05 kernel's parts lie with the rows contiguous: a thread a row, 16 channels a CTA.
+// The tcgen05 kernels' parts lie with the rows contiguous, under SeenArgs eight channels of a row together (part_at): a
+// thread a row, 16 channels a CTA.
 template <typename T, int D, int ROWS, typename M>
 __global__ void __launch_bounds__(ROWS) combine_tc_kernel(AttendArgs a, AttendPlan p, M seen) {
   griddep_launch();
@@ -771,7 +772,10 @@ __global__ void __launch_bounds__(ROWS) combine_tc_kernel(AttendArgs a, AttendPl
 
 // Row tiles of 8 a block takes: one covers the decode step of up to 8 query heads per KV head; more rows
 // share the decoding of a chunk. From kTcMin rows on bf16 queries go to the tcgen05 kernel (32 streams of 8192
-// tokens: 16 rows 24.4 us here and 36.6 there, 24 rows 39.2 and 37.3 with four tiles a block here).
+// tokens: 16 rows 24.4 us here and 36.6 there, 24 rows 39.2 and 37.3 with four tiles a block here). Under SeenArgs (blocks of
+// 16 rows here, by clusters or split, in brackets): 16 x 8 heads, 24 rows, window 1000 24.5 us (29.4), 4000 45.2 (52.6); 64 x 8,
+// 24 rows, 2000 88 (115); 8 x 8, 48 rows, 1000 20.0 (22.4). Few streams would do better in blocks of 16, which this rule does not
+// know: 1 x 8 heads, 24 rows, window 1000 13.5 (9.7), 64 rows 14.4 (12.2); 8 x 8, 32 rows, 1000 19.7 (17.5), but 4000 28.7 (32.7).
 constexpr int kTcMin = 17;
 // What beginning a stream's part costs, in units (query rows read, the ring or pipeline filled, results merged):
 // counted when the work is split, so that a CTA with two parts gets less (64 new tokens over 4 x 8192: 46.7 us

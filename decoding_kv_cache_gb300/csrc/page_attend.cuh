@@ -23,7 +23,7 @@ struct AttendPlan {
   int grid;    // CTAs of the main kernel
   int whole;   // a CTA takes a whole stream: no parts, no second kernel
   int ctas;    // under SeenArgs, whole: a cluster of so many CTAs does
-  float* part;  // [grid][2][rb][D] (tcgen05 kernel: [grid][2][D][rb])
+  float* part;  // [grid][2][rb][D] (tcgen05 kernels: [grid][2][D][rb], under SeenArgs in part_at's order)
   float2* ml;   // [grid][2][rb] (reference, sum)
   int2* span;   // [nvs] first and last CTA of a stream's units (streams with units only; negative: that CTA gave up)
 };

@@ -43,6 +43,14 @@ struct Lay {
   static constexpr int bytes = oRaw + kRaw * kRawBytes + 1024;
 };
 
+// Why no wait for a phase's parity can find its barrier two phases off, parts of one unit included (tests/barrier_model.py):
+//   raw_*, k_*, v_*  a stage is filled again only when all who wait for it have given it back, in the order of the units
+//   s_full, p_full   the next S of a buffer is issued behind P V of the unit in it, so after the waiting softmax warps' P, and
+//                    the next P there needs an S that the waiting issuer issues
+//   pv_done          by the softmax within a part, for the unit before the one in hand, whose Q K was issued behind the P V of
+//                    the unit before that: its commit covers both
+//   part_done        once a part, by every warp of the group
+//   q_full, merge    the softmax warps stage a part's queries when all of them have met at the end of the part before
 struct Bars {
   uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[kTiles], k_empty[kTiles], v_full[kTiles], v_empty[kTiles];
   uint64_t s_full[2], p_full[2][2], pv_done[2], part_done[2];  // p_full: S buffer, group (a group may be a unit ahead)

@@ -615,8 +615,10 @@ __device__ __forceinline__ void slide_streams(const PoolGeom& g, const PageTab& 
   }
 }
 
-// Streams a warp has in the wide form; up to kSlideOne a cluster has all (36 x 8 x 8 streams that grow by a token with room
-// for it: 13 us against 18 called from Python, 12 against 10 in a graph)
+// Streams a warp has in the wide form; up to kSlideOne streams a cluster has all. That is chosen by what a step's call costs the
+// host: 36 x 8 x 8 streams called from Python 5.6 us and 8.5, with kvc_page_extend before 13 and 18. By the device's time alone
+// (in a graph; the wide form in brackets) it holds up to some 768 streams, 5.4 us (6.8); 2304 take 5.9 (4.0), and where each gives
+// up many pages at once, as behind a prompt, 768 streams 12.8 (14.2) with 16 pages, 18.8 (14.3) with 64, 2304 32 (16) with 64.
 constexpr int kSlideStreams = 4, kSlideOne = 4096;
 __global__ void __launch_bounds__(256) slide_kernel(PoolGeom g, PageTab t, int window, int first, int32_t* gone,
                                                    int32_t* status, PageWs w) {
