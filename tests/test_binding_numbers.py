@@ -52,7 +52,7 @@ def test_numbers_beyond_32_bits(kvc, n):
             call()
 
 
-def test_numbers_at_the_ends_are_the_library_s_to_judge(kvc):
+def test_numbers_at_the_ends_are_checked_by_the_library(kvc):
     pool, pages, _ = handles(kvc)
     size = kvc.kvc_page_attend_masked_workspace_size
     assert size(pool, pages, 4, 1, (1 << 31) - 1, (1 << 31) - 1) == size(pool, pages, 4, 1) > 0

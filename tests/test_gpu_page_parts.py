@@ -214,3 +214,21 @@ def test_a_wait_that_runs_out_among_many_streams(D, G, T, B, n):
         assert not torch.equal(l[:2], l0[:2])
     assert torch.equal(late[0][0], late[1][0]) and torch.equal(late[0][1], late[1][1])
     check(x, window=40, sinks=3)
+
+
+@pytest.mark.parametrize("dt,D,G,T,B,n,w", [("bf16", 128, 4, 1, 300, 200, 3500), ("bf16", 64, 2, 8, 250, 130, 3000), ("f32", 128, 4, 2, 160, 150, 2500),
+                                            ("f32", 64, 4, 4, 120, 300, 4000), ("f32", 64, 2, 30, 40, 200, 2500)])
+def test_few_rows_of_many_short_streams(dt, D, G, T, B, n, w):
+    """Blocks of 8 and 16 rows, tables for many more tokens than the streams have: the streams' units are split over all CTAs,
+    several whole streams each."""
+    rng = np.random.default_rng(B + T)
+    lens = rng.integers(1, n + 1, B * 8)
+    lens[3::40] = 0
+    x = Made(dt, D, B, 8, G, T, 64, lens, B, maxp=70)
+    uneven(x.q, rng)
+    n_q = rng.integers(0, T + 1, B)
+    mask, depth, _ = Q.tree_mask(Q.random_trees(rng, B, T))
+    check(x, mask=mask, depth=depth, n_q=n_q)
+    check(x, window=w, sinks=2)
+    check(x, window=w, sinks=0, mask=mask, depth=depth)
+    check(x, causal=True, n_q=n_q)
